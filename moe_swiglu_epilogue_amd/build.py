@@ -13,6 +13,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "moe_nvfp4.hip")
 GEMM_SRC = os.path.join(HERE, "csrc", "moe_gemm.hip")
+# the operators of a decoding step (include/nvfp4_serving.h), in the same library
+SERVING_SRCS = [os.path.join(HERE, "csrc", f)
+                for f in ("kv_tables.hip", "paged_attention.hip", "moe_layer.hip")]
 LIB = os.path.join(HERE, "libmoe_nvfp4.so")
 CALIB_SRC = os.path.join(HERE, "csrc", "calib.hip")
 CALIB_LIB = os.path.join(HERE, "libnvfp4_calib.so")
@@ -37,7 +40,7 @@ def build(verbose: bool = False) -> str:
     """Build the three libraries; return the path of libmoe_nvfp4.so."""
     _build_one([CALIB_SRC], CALIB_LIB, verbose)
     _build_one([DIVCHECK_SRC], DIVCHECK_LIB, verbose)
-    return _build_one([SRC, GEMM_SRC], LIB, verbose)
+    return _build_one([SRC, GEMM_SRC, *SERVING_SRCS], LIB, verbose)
 
 
 def _build_one(srcs, lib: str, verbose: bool) -> str:
