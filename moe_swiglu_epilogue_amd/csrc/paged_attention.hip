@@ -1,13 +1,23 @@
 // Attention over the paged NVFP4 cache (include/nvfp4_serving.h).
 //
-// The simplest form: one wave per (query row, head). Each lane owns head_dim /
-// 64 consecutive dimensions of the row; the keys are walked one by one, their
-// scores summed over the wave, with the running maximum and sum of the
-// softmax in FP32.
+// An E2M1 code times an E4M3 scale has at most 6 significant bits and lies in
+// [2^-10, 2688], so every cache value is exact in FP16. Both products run on
+// the FP16 matrix cores with FP32 sums, on values converted in registers: two
+// codes a conversion (v_cvt_scalef32_pk_f16_fp4), then one packed FP16
+// product with the block's scale. Global scales are folded into the softmax
+// scale and the output.
 #include "serving_common.hpp"
-#include "nvfp4_device.hpp"
 
 namespace {
+
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
 
 struct Attn {
     const uint16_t* q;
@@ -16,69 +26,614 @@ struct Attn {
     const float *k_gs, *v_gs;
     uint16_t* out;
     float* lse;
+    float* part;       // workspace: [splits][tokens * heads][D], then [splits][tokens * heads] pairs (m, l)
     int64_t ld_q, ld_out, ld_table, window;
     int tokens, heads, kv_heads, page, num_pages, max_pages, num_seqs, causal;
     float scale;
+    uint32_t page_magic, page_shift;   // t / page == t * magic >> shift for 0 <= t < 2^31
+    int splits, chunk, row_blocks;
 };
 
-__device__ __forceinline__ float e2m1(uint32_t c)
+// What the rows of one block of a request see, and how a long range of tokens
+// is cut into splits. The same for the kernel that computes a split and the
+// one that joins them.
+struct Span {
+    int first, rows, len;      // first row of q, query rows (tokens x group), cached tokens
+    int begin, end, chunk;     // tokens that some row of the block sees (begin: a multiple of 32)
+    int all_begin, all_end;    // tokens that every row of the block sees
+};
+
+__device__ __forceinline__ Span request_span(const Attn& a, int b, int group)
 {
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-    return c & 8u ? -v : v;
+    Span s;
+    s.first = min(max(a.offsets[b], 0), a.tokens);
+    s.rows = (min(max(a.offsets[b + 1], s.first), a.tokens) - s.first) * group;
+    s.len = a.num_pages > 0 ? min(max(a.lens[b], 0), a.max_pages * a.page) : 0;
+    return s;
+}
+
+// The tokens [lo, hi) that query `i` of `n` sees.
+__device__ __forceinline__ void sees(const Attn& a, int len, int n, int i, int& lo, int& hi)
+{
+    const int pos = len - n + i;
+    hi = a.causal ? min(pos + 1, len) : len;
+    lo = a.window > 0 ? (int)max((int64_t)pos - a.window + 1, (int64_t)0) : 0;
+}
+
+__device__ __forceinline__ void block_span(const Attn& a, Span& s, int group, int row0, int block)
+{
+    const int n = s.rows / group;
+    int lo0, hi0, lo1, hi1;
+    sees(a, s.len, n, row0 / group, lo0, hi0);
+    sees(a, s.len, n, min(row0 + block, s.rows) / group - (min(row0 + block, s.rows) % group == 0),
+         lo1, hi1);
+    s.begin = lo0 & ~31;
+    s.end = max(hi1, s.begin);
+    s.all_begin = lo1;
+    s.all_end = hi0;
+    // splits of a.chunk tokens, of more where the range is longer than promised
+    const int total = s.end - s.begin;
+    s.chunk = max(a.chunk, ((total + a.splits - 1) / a.splits + 127) & ~127);
+}
+
+__device__ __forceinline__ uint32_t page_of(const Attn& a, uint32_t t)
+{
+    return (uint32_t)(((uint64_t)t * a.page_magic) >> a.page_shift);
+}
+
+__device__ __forceinline__ half2v fp4x2(uint32_t w, int byte)
+{
+    switch (byte) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+    }
+}
+
+// The two E4M3 values in the low bytes of w.
+__device__ __forceinline__ half2v e4m3x2(uint32_t w)
+{
+    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+}
+
+__device__ __forceinline__ half8v join(half2v a, half2v b, half2v c, half2v d)
+{
+    return half8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Eight codes of one block times its scale.
+__device__ __forceinline__ half8v fp4x8(uint32_t w, _Float16 scale)
+{
+    const half2v s = {scale, scale};
+    return join(fp4x2(w, 0) * s, fp4x2(w, 1) * s, fp4x2(w, 2) * s, fp4x2(w, 3) * s);
+}
+
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)v);
+}
+
+// Largest / sum over the four lanes that hold one query row (lane % 16).
+__device__ __forceinline__ float row_max(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+
+__device__ __forceinline__ float row_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// A query row's values for one matrix operand: BF16 to FP16 with the row's
+// power of two 2^e.
+__device__ __forceinline__ half8v scaled_half8(uint4v w, int e)
+{
+    half8v r;
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = (_Float16)ldexpf(__uint_as_float(w[i] << 16), e);
+        r[2 * i + 1] = (_Float16)ldexpf(__uint_as_float(w[i] & 0xffff0000u), e);
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t largest_bits(uint4v w, uint32_t top)
+{
+    for (int i = 0; i < 4; ++i)
+        top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+    return top;
+}
+
+// Exponent that puts a row whose largest magnitude has these bits into
+// [2^14, 2^15); 0 for a row of zeros.
+__device__ __forceinline__ int row_exponent(uint32_t top)
+{
+    if (top == 0)
+        return 0;
+    return 14 - (ilogbf(__uint_as_float(top)));
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    const bf2 v = {(__bf16)lo, (__bf16)hi};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// ---- few query rows ----------------------------------------------------------
+// One workgroup per (request, block of 16 RT query rows, key/value head,
+// split of the tokens); query rows are tokens x the heads that share the
+// key/value head. Its four waves take tiles of 32 tokens in turn, each with
+// its own running maximum, sum and output, joined through LDS at the end.
+//
+// Scores are computed transposed, S^T = K Q^T (v_mfma_f32_16x16x32_f16): a lane
+// holds one query row (lane % 16) and the tokens 4 (lane / 16) + r of each
+// half tile, which is the layout of the second product's right operand as it
+// stands if that product sums over the tokens in the order (half 0: 4g .. 4g+3,
+// half 1: 4g .. 4g+3) for lane group g. Its left operand V^T needs, per lane,
+// eight tokens of one dimension: a lane loads the same 8 dimensions of its
+// eight tokens and pairs their codes by two nibble merges per token pair; the
+// conversion then picks a byte (a dimension) of each pair. So nothing crosses
+// lanes but the scale bytes.
+//
+// The maximum is kept lazily: a row's exponentials are taken against a maximum
+// that is raised only when a score exceeds it by 2^kSlack or more, which FP16
+// holds without loss; most tiles then need no rescaling and no exchange.
+constexpr float kSlack = 8.0f;
+
+template <int D>
+struct Tile {
+    static constexpr int C = D > 64 ? D / 128 : 1;    // 128-wide chunks
+    static constexpr int KW = D > 64 ? 4 : 2;         // words of a lane's keys per chunk
+    static constexpr int VM = D > 64 ? 8 : 4;         // dimensions of a lane's values per chunk
+    uint32_t k[2][C][KW];
+    uint32_t v[8][C];
+    uint32_t ks[C], vs[C];
+    bool shown;                                       // this lane's token (lane % 32) counts
+    bool hidden0, hidden1;                            // uniform: a whole half is hidden
+};
+
+template <int D, bool kPaged16>
+__device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32_t* table, int h,
+                                          int t0, int begin, int end, int lane)
+{
+    using T = Tile<D>;
+    const int g = lane >> 4, n = lane & 15, tok = lane & 31;
+    const int64_t row = (int64_t)a.kv_heads * (D / 2), srow = (int64_t)a.kv_heads * (D / 16);
+    const uint8_t* kp = a.kp + h * (D / 2);
+    const uint8_t* vp = a.vp + h * (D / 2);
+    const uint8_t* ks = a.ks + h * (D / 16);
+    const uint8_t* vs = a.vs + h * (D / 16);
+    int64_t mine;                 // slot of this lane's token
+    int64_t slot_k[2], slot_v[8];
+    bool shown;
+    if (kPaged16) {
+        // 16 tokens of a half tile stand in one page: one entry a half
+        int64_t base[2];
+        bool hid[2];
+        for (int hh = 0; hh < 2; ++hh) {
+            const int first = t0 + 16 * hh;
+            const int p = (int)page_of(a, first);
+            const int entry = p < a.max_pages && first < end ? table[p] : -1;
+            hid[hh] = entry < 0 || entry >= a.num_pages;
+            base[hh] = hid[hh] ? 0 : (int64_t)entry * a.page + (first - p * a.page);
+        }
+        t.hidden0 = hid[0];
+        t.hidden1 = hid[1];
+        // a hidden half reads the cache's first slots instead (a page holds 16 or more)
+        for (int hh = 0; hh < 2; ++hh)
+            slot_k[hh] = base[hh] + n;
+        for (int j = 0; j < 8; ++j)
+            slot_v[j] = base[j >> 2] + 4 * g + (j & 3);
+        mine = base[tok >> 4] + (tok & 15);
+        shown = !(tok < 16 ? hid[0] : hid[1]);
+    } else {
+        const int at = t0 + tok;
+        const int p = (int)page_of(a, at);
+        const int entry = at < end ? table[p] : -1;
+        shown = entry >= 0 && entry < a.num_pages;
+        const int slot = shown ? entry * a.page + (at - p * a.page) : 0;
+        mine = slot;
+        for (int hh = 0; hh < 2; ++hh)
+            slot_k[hh] = (int)from_lane(slot, n + 16 * hh);
+        for (int j = 0; j < 8; ++j)
+            slot_v[j] = (int)from_lane(slot, 16 * (j >> 2) + 4 * g + (j & 3));
+        t.hidden0 = t.hidden1 = false;
+    }
+    t.shown = shown && t0 + tok >= begin && t0 + tok < end;
+    for (int c = 0; c < T::C; ++c) {
+        for (int hh = 0; hh < 2; ++hh) {
+            if (D > 64) {
+                const uint4v w = *(const uint4v*)(kp + slot_k[hh] * row + 64 * c + 16 * g);
+                for (int i = 0; i < 4; ++i)
+                    t.k[hh][c][i % T::KW] = w[i];
+            } else {
+                const uint2v w = *(const uint2v*)(kp + slot_k[hh] * row + 8 * g);
+                t.k[hh][c][0] = w[0];
+                t.k[hh][c][1] = w[1];
+            }
+        }
+        // scales: a lane takes 4 bytes of its token (the second half of the
+        // wave the next 4), handed to the lanes that need them when used
+        const int64_t at = mine * srow + (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
+        t.ks[c] = *(const uint32_t*)(ks + at);
+        t.vs[c] = *(const uint32_t*)(vs + at);
+        for (int j = 0; j < 8; ++j) {
+            if (D > 64)
+                t.v[j][c] = *(const uint32_t*)(vp + slot_v[j] * row + 64 * c + 4 * n);
+            else
+                t.v[j][c] = *(const uint16_t*)(vp + slot_v[j] * row + 2 * n);
+        }
+    }
+}
+
+template <int D, int RT, bool kPaged16>
+__global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
+{
+    using T = Tile<D>;
+    constexpr int C = T::C, KF = D / 32, VM = T::VM;
+    constexpr int kPad = D + 4;
+    __shared__ float o_lds[4][16][kPad];
+    __shared__ float m_lds[4][16], l_lds[4][16];
+
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = a.heads / a.kv_heads;
+
+    // Workgroups go to the 8 XCDs in turn. All key/value heads of one range of
+    // tokens go to the same XCD one after the other: their rows lie side by
+    // side in memory, 64 bytes of codes and 8 of scales each, and share its L2.
+    const int per_split = a.num_seqs * a.row_blocks;
+    const int j = blockIdx.x >> 3;
+    const int work = (j / a.kv_heads) * 8 + (blockIdx.x & 7);
+    const int h = j % a.kv_heads;
+    if (work >= per_split * a.splits)
+        return;
+    const int split = work / per_split;
+    // requests rotate with the split, so that no XCD gets only first splits
+    const int item = (work % per_split + split) % per_split;
+    const int b = item / a.row_blocks;
+    Span s = request_span(a, b, group);
+    const int32_t* table = a.table + b * a.ld_table;
+    const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
+
+    for (int row0 = (item % a.row_blocks) * 16 * RT; row0 < s.rows;
+         row0 += a.row_blocks * 16 * RT) {
+        block_span(a, s, group, row0, 16 * RT);
+        const int first = s.begin + split * s.chunk;
+        const int last = min(first + s.chunk, s.end);
+        if (first >= last && split > 0)
+            continue;
+
+        // the query rows as the right operand: lane = row, 8 values a register
+        half8v q[RT][KF];
+        float factor[RT];
+        int lo[RT], hi[RT];
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = row0 + 16 * rt + n;
+            lo[rt] = hi[rt] = 0;
+            uint4v w[KF];
+            uint32_t top = 0;
+            for (int f = 0; f < KF; ++f)
+                w[f] = uint4v{0, 0, 0, 0};
+            if (r < s.rows) {
+                const uint16_t* src = a.q + (s.first + r / group) * a.ld_q + (h * group + r % group) * D;
+                for (int f = 0; f < KF; ++f) {
+                    // D > 64: chunk f / 4, dimensions 32 g + 8 (f % 4); else 16 g + 8 f
+                    const int d = D > 64 ? 128 * (f / 4) + 32 * g + 8 * (f % 4) : 16 * g + 8 * f;
+                    w[f] = *(const uint4v*)(src + d);
+                    top = largest_bits(w[f], top);
+                }
+                sees(a, s.len, s.rows / group, r / group, lo[rt], hi[rt]);
+            }
+            top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            const int e = row_exponent(top);
+            for (int f = 0; f < KF; ++f)
+                q[rt][f] = scaled_half8(w[f], e);
+            factor[rt] = ldexpf(k_scale, -e);
+        }
+
+        float4v o[RT][C][VM];
+        float m[RT], l[RT];
+        for (int rt = 0; rt < RT; ++rt) {
+            m[rt] = -INFINITY;
+            l[rt] = 0;
+            for (int c = 0; c < C; ++c)
+                for (int i = 0; i < VM; ++i)
+                    o[rt][c][i] = float4v{0, 0, 0, 0};
+        }
+
+        int t0 = first + 32 * wave;
+        Tile<D> next;
+        if (t0 < last)
+            load_tile<D, kPaged16>(next, a, table, h, t0, s.begin, s.end, lane);
+        for (; t0 < last; t0 += 128) {
+            Tile<D> t = next;
+            if (t0 + 128 < last)
+                load_tile<D, kPaged16>(next, a, table, h, t0 + 128, s.begin, s.end, lane);
+
+            // S^T = K Q^T
+            float4v sc[RT][2];
+            for (int hh = 0; hh < 2; ++hh)
+                for (int rt = 0; rt < RT; ++rt)
+                    sc[rt][hh] = float4v{0, 0, 0, 0};
+            for (int c = 0; c < C; ++c) {
+                const uint32_t mine = t.shown ? t.ks[c] : 0;
+                for (int hh = 0; hh < 2; ++hh) {
+                    uint32_t w = from_lane(mine, n + 16 * hh + (D > 64 ? 32 * (g >> 1) : 0));
+                    w >>= D > 64 ? 16 * (g & 1) : 8 * g;
+                    const half2v sk = e4m3x2(w);
+                    for (int i = 0; i < T::KW; ++i) {
+                        const half8v kf = fp4x8(t.k[hh][c][i], D > 64 ? sk[i >> 1] : sk[0]);
+                        for (int rt = 0; rt < RT; ++rt)
+                            sc[rt][hh] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                kf, q[rt][T::KW * c + i], sc[rt][hh], 0, 0, 0);
+                    }
+                }
+            }
+
+            // exponentials: base 2, against the row's lazily raised maximum
+            const bool whole = t0 >= s.all_begin && t0 + 32 <= s.all_end &&
+                               !(kPaged16 ? t.hidden0 || t.hidden1 : __any(!t.shown));
+            uint32_t hid = 0;      // bit j: token j of the tile does not count
+            if (!kPaged16)
+                hid = ~(uint32_t)__ballot(t.shown);
+            half8v p[RT];
+            for (int rt = 0; rt < RT; ++rt) {
+                float x[8];
+                for (int i = 0; i < 8; ++i)
+                    x[i] = sc[rt][i >> 2][i & 3] * factor[rt];
+                if (!whole) {
+                    for (int i = 0; i < 8; ++i) {
+                        const int in = 16 * (i >> 2) + 4 * g + (i & 3);
+                        const bool gone = kPaged16 ? (i < 4 ? t.hidden0 : t.hidden1) : (hid >> in & 1);
+                        if (gone || t0 + in < lo[rt] || t0 + in >= hi[rt])
+                            x[i] = -INFINITY;
+                    }
+                }
+                float top = x[0];
+                for (int i = 1; i < 8; ++i)
+                    top = fmaxf(top, x[i]);
+                if (__any(top > m[rt] + kSlack)) {
+                    const float up = fmaxf(m[rt], row_max(top));
+                    const float f = m[rt] == up ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - up);
+                    m[rt] = up;
+                    l[rt] *= f;
+                    for (int c = 0; c < C; ++c)
+                        for (int i = 0; i < VM; ++i)
+                            o[rt][c][i] *= f;
+                }
+                // a row that has seen nothing keeps m = -inf: its terms are 0
+                const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+                    l[rt] += x[i];
+                    p[rt][i] = (_Float16)x[i];
+                }
+            }
+
+            // O^T += V^T P^T
+            for (int c = 0; c < C; ++c) {
+                const uint32_t mine = t.shown ? t.vs[c] : 0;
+                const uint32_t byte = D > 64 ? (n >> 1) & 3 : n >> 2;
+                const uint32_t sel = byte | (4 + byte) << 8 | 0x0c0c0000u;
+                half2v sv[4];
+                uint32_t even[4], odd[4];       // dimensions 2x, 2x + 1 of token pairs, a byte each
+                for (int u = 0; u < 4; ++u) {
+                    const int tok = 16 * (u >> 1) + 4 * g + 2 * (u & 1) + (D > 64 ? 32 * (n >> 3) : 0);
+                    sv[u] = e4m3x2(__builtin_amdgcn_perm(from_lane(mine, tok + 1), from_lane(mine, tok), sel));
+                    const uint32_t x = t.v[2 * u][c], y = t.v[2 * u + 1][c];
+                    even[u] = (x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u);
+                    odd[u] = (x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+                }
+                for (int i = 0; i < VM; ++i) {
+                    const uint32_t* w = i & 1 ? odd : even;
+                    const half8v vf = join(fp4x2(w[0], i >> 1) * sv[0], fp4x2(w[1], i >> 1) * sv[1],
+                                           fp4x2(w[2], i >> 1) * sv[2], fp4x2(w[3], i >> 1) * sv[3]);
+                    for (int rt = 0; rt < RT; ++rt)
+                        o[rt][c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[rt][c][i], 0, 0, 0);
+                }
+            }
+        }
+
+        // Join the four waves, a row tile at a time.
+        for (int rt = 0; rt < RT; ++rt) {
+            const float sum = row_sum(l[rt]);
+            __syncthreads();
+            for (int c = 0; c < C; ++c)
+                for (int r = 0; r < 4; ++r)
+                    for (int i = 0; i < VM; i += 4)
+                        *(float4v*)&o_lds[wave][n][128 * c + VM * (4 * g + r) + i] =
+                            float4v{o[rt][c][i][r], o[rt][c][i + 1][r], o[rt][c][i + 2][r], o[rt][c][i + 3][r]};
+            if (g == 0) {
+                m_lds[wave][n] = m[rt];
+                l_lds[wave][n] = sum;
+            }
+            __syncthreads();
+            const int row = tid >> 4, r = row0 + 16 * rt + row;
+            if (r >= s.rows)
+                continue;
+            float top = -INFINITY, total = 0, f[4];
+            for (int w = 0; w < 4; ++w)
+                top = fmaxf(top, m_lds[w][row]);
+            for (int w = 0; w < 4; ++w) {
+                f[w] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m_lds[w][row] - top);
+                total += f[w] * l_lds[w][row];
+            }
+            const int64_t token = s.first + r / group;
+            const int head = h * group + r % group;
+            const bool whole_row = a.splits == 1;
+            const float norm = whole_row ? (total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
+            for (int d = (tid & 15) * 4; d < D; d += 64) {
+                float4v v = {0, 0, 0, 0};
+                for (int w = 0; w < 4; ++w)
+                    v += f[w] * *(float4v*)&o_lds[w][row][d];
+                v *= norm;
+                if (whole_row)
+                    *(uint2v*)(a.out + token * a.ld_out + head * D + d) = uint2v{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+                else
+                    *(float4v*)(a.part + (((int64_t)split * a.tokens + token) * a.heads + head) * D + d) = v;
+            }
+            if ((tid & 15) == 0) {
+                if (!whole_row) {
+                    float* ml = a.part + (int64_t)a.splits * a.tokens * a.heads * D +
+                                2 * (((int64_t)split * a.tokens + token) * a.heads + head);
+                    ml[0] = top;
+                    ml[1] = total;
+                } else if (a.lse) {
+                    a.lse[token * a.heads + head] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+    }
+}
+
+// Joins the splits of one query row: a workgroup per (token, head), whose four
+// waves take a share of the splits each.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int block)
+{
+    constexpr int kLanes = D / 4, kShares = 256 / kLanes;     // lanes across a row; splits read at once
+    __shared__ float4v o_lds[kShares][kLanes];
+    __shared__ float f_lds[256];
+    __shared__ float wave_top[4], wave_sum[4];
+    const int tid = threadIdx.x, head = blockIdx.x % a.heads, token = blockIdx.x / a.heads;
+    const int group = a.heads / a.kv_heads;
+    // the last request whose first row is at or before this one
+    int lo = 0, hi = a.num_seqs + 1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.offsets[mid] <= token)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    if (lo == a.num_seqs || token < a.offsets[0])
+        return;
+    Span s = request_span(a, lo, group);
+    const int r = (token - s.first) * group + head % group;
+    if (r < 0 || r >= s.rows)
+        return;
+    block_span(a, s, group, r / block * block, block);
+    const int used = max(1, (s.end - s.begin + s.chunk - 1) / s.chunk);   // at most a.splits <= 256
+    const int64_t rows = (int64_t)a.tokens * a.heads, row = (int64_t)token * a.heads + head;
+    const float* ml = a.part + a.splits * rows * D;
+
+    float m = -INFINITY, l = 0;
+    if (tid < used) {
+        m = ml[2 * (tid * rows + row)];
+        l = ml[2 * (tid * rows + row) + 1];
+    }
+    float top = m;
+    for (int d = 32; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    if ((tid & 63) == 0)
+        wave_top[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+    f_lds[tid] = f;
+    float sum = f * l;
+    for (int d = 32; d; d >>= 1)
+        sum += __shfl_xor(sum, d);
+    if ((tid & 63) == 0)
+        wave_sum[tid >> 6] = sum;
+    __syncthreads();
+    const float total = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+
+    const int share = tid / kLanes, x = tid % kLanes;
+    float4v o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = share; i < used; i += kShares)
+        o += f_lds[i] * *(const float4v*)(a.part + (i * rows + row) * D + 4 * x);
+    o_lds[share][x] = o;
+    __syncthreads();
+    if (tid < kLanes) {
+        for (int i = 1; i < kShares; ++i)
+            o += o_lds[i][tid];
+        o *= total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f;
+        *(uint2v*)(a.out + token * a.ld_out + head * D + 4 * tid) = uint2v{bf16x2(o[0], o[1]), bf16x2(o[2], o[3])};
+        if (tid == 0 && a.lse)
+            a.lse[row] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+struct Plan {
+    int tiles;         // 16-row tiles of a workgroup
+    int row_blocks;    // workgroups over a request's rows
+    int splits, chunk; // of the tokens
+};
+
+Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,
+               int64_t max_query_len, int64_t max_seq_len, int64_t window)
+{
+    using serving::ceil_div;
+    Plan p;
+    const int64_t group = heads / kv_heads;
+    const int64_t rows = (max_query_len < 1 ? 1 : max_query_len > (1 << 20) ? 1 << 20 : max_query_len) * group;
+    p.tiles = rows <= 16 || head_dim > 128 ? 1 : rows <= 32 ? 2 : 4;
+    int64_t blocks = ceil_div(rows, (int64_t)16 * p.tiles);
+    p.row_blocks = (int)(blocks > 1024 ? 1024 : blocks);
+    int64_t range = max_seq_len > INT32_MAX ? INT32_MAX : max_seq_len;
+    if (window > 0 && window + max_query_len + 32 < range)
+        range = window + max_query_len + 32;
+    const int64_t items = (num_seqs < 1 ? 1 : num_seqs) * kv_heads * p.row_blocks;
+    int64_t want = ceil_div((int64_t)1024, items);
+    const int64_t least = ceil_div(range, (int64_t)1024);
+    if (want < least)
+        want = least;
+    int64_t chunk = ceil_div(ceil_div(range, want), (int64_t)128) * 128;
+    if (chunk < 128)
+        chunk = 128;
+    int64_t splits = ceil_div(range < 1 ? 1 : range, chunk);
+    if (splits > 256)
+        splits = 256;
+    // grids stay below 2^24 workgroups (rows and splits left out are looped over)
+    if (tokens * heads > (1 << 22))
+        splits = 1;
+    const int64_t most = ((1 << 24) - 16) / ((num_seqs < 1 ? 1 : num_seqs) * kv_heads);
+    if (splits * p.row_blocks > most) {
+        splits = 1;
+        if (p.row_blocks > most)
+            p.row_blocks = (int)(most < 1 ? 1 : most);
+    }
+    chunk = ceil_div(ceil_div(range, splits), (int64_t)128) * 128;
+    if (chunk < 128)
+        chunk = 128;
+    p.splits = (int)splits;
+    p.chunk = (int)chunk;
+    return p;
+}
+
+template <int D, int RT>
+void launch_rows(const Attn& a, dim3 grid, hipStream_t stream)
+{
+    if (a.page % 16 == 0)
+        hipLaunchKernelGGL((attn_rows_kernel<D, RT, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attn_rows_kernel<D, RT, false>), grid, dim3(256), 0, stream, a);
 }
 
 template <int D>
-__global__ __launch_bounds__(64) void attn_plain_kernel(Attn a)
+void launch(const Attn& a, int tiles, hipStream_t stream)
 {
-    constexpr int N = D / 64;
-    const int lane = threadIdx.x, t = blockIdx.x, h = blockIdx.y;
-    int b = 0;
-    while (b < a.num_seqs && !(a.offsets[b] <= t && t < a.offsets[b + 1]))
-        ++b;
-    if (b == a.num_seqs)
-        return;
-    const int kvh = h / (a.heads / a.kv_heads), cols = a.kv_heads * D;
-    const int64_t len = min((int64_t)max(a.lens[b], 0), (int64_t)a.max_pages * a.page);
-    const int64_t pos = len - (a.offsets[b + 1] - t);
-    const int64_t end = a.causal ? min(pos + 1, len) : len;
-    const int64_t start = a.window > 0 ? max(pos - a.window + 1, (int64_t)0) : 0;
-    float q[N], o[N], m = -INFINITY, l = 0;
-    for (int i = 0; i < N; ++i) {
-        const uint32_t w = a.q[t * a.ld_q + h * D + lane * N + i];
-        q[i] = __uint_as_float(w << 16) * a.scale * (a.k_gs ? a.k_gs[0] : 1.0f);
-        o[i] = 0;
+    const int64_t work = (int64_t)a.num_seqs * a.row_blocks * a.splits;
+    const dim3 grid((unsigned)((work + 7) / 8 * 8 * a.kv_heads));
+    if (tiles == 1)
+        launch_rows<D, 1>(a, grid, stream);
+    if constexpr (D <= 128) {
+        if (tiles == 2)
+            launch_rows<D, 2>(a, grid, stream);
+        else if (tiles == 4)
+            launch_rows<D, 4>(a, grid, stream);
     }
-    for (int64_t j = start; j < end; ++j) {
-        const int page = a.table[b * a.ld_table + j / a.page];
-        if (page < 0 || page >= a.num_pages)
-            continue;
-        const int64_t slot = (int64_t)page * a.page + j % a.page;
-        float s = 0;
-        for (int i = 0; i < N; ++i) {
-            const int c = kvh * D + lane * N + i;
-            const uint32_t code = a.kp[slot * (cols / 2) + c / 2] >> (4 * (c & 1));
-            s = fmaf(q[i], e2m1(code) * nvfp4::fp8_e4m3_decode(a.ks[slot * (cols / 16) + c / 16]), s);
-        }
-        for (int d = 32; d; d >>= 1)
-            s += __shfl_xor(s, d);
-        const float top = fmaxf(m, s), f = expf(m - top), p = expf(s - top);
-        l = l * f + p;
-        m = top;
-        for (int i = 0; i < N; ++i) {
-            const int c = kvh * D + lane * N + i;
-            const uint32_t code = a.vp[slot * (cols / 2) + c / 2] >> (4 * (c & 1));
-            o[i] = fmaf(p, e2m1(code) * nvfp4::fp8_e4m3_decode(a.vs[slot * (cols / 16) + c / 16]),
-                        o[i] * f);
-        }
-    }
-    const float gs = a.v_gs ? a.v_gs[0] : 1.0f;
-    for (int i = 0; i < N; ++i) {
-        const __bf16 r = (__bf16)(l > 0 ? o[i] * gs / l : 0.0f);
-        a.out[t * a.ld_out + h * D + lane * N + i] = __builtin_bit_cast(uint16_t, r);
-    }
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)t * a.heads + h] = l > 0 ? m + logf(l) : -INFINITY;
+    if (a.splits > 1)
+        hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)a.tokens * a.heads), dim3(256), 0, stream, a,
+                           16 * tiles);
 }
 
 bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,
@@ -88,10 +643,11 @@ bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
            heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0;
 }
 
-bool sizes_supported(int64_t tokens, int32_t heads, int32_t head_dim, int64_t num_seqs)
+bool sizes_supported(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                     int64_t num_seqs)
 {
     return (head_dim == 64 || head_dim == 128 || head_dim == 256) && heads <= 1024 &&
-           num_seqs <= 65535 && tokens <= INT32_MAX;
+           num_seqs <= 65535 && num_seqs * kv_heads <= (1 << 22) && tokens <= INT32_MAX;
 }
 
 }  // namespace
@@ -103,9 +659,11 @@ extern "C" int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads
 {
     if (!sizes_ok(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len,
                   window) ||
-        !sizes_supported(tokens, heads, head_dim, num_seqs))
+        !sizes_supported(tokens, heads, kv_heads, head_dim, num_seqs))
         return -1;
-    return 0;
+    const Plan p = make_plan(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len, window);
+    // a split's outputs and (maximum, sum) pairs of every row
+    return p.splits > 1 ? tokens * heads * (head_dim + 2) * 4 * p.splits : 0;
 }
 
 extern "C" nvfp4_status_t nvfp4_paged_attention(
@@ -124,8 +682,8 @@ extern "C" nvfp4_status_t nvfp4_paged_attention(
         ld_table < max_pages || !extent_ok(num_seqs, ld_table, 4) || ld_q < 0 || ld_out < 0 ||
         workspace_bytes < 0 || !(scale - scale == 0.0f))
         return NVFP4_ERROR_INVALID_VALUE;
-    if (!sizes_supported(tokens, heads, head_dim, num_seqs) || num_slots > INT32_MAX ||
-        max_pages > INT32_MAX / page_size)
+    if (!sizes_supported(tokens, heads, kv_heads, head_dim, num_seqs) || num_slots > INT32_MAX ||
+        max_pages > (1 << 30) / page_size)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     const int64_t cols = (int64_t)heads * head_dim;
     if (ld_q < cols || ld_out < cols || !extent_ok(tokens, ld_q, 2) || !extent_ok(tokens, ld_out, 2))
@@ -147,15 +705,24 @@ extern "C" nvfp4_status_t nvfp4_paged_attention(
                                                          window);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return NVFP4_ERROR_INVALID_VALUE;
+    const Plan p = make_plan(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len, window);
     Attn a = {q, k_packed, k_scales, v_packed, v_scales, block_table, seq_lens, query_offsets,
-              k_gs, v_gs, out, lse, ld_q, ld_out, ld_table, window, (int)tokens, heads, kv_heads,
-              page_size, (int)(num_slots / page_size), (int)max_pages, (int)num_seqs, causal, scale};
-    const dim3 grid((unsigned)tokens, (unsigned)heads);
+              k_gs, v_gs, out, lse, (float*)workspace, ld_q, ld_out, ld_table, window, (int)tokens,
+              heads, kv_heads, page_size, (int)(num_slots / page_size), (int)max_pages,
+              (int)num_seqs, causal, scale};
+    int shift = 0;
+    while (((int64_t)1 << shift) < page_size)
+        ++shift;
+    a.page_shift = 31 + shift;
+    a.page_magic = (uint32_t)((((uint64_t)1 << a.page_shift) + page_size - 1) / page_size);
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.row_blocks = p.row_blocks;
     if (head_dim == 64)
-        hipLaunchKernelGGL(attn_plain_kernel<64>, grid, dim3(64), 0, stream, a);
+        launch<64>(a, p.tiles, stream);
     else if (head_dim == 128)
-        hipLaunchKernelGGL(attn_plain_kernel<128>, grid, dim3(64), 0, stream, a);
+        launch<128>(a, p.tiles, stream);
     else
-        hipLaunchKernelGGL(attn_plain_kernel<256>, grid, dim3(64), 0, stream, a);
+        launch<256>(a, p.tiles, stream);
     return launched();
 }
