@@ -158,7 +158,7 @@ int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads, int32_t k
  * top_k <= 32 and <= num_experts; ld_x, ld_out multiples of 8; x, out, weights
  * and scales... 16-byte aligned (scales 2-byte, logits, ids, weights 4-byte).
  * tokens == 0 is a no-op. workspace: moe_layer_workspace(...) bytes, 16-byte
- * aligned. Two kernels.
+ * aligned. Three kernels.
  */
 nvfp4_status_t moe_layer_nvfp4(const uint16_t *x, int64_t tokens, int64_t ld_x,
                                const float *logits, const uint8_t *w1_packed,

@@ -1,15 +1,24 @@
 // A whole mixture-of-experts layer for a few tokens (include/nvfp4_serving.h).
 //
-// The simplest form, two kernels. The first: one workgroup per (token, rank)
-// pair and slice of 64 intermediate columns; it finds the pair's expert from
-// the logits by counting, and each wave sums the products of its columns. The
-// second: one workgroup per token and slice of 64 outputs.
+// Bound by memory: every weight of the reached experts is read once. Three
+// kernels. The first two are one grouped product each, h = swiglu(x W1^T) and
+// y = h W2^T, with a workgroup per (expert, 64 weight rows); a row tile of 16
+// weights stands in the left operand of the matrix instructions, straight from
+// memory, the expert's tokens in the right one, from LDS. The third adds up a
+// token's top_k rows of y with the routing weights. The first finds the
+// routing itself: each workgroup counts, for the tokens, how many logits stand
+// before its expert's.
+#include "fp4_operand.hpp"
 #include "serving_common.hpp"
-#include "nvfp4_device.hpp"
 
 namespace {
 
+using namespace fp4op;
+
+typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
+
 constexpr int kThreads = 256;
+constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 32;
 
 struct Moe {
     const uint16_t* x;
@@ -21,133 +30,373 @@ struct Moe {
     int32_t* ids;
     float* weights;
     float* h;          // workspace: [tokens * top_k][inter]
+    float* y;          // workspace: [tokens * top_k][hidden]
+    float* p;          // workspace: [tokens * top_k] probabilities
     int64_t ld_x, ld_out;
     int tokens, hidden, inter, experts, top_k, renormalize;
+    int by_pair;       // workgroups go by (token, rank) pairs, not by experts
 };
 
-__device__ __forceinline__ float e2m1(uint32_t c)
-{
-    const uint32_t m = c & 7u;
-    const float v = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-    return c & 8u ? -v : v;
-}
-
 // A logit as it is compared: NaN stands behind everything, with -inf.
-__device__ __forceinline__ float logit(const float* row, int e)
+__device__ __forceinline__ float logit(const Moe& a, int t, int e)
 {
-    const float v = row[e];
+    const float v = a.logits[t * a.experts + e];
     return v == v ? v : -INFINITY;
 }
 
-template <bool kFp4>
-__device__ __forceinline__ float weight(const void* w, const uint8_t* s, int64_t row, int cols, int c)
+// How many experts stand before expert e (with logit v) for token t; by a wave.
+__device__ __forceinline__ int rank_of(const Moe& a, int t, int e, float v, int lane)
 {
-    if (!kFp4)
-        return __uint_as_float((uint32_t)((const uint16_t*)w)[row * cols + c] << 16);
-    const uint32_t code = ((const uint8_t*)w)[row * (cols / 2) + c / 2] >> (4 * (c & 1));
-    return e2m1(code) * nvfp4::fp8_e4m3_decode(s[row * (cols / 16) + c / 16]);
-}
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    for (int d = 32; d; d >>= 1)
-        v += __shfl_xor(v, d);
-    return v;
-}
-
-template <bool kFp4>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(Moe a)
-{
-    __shared__ int found;
-    __shared__ float chosen;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int pair = blockIdx.x, t = pair / a.top_k, k = pair % a.top_k;
-    const float* row = a.logits + (int64_t)t * a.experts;
-    for (int e = tid; e < a.experts; e += kThreads) {
-        const float v = logit(row, e);
-        int rank = 0;
-        for (int f = 0; f < a.experts; ++f) {
-            const float u = logit(row, f);
-            rank += u > v || (u == v && f < e);
+    int rank = 0;
+    for (int f0 = 0; f0 < a.experts; f0 += 64) {
+        const int f = f0 + lane;
+        bool before = false;
+        if (f < a.experts) {
+            const float u = logit(a, t, f);
+            before = u > v || (u == v && f < e);
         }
-        if (rank == k) {
-            found = v == -INFINITY ? -1 : e;
-            chosen = v;
+        rank += __popcll(__ballot(before));
+    }
+    return rank;
+}
+
+// softmax(logits[t])[e]; by a wave.
+__device__ __forceinline__ float probability(const Moe& a, int t, float v, int lane)
+{
+    float top = -INFINITY, sum = 0;
+    for (int f = lane; f < a.experts; f += 64)
+        top = fmaxf(top, logit(a, t, f));
+    for (int d = 32; d; d >>= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    for (int f = lane; f < a.experts; f += 64) {
+        const float u = logit(a, t, f);
+        sum += u == top ? 1.0f : expf(u - top);       // +inf - +inf would be NaN
+    }
+    for (int d = 32; d; d >>= 1)
+        sum += __shfl_xor(sum, d);
+    return (v == top ? 1.0f : expf(v - top)) / sum;
+}
+
+// The expert of this workgroup and the pairs (token * top_k + rank) routed to
+// it, in the order of the tokens: `count` of them in pairs[]. Returns -1 when
+// there is none, or when another workgroup has this expert.
+struct Group {
+    int pairs[kMaxTokens];
+    int rank[kMaxTokens];
+    int expert, count;
+    float row[kMaxExperts];
+};
+
+// From the logits; workgroups of slice 0 also write ids and probabilities.
+__device__ int route(const Moe& a, Group& s, int slot, bool write, int tid)
+{
+    const int lane = tid & 63, wave = tid >> 6;
+    int e = slot;
+    if (a.by_pair) {
+        const int t = slot / a.top_k, k = slot % a.top_k;
+        for (int f = tid; f < a.experts; f += kThreads)
+            s.row[f] = logit(a, t, f);
+        __syncthreads();
+        for (int f = tid; f < a.experts; f += kThreads) {
+            const float v = s.row[f];
+            int rank = 0;
+            for (int u = 0; u < a.experts; ++u)
+                rank += s.row[u] > v || (s.row[u] == v && u < f);
+            if (rank == k)
+                s.expert = f;
+        }
+        __syncthreads();
+        e = s.expert;
+    }
+    for (int t = wave; t < a.tokens; t += kThreads / 64) {
+        const float v = logit(a, t, e);
+        int rank = rank_of(a, t, e, v, lane);
+        const bool here = rank < a.top_k && (!a.by_pair || t * a.top_k + rank == slot);
+        if (write && here) {
+            const float p = v == -INFINITY ? 0.0f : probability(a, t, v, lane);
+            if (lane == 0) {
+                a.ids[t * a.top_k + rank] = v == -INFINITY ? -1 : e;
+                a.p[t * a.top_k + rank] = p;
+            }
+        }
+        if (lane == 0)
+            s.rank[t] = v == -INFINITY ? kMaxTopK : rank;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const bool in = lane < a.tokens && s.rank[lane] < a.top_k;
+        const uint64_t all = __ballot(in);
+        if (in)
+            s.pairs[__popcll(all & ((1ull << lane) - 1))] = lane * a.top_k + s.rank[lane];
+        if (lane == 0)
+            s.count = __popcll(all);
+    }
+    __syncthreads();
+    return s.count == 0 || (a.by_pair && s.pairs[0] != slot) ? -1 : e;
+}
+
+// The same from the ids that the first kernel wrote.
+__device__ int routed(const Moe& a, Group& s, int slot, int tid)
+{
+    const int lane = tid & 63, wave = tid >> 6;
+    const int e = a.by_pair ? a.ids[slot] : slot;
+    if (wave == 0) {
+        int rank = kMaxTopK;
+        if (lane < a.tokens)
+            for (int k = 0; k < a.top_k; ++k)
+                if (a.ids[lane * a.top_k + k] == e)
+                    rank = k;
+        const bool in = e >= 0 && rank < a.top_k;
+        const uint64_t all = __ballot(in);
+        if (in)
+            s.pairs[__popcll(all & ((1ull << lane) - 1))] = lane * a.top_k + rank;
+        if (lane == 0)
+            s.count = __popcll(all);
+    }
+    __syncthreads();
+    return s.count == 0 || (a.by_pair && s.pairs[0] != slot) ? -1 : e;
+}
+
+// Chunk of the summed axis that is staged at a time, and what a lane holds of
+// a 16-row weight tile for it. Lane (g = lane / 16, n = lane % 16) holds row
+// n; NVFP4: step s is 16 bytes, k = 128 s + 32 g .. + 31, with two scale
+// bytes; BF16: 16 bytes, k = 32 s + 8 g .. + 7.
+template <bool kFp4, int NT>
+struct Shape {
+    static constexpr int KC = kFp4 && NT < 4 ? 512 : 256;
+    static constexpr int kRun = kFp4 ? 128 : 32;       // k of a step
+    static constexpr int S = KC / kRun;
+    static constexpr int kPitch = KC + 8;              // 16-bit elements: rows 4 banks apart
+};
+
+template <bool kFp4, int NT>
+struct Weights {
+    uint4v w[Shape<kFp4, NT>::S];
+    uint32_t sc[kFp4 ? Shape<kFp4, NT>::S : 1];
+};
+
+template <bool kFp4, int NT>
+__device__ __forceinline__ void load_weights(Weights<kFp4, NT>& r, const uint8_t* row,
+                                             const uint8_t* scales, int k0, int K, int g)
+{
+    using X = Shape<kFp4, NT>;
+    for (int s = 0; s < X::S; ++s) {
+        int k = k0 + X::kRun * s + (kFp4 ? 32 : 8) * g;
+        if (k >= K)
+            k = 0;          // behind the row: any weights, their right operand is 0
+        if (kFp4) {
+            r.w[s] = *(const uint4v*)(row + k / 2);
+            r.sc[s] = *(const uint16_t*)(scales + k / 16);
+        } else {
+            r.w[s] = *(const uint4v*)(row + 2 * k);
+        }
+    }
+}
+
+// The tokens' side of a chunk: 16 threads a token, each with runs of 8
+// elements 128 apart.
+template <bool kFp4, bool kDown, int NT>
+struct Tokens {
+    static constexpr int R = Shape<kFp4, NT>::KC / 128;     // runs of a thread
+    static constexpr int kWords = kDown ? 8 : 4;            // FP32 h or BF16 x
+    uint32_t v[NT][R][kWords];
+};
+
+template <bool kFp4, bool kDown, int NT>
+__device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, const Moe& a,
+                                            const Group& s, int k0, int K, int tid)
+{
+    using X = Tokens<kFp4, kDown, NT>;
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = 16 * nt + (tid >> 4);
+        for (int i = 0; i < X::R; ++i) {
+            const int k = k0 + 128 * i + 8 * (tid & 15);
+            for (int w = 0; w < X::kWords; ++w)
+                r.v[nt][i][w] = 0;
+            if (col < s.count && k < K) {
+                const int pair = s.pairs[col];
+                const uint4v* src = kDown ? (const uint4v*)(a.h + (int64_t)pair * K + k)
+                                          : (const uint4v*)(a.x + (pair / a.top_k) * a.ld_x + k);
+                for (int w = 0; w < X::kWords / 4; ++w) {
+                    const uint4v u = src[w];
+                    for (int j = 0; j < 4; ++j)
+                        r.v[nt][i][4 * w + j] = u[j];
+                }
+            }
+        }
+    }
+}
+
+// FP32 values of a run of 8.
+template <bool kDown>
+__device__ __forceinline__ void values(const uint32_t* v, float* f)
+{
+    for (int j = 0; j < 8; ++j)
+        f[j] = kDown ? __uint_as_float(v[kDown ? j : 0])
+                     : __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
+}
+
+template <bool kFp4, bool kDown, int NT>
+__global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
+{
+    using X = Shape<kFp4, NT>;
+    constexpr bool kSplit = !kFp4 && kDown;      // h as a sum of two BF16 numbers
+    __shared__ Group s;
+    __shared__ __attribute__((aligned(16))) uint16_t tok_lds[2][kSplit ? 2 : 1][16 * NT][X::kPitch];
+    __shared__ float scale_lds[2][16 * NT];      // 2^-e of a token's chunk
+
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int e = kDown ? routed(a, s, blockIdx.y, tid)
+                        : route(a, s, blockIdx.y, blockIdx.x == 0, tid);
+    if (e < 0)
+        return;
+    const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
+    const int tiles = (s.count + 15) >> 4;
+    const int row0 = blockIdx.x * 64 + 16 * wave;
+    const bool mine = row0 < rows;
+    const int64_t row = (int64_t)e * rows + (mine ? row0 : 0) + n;
+    const uint8_t* w = (const uint8_t*)(kDown ? a.w2 : a.w1) + (kFp4 ? row * (K / 2) : row * K * 2);
+    const uint8_t* sc = kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr;
+
+    float4v acc[NT];
+    for (int nt = 0; nt < NT; ++nt)
+        acc[nt] = float4v{0, 0, 0, 0};
+
+    Weights<kFp4, NT> next;
+    Tokens<kFp4, kDown, NT> tokens;
+    load_weights<kFp4, NT>(next, w, sc, 0, K, g);
+    load_tokens<kFp4, kDown, NT>(tokens, a, s, 0, K, tid);
+    for (int k0 = 0, buf = 0; k0 < K; k0 += X::KC, buf ^= 1) {
+        // this chunk's tokens into LDS
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = 16 * nt + (tid >> 4);
+            int ex = 0;
+            if (kFp4) {
+                uint32_t top = 0;
+                for (int i = 0; i < X::KC / 128; ++i) {
+                    float f[8];
+                    values<kDown>(tokens.v[nt][i], f);
+                    for (int j = 0; j < 8; ++j)
+                        top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+                }
+                for (int d = 1; d < 16; d <<= 1)
+                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
+                ex = fp16_exponent(top);
+                if ((tid & 15) == 0)
+                    scale_lds[buf][col] = ldexpf(1.0f, -ex);
+            }
+            for (int i = 0; i < X::KC / 128; ++i) {
+                uint4v* dst = (uint4v*)&tok_lds[buf][0][col][128 * i + 8 * (tid & 15)];
+                if (!kFp4 && !kDown) {
+                    const uint32_t* v = tokens.v[nt][i];
+                    *dst = uint4v{v[0], v[1], v[2], v[3]};
+                    continue;
+                }
+                float f[8];
+                values<kDown>(tokens.v[nt][i], f);
+                if (kFp4) {
+                    half8v h;
+                    for (int j = 0; j < 8; ++j)
+                        h[j] = (_Float16)ldexpf(f[j], ex);
+                    *dst = __builtin_bit_cast(uint4v, h);
+                } else {
+                    bf8v hi, lo;
+                    for (int j = 0; j < 8; ++j) {
+                        hi[j] = (__bf16)f[j];
+                        lo[j] = (__bf16)(f[j] - (float)hi[j]);
+                    }
+                    *dst = __builtin_bit_cast(uint4v, hi);
+                    *(uint4v*)&tok_lds[buf][kSplit ? 1 : 0][col][128 * i + 8 * (tid & 15)] =
+                        __builtin_bit_cast(uint4v, lo);
+                }
+            }
+        }
+        const Weights<kFp4, NT> now = next;
+        if (k0 + X::KC < K) {
+            load_weights<kFp4, NT>(next, w, sc, k0 + X::KC, K, g);
+            load_tokens<kFp4, kDown, NT>(tokens, a, s, k0 + X::KC, K, tid);
+        }
+        __syncthreads();
+
+        float4v c[NT];
+        for (int nt = 0; nt < NT; ++nt)
+            c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
+        for (int st = 0; st < X::S; ++st) {
+            if (kFp4) {
+                const half2v sv = e4m3x2(now.sc[kFp4 ? st : 0]);
+                for (int i = 0; i < 4; ++i) {
+                    const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < tiles)
+                            c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                wf, *(const half8v*)&tok_lds[buf][0][16 * nt + n][128 * st + 32 * g + 8 * i],
+                                c[nt], 0, 0, 0);
+                }
+            } else {
+                const bf8v wf = __builtin_bit_cast(bf8v, now.w[st]);
+                for (int nt = 0; nt < NT; ++nt)
+                    if (nt < tiles) {
+                        c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            wf, *(const bf8v*)&tok_lds[buf][0][16 * nt + n][32 * st + 8 * g], c[nt], 0, 0, 0);
+                        if (kSplit)
+                            c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                wf, *(const bf8v*)&tok_lds[buf][kSplit ? 1 : 0][16 * nt + n][32 * st + 8 * g],
+                                c[nt], 0, 0, 0);
+                    }
+            }
+        }
+        for (int nt = 0; nt < NT; ++nt)
+            acc[nt] = kFp4 ? acc[nt] + c[nt] * scale_lds[buf][16 * nt + n] : c[nt];
+    }
+
+    const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = 16 * nt + n;
+        const float4v v = acc[nt] * gs;
+        if (kDown) {
+            if (mine && col < s.count)
+                *(float4v*)(a.y + (int64_t)s.pairs[col] * rows + row0 + 4 * g) = v;
+        } else {
+            // rows 0..7 of the tile (g = 0, 1) are gates, 8..15 their ups
+            float4v h;
+            for (int r = 0; r < 4; ++r) {
+                const float up = __shfl_xor(v[r], 32);
+                h[r] = v[r] / (1.0f + expf(-v[r])) * up;
+            }
+            if (mine && g < 2 && col < s.count)
+                *(float4v*)(a.h + (int64_t)s.pairs[col] * a.inter + row0 / 2 + 4 * g) = h;
+        }
+    }
+}
+
+// out[t] = sum_k w[t][k] y[t][k], in the order of k; the first workgroup of a
+// token also writes its weights.
+__global__ __launch_bounds__(kThreads) void moe_sum_kernel(Moe a)
+{
+    __shared__ float w[kMaxTopK];
+    const int t = blockIdx.y, tid = threadIdx.x;
+    if (tid < 64) {
+        const int k = tid;
+        const float p = k < a.top_k ? a.p[t * a.top_k + k] : 0.0f;
+        float total = p;
+        for (int d = 32; d; d >>= 1)
+            total += __shfl_xor(total, d);
+        if (k < a.top_k) {
+            w[k] = a.renormalize && total > 0 ? p / total : p;
+            if (blockIdx.x == 0)
+                a.weights[t * a.top_k + k] = w[k];
         }
     }
     __syncthreads();
-    const int e = found;
-    if (blockIdx.y == 0 && tid == 0) {
-        float top = -INFINITY, sum = 0;
-        for (int f = 0; f < a.experts; ++f)
-            top = fmaxf(top, logit(row, f));
-        for (int f = 0; f < a.experts; ++f) {
-            const float v = logit(row, f);
-            sum += v == top ? 1.0f : expf(v - top);
-        }
-        a.ids[pair] = e;
-        a.weights[pair] = e < 0 ? 0.0f : (chosen == top ? 1.0f : expf(chosen - top)) / sum;
+    const int n = (blockIdx.x * kThreads + tid) * 4;
+    if (n < a.hidden) {
+        float4v v = {0, 0, 0, 0};
+        for (int k = 0; k < a.top_k; ++k)
+            if (a.ids[t * a.top_k + k] >= 0)
+                v += w[k] * *(const float4v*)(a.y + (int64_t)(t * a.top_k + k) * a.hidden + n);
+        *(uint2v*)(a.out + t * a.ld_out + n) = uint2v{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
     }
-    if (e < 0)
-        return;
-    for (int c = wave; c < 64; c += kThreads / 64) {
-        const int j = blockIdx.y * 64 + c;
-        if (j >= a.inter)
-            break;
-        const int64_t r = (int64_t)e * 2 * a.inter + 16 * (j / 8) + j % 8;
-        float g = 0, u = 0;
-        for (int i = lane; i < a.hidden; i += 64) {
-            const float x = __uint_as_float((uint32_t)a.x[t * a.ld_x + i] << 16);
-            g = fmaf(x, weight<kFp4>(a.w1, a.s1, r, a.hidden, i), g);
-            u = fmaf(x, weight<kFp4>(a.w1, a.s1, r + 8, a.hidden, i), u);
-        }
-        const float gs = a.gs1 ? a.gs1[e] : 1.0f;
-        g = wave_sum(g) * gs;
-        u = wave_sum(u) * gs;
-        if (lane == 0)
-            a.h[(int64_t)pair * a.inter + j] = g / (1.0f + expf(-g)) * u;
-    }
-}
-
-template <bool kFp4>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(Moe a)
-{
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
-    float total = 0;
-    for (int k = 0; k < a.top_k; ++k)
-        total += a.weights[t * a.top_k + k];
-    for (int c = wave; c < 64; c += kThreads / 64) {
-        const int n = blockIdx.y * 64 + c;
-        if (n >= a.hidden)
-            break;
-        float y = 0;
-        for (int k = 0; k < a.top_k; ++k) {
-            const int e = a.ids[t * a.top_k + k];
-            if (e < 0)
-                continue;
-            float s = 0;
-            for (int i = lane; i < a.inter; i += 64)
-                s = fmaf(a.h[((int64_t)t * a.top_k + k) * a.inter + i],
-                         weight<kFp4>(a.w2, a.s2, (int64_t)e * a.hidden + n, a.inter, i), s);
-            float w = a.weights[t * a.top_k + k];
-            if (a.renormalize)
-                w /= total;
-            y += w * wave_sum(s) * (a.gs2 ? a.gs2[e] : 1.0f);
-        }
-        if (lane == 0)
-            a.out[t * a.ld_out + n] = __builtin_bit_cast(uint16_t, (__bf16)y);
-    }
-}
-
-__global__ void moe_renormalize_kernel(Moe a)
-{
-    const int t = threadIdx.x;
-    float total = 0;
-    for (int k = 0; k < a.top_k; ++k)
-        total += a.weights[t * a.top_k + k];
-    for (int k = 0; k < a.top_k; ++k)
-        if (total > 0)
-            a.weights[t * a.top_k + k] /= total;
 }
 
 nvfp4_status_t check_sizes(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts,
@@ -159,6 +408,30 @@ nvfp4_status_t check_sizes(int64_t tokens, int64_t hidden, int64_t inter, int32_
         hidden > (1 << 20) || inter > (1 << 20) || experts > 512 || top_k > 32)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     return NVFP4_SUCCESS;
+}
+
+template <bool kFp4, int NT>
+void launch_both(const Moe& a, hipStream_t stream)
+{
+    using serving::ceil_div;
+    const unsigned slots = (unsigned)(a.by_pair ? a.tokens * a.top_k : a.experts);
+    hipLaunchKernelGGL((moe_product_kernel<kFp4, false, NT>), dim3(ceil_div(2 * a.inter, 64), slots),
+                       dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((moe_product_kernel<kFp4, true, NT>), dim3(ceil_div(a.hidden, 64), slots),
+                       dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL(moe_sum_kernel, dim3(ceil_div(a.hidden, 4 * kThreads), a.tokens), dim3(kThreads),
+                       0, stream, a);
+}
+
+template <bool kFp4>
+void launch_products(const Moe& a, int nt, hipStream_t stream)
+{
+    if (nt == 1)
+        launch_both<kFp4, 1>(a, stream);
+    else if (nt == 2)
+        launch_both<kFp4, 2>(a, stream);
+    else
+        launch_both<kFp4, 4>(a, stream);
 }
 
 template <bool kFp4>
@@ -188,12 +461,13 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
     a.hidden = (int)hidden;
     a.inter = (int)inter;
     a.h = (float*)workspace;
-    hipLaunchKernelGGL(moe_up_kernel<kFp4>, dim3(a.tokens * a.top_k, ceil_div(a.inter, 64)),
-                       dim3(kThreads), 0, stream, a);
-    hipLaunchKernelGGL(moe_down_kernel<kFp4>, dim3(a.tokens, ceil_div(a.hidden, 64)),
-                       dim3(kThreads), 0, stream, a);
-    if (a.renormalize)
-        hipLaunchKernelGGL(moe_renormalize_kernel, dim3(1), dim3(a.tokens), 0, stream, a);
+    a.y = a.h + tokens * a.top_k * inter;
+    a.p = a.y + tokens * a.top_k * hidden;
+    // the reached experts are few: one workgroup column per pair, where pairs
+    // with an expert that an earlier token has leave at once; else per expert
+    a.by_pair = tokens * a.top_k <= a.experts;
+    const int nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+    launch_products<kFp4>(a, nt, stream);
     return launched();
 }
 
@@ -204,7 +478,7 @@ extern "C" int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t i
 {
     if (check_sizes(tokens, hidden, inter, num_experts, top_k) != NVFP4_SUCCESS)
         return -1;
-    return tokens * top_k * inter * 4;
+    return tokens * top_k * (inter + hidden + 1) * 4;
 }
 
 extern "C" nvfp4_status_t moe_layer_nvfp4(
@@ -215,7 +489,7 @@ extern "C" nvfp4_status_t moe_layer_nvfp4(
     void* workspace, int64_t workspace_bytes, hipStream_t stream)
 {
     Moe a = {x, logits, w1_packed, w2_packed, w1_scales, w2_scales, gs1, gs2, out, topk_ids,
-             topk_weights, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
+             topk_weights, nullptr, nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
     return run<true>(a, hidden, inter, workspace_bytes, tokens, workspace, stream);
 }
 
@@ -228,6 +502,6 @@ extern "C" nvfp4_status_t moe_layer_bf16(const uint16_t* x, int64_t tokens, int6
                                          int64_t workspace_bytes, hipStream_t stream)
 {
     Moe a = {x, logits, w1, w2, nullptr, nullptr, nullptr, nullptr, out, topk_ids, topk_weights,
-             nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
+             nullptr, nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
     return run<false>(a, hidden, inter, workspace_bytes, tokens, workspace, stream);
 }

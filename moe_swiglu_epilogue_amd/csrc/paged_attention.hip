@@ -1,20 +1,14 @@
 // Attention over the paged NVFP4 cache (include/nvfp4_serving.h).
 //
-// An E2M1 code times an E4M3 scale has at most 6 significant bits and lies in
-// [2^-10, 2688], so every cache value is exact in FP16. Both products run on
-// the FP16 matrix cores with FP32 sums, on values converted in registers: two
-// codes a conversion (v_cvt_scalef32_pk_f16_fp4), then one packed FP16
-// product with the block's scale. Global scales are folded into the softmax
-// scale and the output.
+// Both products run on the FP16 matrix cores with FP32 sums, on cache values
+// converted in registers (exact in FP16). Global scales are folded into the
+// softmax scale and the output.
+#include "fp4_operand.hpp"
 #include "serving_common.hpp"
 
 namespace {
 
-typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef _Float16 half8v __attribute__((ext_vector_type(8)));
-typedef float float4v __attribute__((ext_vector_type(4)));
-typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
-typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+using namespace fp4op;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
@@ -81,34 +75,6 @@ __device__ __forceinline__ uint32_t page_of(const Attn& a, uint32_t t)
     return (uint32_t)(((uint64_t)t * a.page_magic) >> a.page_shift);
 }
 
-__device__ __forceinline__ half2v fp4x2(uint32_t w, int byte)
-{
-    switch (byte) {
-    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
-    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
-    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
-    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
-    }
-}
-
-// The two E4M3 values in the low bytes of w.
-__device__ __forceinline__ half2v e4m3x2(uint32_t w)
-{
-    return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
-}
-
-__device__ __forceinline__ half8v join(half2v a, half2v b, half2v c, half2v d)
-{
-    return half8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// Eight codes of one block times its scale.
-__device__ __forceinline__ half8v fp4x8(uint32_t w, _Float16 scale)
-{
-    const half2v s = {scale, scale};
-    return join(fp4x2(w, 0) * s, fp4x2(w, 1) * s, fp4x2(w, 2) * s, fp4x2(w, 3) * s);
-}
-
 __device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane)
 {
     return (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)v);
@@ -144,22 +110,6 @@ __device__ __forceinline__ uint32_t largest_bits(uint4v w, uint32_t top)
     for (int i = 0; i < 4; ++i)
         top = max(top, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
     return top;
-}
-
-// Exponent that puts a row whose largest magnitude has these bits into
-// [2^14, 2^15); 0 for a row of zeros.
-__device__ __forceinline__ int row_exponent(uint32_t top)
-{
-    if (top == 0)
-        return 0;
-    return 14 - (ilogbf(__uint_as_float(top)));
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
-    const bf2 v = {(__bf16)lo, (__bf16)hi};
-    return __builtin_bit_cast(uint32_t, v);
 }
 
 // ---- few query rows ----------------------------------------------------------
@@ -330,7 +280,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
             }
             top = max(top, (uint32_t)__shfl_xor((int)top, 16));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-            const int e = row_exponent(top);
+            const int e = fp16_exponent(top);
             for (int f = 0; f < KF; ++f)
                 q[rt][f] = scaled_half8(w[f], e);
             factor[rt] = ldexpf(k_scale, -e);
