@@ -193,35 +193,40 @@ __device__ __forceinline__ void load_weights(Weights<kFp4, NT>& r, const uint8_t
     }
 }
 
-// The tokens' side of a chunk: 16 threads a token, each with runs of 8
-// elements 128 apart.
+// The tokens' side of a chunk: kLanes lanes a token, 8 elements each; a wave
+// takes every fourth group of kAtOnce tokens. Columns behind the last token
+// are left as they are: they only reach columns of the result that nothing
+// reads.
 template <bool kFp4, bool kDown, int NT>
 struct Tokens {
-    static constexpr int R = Shape<kFp4, NT>::KC / 128;     // runs of a thread
+    static constexpr int kLanes = Shape<kFp4, NT>::KC / 8;
+    static constexpr int kAtOnce = 64 / kLanes;
+    static constexpr int R = 4 * NT / kAtOnce;              // turns of a wave
     static constexpr int kWords = kDown ? 8 : 4;            // FP32 h or BF16 x
-    uint32_t v[NT][R][kWords];
+    uint32_t v[R][kWords];
 };
 
 template <bool kFp4, bool kDown, int NT>
-__device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, const Moe& a,
-                                            const Group& s, int k0, int K, int tid)
+__device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, const Moe& a, const int* pairs,
+                                            int count, int k0, int K, int wave, int lane)
 {
     using X = Tokens<kFp4, kDown, NT>;
-    for (int nt = 0; nt < NT; ++nt) {
-        const int col = 16 * nt + (tid >> 4);
-        for (int i = 0; i < X::R; ++i) {
-            const int k = k0 + 128 * i + 8 * (tid & 15);
-            for (int w = 0; w < X::kWords; ++w)
-                r.v[nt][i][w] = 0;
-            if (col < s.count && k < K) {
-                const int pair = s.pairs[col];
-                const uint4v* src = kDown ? (const uint4v*)(a.h + (int64_t)pair * K + k)
-                                          : (const uint4v*)(a.x + (pair / a.top_k) * a.ld_x + k);
-                for (int w = 0; w < X::kWords / 4; ++w) {
-                    const uint4v u = src[w];
-                    for (int j = 0; j < 4; ++j)
-                        r.v[nt][i][4 * w + j] = u[j];
-                }
+    const int k = k0 + 8 * (lane % X::kLanes);
+#pragma unroll
+    for (int i = 0; i < X::R; ++i) {
+        const int first = (wave + 4 * i) * X::kAtOnce, col = first + lane / X::kLanes;
+        if (first >= count)
+            continue;
+        for (int w = 0; w < X::kWords; ++w)
+            r.v[i][w] = 0;
+        if (col < count && k < K) {
+            const int pair = pairs[col];
+            const uint4v* src = kDown ? (const uint4v*)(a.h + (int64_t)pair * K + k)
+                                      : (const uint4v*)(a.x + (pair / a.top_k) * a.ld_x + k);
+            for (int w = 0; w < X::kWords / 4; ++w) {
+                const uint4v u = src[w];
+                for (int j = 0; j < 4; ++j)
+                    r.v[i][4 * w + j] = u[j];
             }
         }
     }
@@ -252,53 +257,58 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     if (e < 0)
         return;
     const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
-    const int tiles = (s.count + 15) >> 4;
     const int row0 = blockIdx.x * 64 + 16 * wave;
     const bool mine = row0 < rows;
     const int64_t row = (int64_t)e * rows + (mine ? row0 : 0) + n;
     const uint8_t* w = (const uint8_t*)(kDown ? a.w2 : a.w1) + (kFp4 ? row * (K / 2) : row * K * 2);
     const uint8_t* sc = kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr;
 
-    float4v acc[NT];
-    for (int nt = 0; nt < NT; ++nt)
-        acc[nt] = float4v{0, 0, 0, 0};
+    using Tok = Tokens<kFp4, kDown, NT>;
+    const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
 
-    Weights<kFp4, NT> next;
-    Tokens<kFp4, kDown, NT> tokens;
-    load_weights<kFp4, NT>(next, w, sc, 0, K, g);
-    load_tokens<kFp4, kDown, NT>(tokens, a, s, 0, K, tid);
-    for (int k0 = 0, buf = 0; k0 < K; k0 += X::KC, buf ^= 1) {
-        // this chunk's tokens into LDS
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = 16 * nt + (tid >> 4);
-            int ex = 0;
-            if (kFp4) {
-                uint32_t top = 0;
-                for (int i = 0; i < X::KC / 128; ++i) {
-                    float f[8];
-                    values<kDown>(tokens.v[nt][i], f);
-                    for (int j = 0; j < 8; ++j)
-                        top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-                }
-                for (int d = 1; d < 16; d <<= 1)
-                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
-                ex = fp16_exponent(top);
-                if ((tid & 15) == 0)
-                    scale_lds[buf][col] = ldexpf(1.0f, -ex);
-            }
-            for (int i = 0; i < X::KC / 128; ++i) {
-                uint4v* dst = (uint4v*)&tok_lds[buf][0][col][128 * i + 8 * (tid & 15)];
+    // Tokens beyond 16 NT take another pass over the weights.
+    for (int col0 = 0; col0 < s.count; col0 += 16 * NT) {
+        const int* pairs = s.pairs + col0;
+        const int count = min(s.count - col0, 16 * NT), tiles = (count + 15) >> 4;
+        float4v acc[NT];
+        for (int nt = 0; nt < NT; ++nt)
+            acc[nt] = float4v{0, 0, 0, 0};
+
+        Weights<kFp4, NT> next;
+        Tok tokens;
+        load_weights<kFp4, NT>(next, w, sc, 0, K, g);
+        load_tokens<kFp4, kDown, NT>(tokens, a, pairs, count, 0, K, wave, lane);
+        if (col0 > 0)
+            __syncthreads();        // the pass before may still read either buffer
+        for (int k0 = 0, buf = 0; k0 < K; k0 += X::KC, buf ^= 1) {
+            // this chunk's tokens into LDS
+#pragma unroll
+            for (int i = 0; i < Tok::R; ++i) {
+                const int first = (wave + 4 * i) * Tok::kAtOnce;
+                if (first >= count)
+                    continue;
+                const int col = first + lane / Tok::kLanes, at = 8 * (lane % Tok::kLanes);
+                uint4v* dst = (uint4v*)&tok_lds[buf][0][col][at];
                 if (!kFp4 && !kDown) {
-                    const uint32_t* v = tokens.v[nt][i];
+                    const uint32_t* v = tokens.v[i];
                     *dst = uint4v{v[0], v[1], v[2], v[3]};
                     continue;
                 }
                 float f[8];
-                values<kDown>(tokens.v[nt][i], f);
+                values<kDown>(tokens.v[i], f);
                 if (kFp4) {
+                    uint32_t top = 0;
+                    for (int j = 0; j < 8; ++j)
+                        top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+                    for (int d = 1; d < Tok::kLanes; d <<= 1)
+                        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+                    const int ex = fp16_exponent(top);
+                    const float up = ldexpf(1.0f, ex);
+                    if (at == 0)
+                        scale_lds[buf][col] = ldexpf(1.0f, -ex);
                     half8v h;
                     for (int j = 0; j < 8; ++j)
-                        h[j] = (_Float16)ldexpf(f[j], ex);
+                        h[j] = (_Float16)(f[j] * up);
                     *dst = __builtin_bit_cast(uint4v, h);
                 } else {
                     bf8v hi, lo;
@@ -307,65 +317,63 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                         lo[j] = (__bf16)(f[j] - (float)hi[j]);
                     }
                     *dst = __builtin_bit_cast(uint4v, hi);
-                    *(uint4v*)&tok_lds[buf][kSplit ? 1 : 0][col][128 * i + 8 * (tid & 15)] =
-                        __builtin_bit_cast(uint4v, lo);
+                    *(uint4v*)&tok_lds[buf][kSplit ? 1 : 0][col][at] = __builtin_bit_cast(uint4v, lo);
                 }
             }
-        }
-        const Weights<kFp4, NT> now = next;
-        if (k0 + X::KC < K) {
-            load_weights<kFp4, NT>(next, w, sc, k0 + X::KC, K, g);
-            load_tokens<kFp4, kDown, NT>(tokens, a, s, k0 + X::KC, K, tid);
-        }
-        __syncthreads();
+            const Weights<kFp4, NT> now = next;
+            if (k0 + X::KC < K) {
+                load_weights<kFp4, NT>(next, w, sc, k0 + X::KC, K, g);
+                load_tokens<kFp4, kDown, NT>(tokens, a, pairs, count, k0 + X::KC, K, wave, lane);
+            }
+            __syncthreads();
 
-        float4v c[NT];
-        for (int nt = 0; nt < NT; ++nt)
-            c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
-        for (int st = 0; st < X::S; ++st) {
-            if (kFp4) {
-                const half2v sv = e4m3x2(now.sc[kFp4 ? st : 0]);
-                for (int i = 0; i < 4; ++i) {
-                    const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
-                    for (int nt = 0; nt < NT; ++nt)
-                        if (nt < tiles)
-                            c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                                wf, *(const half8v*)&tok_lds[buf][0][16 * nt + n][128 * st + 32 * g + 8 * i],
-                                c[nt], 0, 0, 0);
-                }
-            } else {
-                const bf8v wf = __builtin_bit_cast(bf8v, now.w[st]);
-                for (int nt = 0; nt < NT; ++nt)
-                    if (nt < tiles) {
-                        c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wf, *(const bf8v*)&tok_lds[buf][0][16 * nt + n][32 * st + 8 * g], c[nt], 0, 0, 0);
-                        if (kSplit)
-                            c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                wf, *(const bf8v*)&tok_lds[buf][kSplit ? 1 : 0][16 * nt + n][32 * st + 8 * g],
-                                c[nt], 0, 0, 0);
+            float4v c[NT];
+            for (int nt = 0; nt < NT; ++nt)
+                c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
+            for (int st = 0; st < X::S; ++st) {
+                if (kFp4) {
+                    const half2v sv = e4m3x2(now.sc[kFp4 ? st : 0]);
+                    for (int i = 0; i < 4; ++i) {
+                        const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            if (nt < tiles)
+                                c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                    wf, *(const half8v*)&tok_lds[buf][0][16 * nt + n][128 * st + 32 * g + 8 * i],
+                                    c[nt], 0, 0, 0);
                     }
+                } else {
+                    const bf8v wf = __builtin_bit_cast(bf8v, now.w[st]);
+                    for (int nt = 0; nt < NT; ++nt)
+                        if (nt < tiles) {
+                            c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                wf, *(const bf8v*)&tok_lds[buf][0][16 * nt + n][32 * st + 8 * g], c[nt], 0, 0, 0);
+                            if (kSplit)
+                                c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    wf, *(const bf8v*)&tok_lds[buf][kSplit ? 1 : 0][16 * nt + n][32 * st + 8 * g],
+                                    c[nt], 0, 0, 0);
+                        }
+                }
             }
+            for (int nt = 0; nt < NT; ++nt)
+                acc[nt] = kFp4 ? acc[nt] + c[nt] * scale_lds[buf][16 * nt + n] : c[nt];
         }
-        for (int nt = 0; nt < NT; ++nt)
-            acc[nt] = kFp4 ? acc[nt] + c[nt] * scale_lds[buf][16 * nt + n] : c[nt];
-    }
 
-    const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
-    for (int nt = 0; nt < NT; ++nt) {
-        const int col = 16 * nt + n;
-        const float4v v = acc[nt] * gs;
-        if (kDown) {
-            if (mine && col < s.count)
-                *(float4v*)(a.y + (int64_t)s.pairs[col] * rows + row0 + 4 * g) = v;
-        } else {
-            // rows 0..7 of the tile (g = 0, 1) are gates, 8..15 their ups
-            float4v h;
-            for (int r = 0; r < 4; ++r) {
-                const float up = __shfl_xor(v[r], 32);
-                h[r] = v[r] / (1.0f + expf(-v[r])) * up;
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = 16 * nt + n;
+            const float4v v = acc[nt] * gs;
+            if (kDown) {
+                if (mine && col < count)
+                    *(float4v*)(a.y + (int64_t)pairs[col] * rows + row0 + 4 * g) = v;
+            } else {
+                // rows 0..7 of the tile (g = 0, 1) are gates, 8..15 their ups
+                float4v h;
+                for (int r = 0; r < 4; ++r) {
+                    const float up = __shfl_xor(v[r], 32);
+                    h[r] = v[r] / (1.0f + expf(-v[r])) * up;
+                }
+                if (mine && g < 2 && col < count)
+                    *(float4v*)(a.h + (int64_t)pairs[col] * a.inter + row0 / 2 + 4 * g) = h;
             }
-            if (mine && g < 2 && col < s.count)
-                *(float4v*)(a.h + (int64_t)s.pairs[col] * a.inter + row0 / 2 + 4 * g) = h;
         }
     }
 }
@@ -466,7 +474,10 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
     // the reached experts are few: one workgroup column per pair, where pairs
     // with an expert that an earlier token has leave at once; else per expert
     a.by_pair = tokens * a.top_k <= a.experts;
-    const int nt = tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4;
+    // columns of 16 tokens for twice an expert's share: more take another pass
+    const int64_t share = a.experts == 1 ? tokens : 2 * tokens * a.top_k / a.experts;
+    const int64_t cols = share < tokens ? share : tokens;
+    const int nt = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;
     launch_products<kFp4>(a, nt, stream);
     return launched();
 }
