@@ -163,7 +163,7 @@ __device__ int routed(const Moe& a, Group& s, int slot, int tid)
 // bytes; BF16: 16 bytes, k = 32 s + 8 g .. + 7.
 template <bool kFp4, int NT>
 struct Shape {
-    static constexpr int KC = kFp4 && NT < 4 ? 512 : 256;
+    static constexpr int KC = kFp4 && NT == 1 ? 512 : 256;
     static constexpr int kRun = kFp4 ? 128 : 32;       // k of a step
     static constexpr int S = KC / kRun;
     static constexpr int kPitch = KC + 8;              // 16-bit elements: rows 4 banks apart
@@ -172,24 +172,38 @@ struct Shape {
 template <bool kFp4, int NT>
 struct Weights {
     uint4v w[Shape<kFp4, NT>::S];
-    uint32_t sc[kFp4 ? Shape<kFp4, NT>::S : 1];
+    uint16_t sc[kFp4 ? Shape<kFp4, NT>::S : 1];
+};
+
+// All loads of the product loop are buffer loads, issued whether or not there
+// is something to load: what lies behind the summed axis or the last token
+// gets an offset out of the buffer's range, which reads as 0 without a memory
+// access. So the loop has no branch around a load, behind which the compiler
+// would have to wait for everything in flight.
+constexpr uint32_t kOutside = 0x7fffffffu;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+
+// Where a lane's part of a row tile lies, relative to the tile's first row.
+struct Tile {
+    __amdgpu_buffer_rsrc_t w, sc;
+    uint32_t w_at, sc_at;
 };
 
 template <bool kFp4, int NT>
-__device__ __forceinline__ void load_weights(Weights<kFp4, NT>& r, const uint8_t* row,
-                                             const uint8_t* scales, int k0, int K, int g)
+__device__ __forceinline__ void load_weights(Weights<kFp4, NT>& r, const Tile& t, int k0, int K, int g)
 {
     using X = Shape<kFp4, NT>;
     for (int s = 0; s < X::S; ++s) {
-        int k = k0 + X::kRun * s + (kFp4 ? 32 : 8) * g;
-        if (k >= K)
-            k = 0;          // behind the row: any weights, their right operand is 0
-        if (kFp4) {
-            r.w[s] = *(const uint4v*)(row + k / 2);
-            r.sc[s] = *(const uint16_t*)(scales + k / 16);
-        } else {
-            r.w[s] = *(const uint4v*)(row + 2 * k);
-        }
+        const int k = k0 + X::kRun * s;
+        const bool in = k + (kFp4 ? 32 : 8) * g < K;
+        r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+            t.w, in ? t.w_at + (kFp4 ? k / 2 : 2 * k) : kOutside, 0, 0));
+        if (kFp4)
+            r.sc[s] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(t.sc, in ? t.sc_at + k / 16 : kOutside, 0, 0);
     }
 }
 
@@ -206,30 +220,47 @@ struct Tokens {
     uint32_t v[R][kWords];
 };
 
+// `at`: byte offsets of the tokens that this lane loads, kOutside for none.
 template <bool kFp4, bool kDown, int NT>
-__device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, const Moe& a, const int* pairs,
-                                            int count, int k0, int K, int wave, int lane)
+__device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, __amdgpu_buffer_rsrc_t src,
+                                            const uint32_t* at, int k0, int K, int lane)
 {
     using X = Tokens<kFp4, kDown, NT>;
     const int k = k0 + 8 * (lane % X::kLanes);
-#pragma unroll
     for (int i = 0; i < X::R; ++i) {
-        const int first = (wave + 4 * i) * X::kAtOnce, col = first + lane / X::kLanes;
-        if (first >= count)
-            continue;
-        for (int w = 0; w < X::kWords; ++w)
-            r.v[i][w] = 0;
-        if (col < count && k < K) {
-            const int pair = pairs[col];
-            const uint4v* src = kDown ? (const uint4v*)(a.h + (int64_t)pair * K + k)
-                                      : (const uint4v*)(a.x + (pair / a.top_k) * a.ld_x + k);
-            for (int w = 0; w < X::kWords / 4; ++w) {
-                const uint4v u = src[w];
+        const uint32_t from = k < K && at[i] != kOutside ? at[i] + (kDown ? 4 : 2) * k : kOutside;
+        for (int w = 0; w < X::kWords / 4; ++w) {
+            const uint4v u = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(src, from, 0, 0));
+            // the second half of a run out of range is out of range by itself
+            for (int j = 0; j < 4; ++j)
+                r.v[i][4 * w + j] = u[j];
+            if (w + 1 < X::kWords / 4) {
+                const uint4v u2 = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(src, from, 16, 0));
                 for (int j = 0; j < 4; ++j)
-                    r.v[i][4 * w + j] = u[j];
+                    r.v[i][4 + j] = u2[j];
+                break;
             }
         }
     }
+}
+
+// Largest over the lanes that share a token, in all of them: within rows of 16
+// lanes by row permutations, across them by row swaps; nothing goes through
+// LDS.
+template <int kLanes>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true));     // lane ^ 1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true));     // lane ^ 2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));    // 8 mirrored
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true));    // 16 mirrored
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(a[0], a[1]);
+    if (kLanes == 64) {
+        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = max(b[0], b[1]);
+    }
+    return v;
 }
 
 // FP32 values of a run of 8.
@@ -259,9 +290,17 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
     const int row0 = blockIdx.x * 64 + 16 * wave;
     const bool mine = row0 < rows;
-    const int64_t row = (int64_t)e * rows + (mine ? row0 : 0) + n;
-    const uint8_t* w = (const uint8_t*)(kDown ? a.w2 : a.w1) + (kFp4 ? row * (K / 2) : row * K * 2);
-    const uint8_t* sc = kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr;
+    const int64_t row = (int64_t)e * rows + (mine ? row0 : 0);
+    const int pitch = kFp4 ? K / 2 : 2 * K;
+    Tile tile;
+    tile.w = buffer((const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch, 16 * pitch);
+    tile.sc = kFp4 ? buffer((kDown ? a.s2 : a.s1) + row * (K / 16), K) : tile.w;
+    tile.w_at = n * pitch + 16 * g;
+    tile.sc_at = n * (K / 16) + 2 * g;
+    // x or h: at most 2^31 bytes, checked on the host
+    const __amdgpu_buffer_rsrc_t src =
+        kDown ? buffer(a.h, (uint32_t)(a.tokens * a.top_k) * K * 4)
+              : buffer(a.x, (uint32_t)((a.tokens - 1) * a.ld_x + K) * 2);
 
     using Tok = Tokens<kFp4, kDown, NT>;
     const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
@@ -274,13 +313,23 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
         for (int nt = 0; nt < NT; ++nt)
             acc[nt] = float4v{0, 0, 0, 0};
 
-        Weights<kFp4, NT> next;
+        // Two chunks of weights are in flight: a chunk's loads go out a whole
+        // chunk before they are waited for, behind the loads of its tokens,
+        // so that staging these does not wait for weights.
+        Weights<kFp4, NT> even, odd;
         Tok tokens;
-        load_weights<kFp4, NT>(next, w, sc, 0, K, g);
-        load_tokens<kFp4, kDown, NT>(tokens, a, pairs, count, 0, K, wave, lane);
+        uint32_t at[Tok::R];
+        for (int i = 0; i < Tok::R; ++i) {
+            const int col = (wave + 4 * i) * Tok::kAtOnce + lane / Tok::kLanes;
+            at[i] = kOutside;
+            if (col < count)
+                at[i] = kDown ? pairs[col] * K * 4 : (uint32_t)(pairs[col] / a.top_k * a.ld_x * 2);
+        }
+        load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
+        load_weights<kFp4, NT>(even, tile, 0, K, g);
         if (col0 > 0)
             __syncthreads();        // the pass before may still read either buffer
-        for (int k0 = 0, buf = 0; k0 < K; k0 += X::KC, buf ^= 1) {
+        auto chunk = [&](const Weights<kFp4, NT>& now, Weights<kFp4, NT>& next, int k0, int buf) {
             // this chunk's tokens into LDS
 #pragma unroll
             for (int i = 0; i < Tok::R; ++i) {
@@ -300,8 +349,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                     uint32_t top = 0;
                     for (int j = 0; j < 8; ++j)
                         top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
-                    for (int d = 1; d < Tok::kLanes; d <<= 1)
-                        top = max(top, (uint32_t)__shfl_xor((int)top, d));
+                    top = lanes_max<Tok::kLanes>(top);
                     const int ex = fp16_exponent(top);
                     const float up = ldexpf(1.0f, ex);
                     if (at == 0)
@@ -320,11 +368,11 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                     *(uint4v*)&tok_lds[buf][kSplit ? 1 : 0][col][at] = __builtin_bit_cast(uint4v, lo);
                 }
             }
-            const Weights<kFp4, NT> now = next;
-            if (k0 + X::KC < K) {
-                load_weights<kFp4, NT>(next, w, sc, k0 + X::KC, K, g);
-                load_tokens<kFp4, kDown, NT>(tokens, a, pairs, count, k0 + X::KC, K, wave, lane);
-            }
+            load_tokens<kFp4, kDown, NT>(tokens, src, at, k0 + X::KC, K, lane);
+            load_weights<kFp4, NT>(next, tile, k0 + X::KC, K, g);
+            // no use of this chunk's weights moves in front of these loads,
+            // where it would wait for all of them
+            __builtin_amdgcn_sched_barrier(0);
             __syncthreads();
 
             float4v c[NT];
@@ -332,7 +380,9 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                 c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
             for (int st = 0; st < X::S; ++st) {
                 if (kFp4) {
-                    const half2v sv = e4m3x2(now.sc[kFp4 ? st : 0]);
+                    uint16_t pair = now.sc[kFp4 ? st : 0];
+                    asm volatile("" : "+v"(pair));      // nothing is done with it further up
+                    const half2v sv = e4m3x2(pair);
                     for (int i = 0; i < 4; ++i) {
                         const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
                         for (int nt = 0; nt < NT; ++nt)
@@ -356,6 +406,10 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
             }
             for (int nt = 0; nt < NT; ++nt)
                 acc[nt] = kFp4 ? acc[nt] + c[nt] * scale_lds[buf][16 * nt + n] : c[nt];
+        };
+        for (int k0 = 0; k0 < K; k0 += 2 * X::KC) {
+            chunk(even, odd, k0, 0);
+            chunk(odd, even, k0 + X::KC, 1);      // zeros where the chunks are odd in number
         }
 
         for (int nt = 0; nt < NT; ++nt) {
@@ -453,6 +507,9 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
     if (a.ld_x < hidden || a.ld_out < hidden || !extent_ok(tokens, a.ld_x, 2) ||
         !extent_ok(tokens, a.ld_out, 2))
         return NVFP4_ERROR_INVALID_VALUE;
+    // rows are addressed with 31-bit offsets from the first one
+    if (tokens * a.top_k * inter * 4 > INT32_MAX || (tokens - 1) * a.ld_x + hidden > INT32_MAX / 2)
+        return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     if (tokens == 0)
         return NVFP4_SUCCESS;
     if (!a.x || !a.logits || !a.w1 || !a.w2 || (kFp4 && (!a.s1 || !a.s2)) || !a.out || !a.ids ||
