@@ -169,10 +169,17 @@ struct Shape {
     static constexpr int kPitch = KC + 8;              // 16-bit elements: rows 4 banks apart
 };
 
-template <bool kFp4, int NT>
+// Scales: a lane's two bytes of each step, or (kWide, for a summed axis of whole
+// steps) 8 bytes of one step of its row, the one with the lane's group's
+// number, which are dealt to the four groups when they are used. Loaded step by
+// step, the scales of 16 rows take 16 cache lines for 8 bytes each time, which
+// are gone from the L1 when the next step wants them (one token: 39 us against
+// 28 for the first product).
+template <bool kFp4, int NT, bool kWide>
 struct Weights {
     uint4v w[Shape<kFp4, NT>::S];
-    uint16_t sc[kFp4 ? Shape<kFp4, NT>::S : 1];
+    uint16_t sc[kFp4 && !kWide ? Shape<kFp4, NT>::S : 1];
+    uint2v wide;
 };
 
 // All loads of the product loop are buffer loads, issued whether or not there
@@ -193,17 +200,51 @@ struct Tile {
     uint32_t w_at, sc_at;
 };
 
-template <bool kFp4, int NT>
-__device__ __forceinline__ void load_weights(Weights<kFp4, NT>& r, const Tile& t, int k0, int K, int g)
+template <bool kFp4, int NT, bool kWide>
+__device__ __forceinline__ void load_weights(Weights<kFp4, NT, kWide>& r, const Tile& t, int k0, int K, int g)
 {
     using X = Shape<kFp4, NT>;
+    if (kFp4 && kWide) {
+        const int k = k0 + 128 * (g & (X::S - 1));
+        r.wide = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(
+            t.sc, k < K ? t.sc_at + k / 16 : kOutside, 0, 0));
+    }
     for (int s = 0; s < X::S; ++s) {
         const int k = k0 + X::kRun * s;
         const bool in = k + (kFp4 ? 32 : 8) * g < K;
         r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
             t.w, in ? t.w_at + (kFp4 ? k / 2 : 2 * k) : kOutside, 0, 0));
-        if (kFp4)
-            r.sc[s] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(t.sc, in ? t.sc_at + k / 16 : kOutside, 0, 0);
+        if (kFp4 && !kWide)
+            r.sc[kFp4 && !kWide ? s : 0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(t.sc, in ? t.sc_at + k / 16 : kOutside, 0, 0);
+    }
+}
+
+// The two scale bytes of each step for this lane (in the low half of sc[s]).
+template <bool kFp4, int NT, bool kWide>
+__device__ __forceinline__ void deal_scales(const Weights<kFp4, NT, kWide>& r, uint32_t* sc, int g)
+{
+    if (!kWide) {
+        for (int s = 0; s < Shape<kFp4, NT>::S; ++s) {
+            uint16_t pair = r.sc[kFp4 && !kWide ? s : 0];
+            asm volatile("" : "+v"(pair));      // nothing is done with it further up
+            sc[s] = pair;
+        }
+        return;
+    }
+    uint32_t x = r.wide[0], y = r.wide[1];
+    asm volatile("" : "+v"(x), "+v"(y));
+    // group s holds step s's pairs (0, 1) in x, (2, 3) in y. Upper half of x
+    // against lower half of y: groups 0, 1 then have the pairs (0, 1) of
+    // steps 0, 1 in x and of 2, 3 in y, groups 2, 3 the pairs (2, 3). Then
+    // each row pair gets both rows of either.
+    const auto h = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    sc[0] = a[0] >> (16 * (g & 1));
+    sc[1] = a[1] >> (16 * (g & 1));
+    if (Shape<kFp4, NT>::S > 2) {
+        const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+        sc[Shape<kFp4, NT>::S > 2 ? 2 : 0] = b[0] >> (16 * (g & 1));
+        sc[Shape<kFp4, NT>::S > 2 ? 3 : 0] = b[1] >> (16 * (g & 1));
     }
 }
 
@@ -272,7 +313,7 @@ __device__ __forceinline__ void values(const uint32_t* v, float* f)
                      : __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
 }
 
-template <bool kFp4, bool kDown, int NT>
+template <bool kFp4, bool kDown, int NT, bool kWide>
 __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
 {
     using X = Shape<kFp4, NT>;
@@ -296,7 +337,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     tile.w = buffer((const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch, 16 * pitch);
     tile.sc = kFp4 ? buffer((kDown ? a.s2 : a.s1) + row * (K / 16), K) : tile.w;
     tile.w_at = n * pitch + 16 * g;
-    tile.sc_at = n * (K / 16) + 2 * g;
+    tile.sc_at = n * (K / 16) + (kWide ? 0 : 2 * g);
     // x or h: at most 2^31 bytes, checked on the host
     const __amdgpu_buffer_rsrc_t src =
         kDown ? buffer(a.h, (uint32_t)(a.tokens * a.top_k) * K * 4)
@@ -316,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
         // Two chunks of weights are in flight: a chunk's loads go out a whole
         // chunk before they are waited for, behind the loads of its tokens,
         // so that staging these does not wait for weights.
-        Weights<kFp4, NT> even, odd;
+        Weights<kFp4, NT, kWide> even, odd;
         Tok tokens;
         uint32_t at[Tok::R];
         for (int i = 0; i < Tok::R; ++i) {
@@ -326,10 +367,10 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                 at[i] = kDown ? pairs[col] * K * 4 : (uint32_t)(pairs[col] / a.top_k * a.ld_x * 2);
         }
         load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
-        load_weights<kFp4, NT>(even, tile, 0, K, g);
+        load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
         if (col0 > 0)
             __syncthreads();        // the pass before may still read either buffer
-        auto chunk = [&](const Weights<kFp4, NT>& now, Weights<kFp4, NT>& next, int k0, int buf) {
+        auto chunk = [&](const Weights<kFp4, NT, kWide>& now, Weights<kFp4, NT, kWide>& next, int k0, int buf) {
             // this chunk's tokens into LDS
 #pragma unroll
             for (int i = 0; i < Tok::R; ++i) {
@@ -369,7 +410,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                 }
             }
             load_tokens<kFp4, kDown, NT>(tokens, src, at, k0 + X::KC, K, lane);
-            load_weights<kFp4, NT>(next, tile, k0 + X::KC, K, g);
+            load_weights<kFp4, NT, kWide>(next, tile, k0 + X::KC, K, g);
             // no use of this chunk's weights moves in front of these loads,
             // where it would wait for all of them
             __builtin_amdgcn_sched_barrier(0);
@@ -378,11 +419,12 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
             float4v c[NT];
             for (int nt = 0; nt < NT; ++nt)
                 c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
+            uint32_t pair[X::S];
+            if (kFp4)
+                deal_scales<kFp4, NT, kWide>(now, pair, g);
             for (int st = 0; st < X::S; ++st) {
                 if (kFp4) {
-                    uint16_t pair = now.sc[kFp4 ? st : 0];
-                    asm volatile("" : "+v"(pair));      // nothing is done with it further up
-                    const half2v sv = e4m3x2(pair);
+                    const half2v sv = e4m3x2(pair[st]);
                     for (int i = 0; i < 4; ++i) {
                         const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
                         for (int nt = 0; nt < NT; ++nt)
@@ -472,17 +514,24 @@ nvfp4_status_t check_sizes(int64_t tokens, int64_t hidden, int64_t inter, int32_
     return NVFP4_SUCCESS;
 }
 
+template <bool kFp4, bool kDown, int NT>
+void launch_product(const Moe& a, hipStream_t stream)
+{
+    const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
+    const dim3 grid(serving::ceil_div(rows, 64), a.by_pair ? a.tokens * a.top_k : a.experts);
+    if (kFp4 && K % 128 == 0 && serving::aligned(kDown ? a.s2 : a.s1, 8))
+        hipLaunchKernelGGL((moe_product_kernel<kFp4, kDown, NT, kFp4>), grid, dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((moe_product_kernel<kFp4, kDown, NT, false>), grid, dim3(kThreads), 0, stream, a);
+}
+
 template <bool kFp4, int NT>
 void launch_both(const Moe& a, hipStream_t stream)
 {
-    using serving::ceil_div;
-    const unsigned slots = (unsigned)(a.by_pair ? a.tokens * a.top_k : a.experts);
-    hipLaunchKernelGGL((moe_product_kernel<kFp4, false, NT>), dim3(ceil_div(2 * a.inter, 64), slots),
+    launch_product<kFp4, false, NT>(a, stream);
+    launch_product<kFp4, true, NT>(a, stream);
+    hipLaunchKernelGGL(moe_sum_kernel, dim3(serving::ceil_div(a.hidden, 4 * kThreads), a.tokens),
                        dim3(kThreads), 0, stream, a);
-    hipLaunchKernelGGL((moe_product_kernel<kFp4, true, NT>), dim3(ceil_div(a.hidden, 64), slots),
-                       dim3(kThreads), 0, stream, a);
-    hipLaunchKernelGGL(moe_sum_kernel, dim3(ceil_div(a.hidden, 4 * kThreads), a.tokens), dim3(kThreads),
-                       0, stream, a);
 }
 
 template <bool kFp4>
