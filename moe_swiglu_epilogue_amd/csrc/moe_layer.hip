@@ -187,19 +187,23 @@ struct Weights {
 // gets an offset out of the buffer's range, which reads as 0 without a memory
 // access. So the loop has no branch around a load, behind which the compiler
 // would have to wait for everything in flight.
-constexpr uint32_t kOutside = 0x7fffffffu;
+constexpr uint32_t kOutside = 0x7fffff00u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
 
-// Where a lane's part of a row tile lies, relative to the tile's first row.
+// A row tile's weights and scales, and where a lane's part of them lies,
+// relative to the tile's first row.
 struct Tile {
-    __amdgpu_buffer_rsrc_t w, sc;
-    uint32_t w_at, sc_at;
+    const uint8_t *w, *sc;
+    uint32_t w_bytes, sc_bytes, w_at, sc_at;
 };
 
+// kWide (and BF16, whose steps are 32 long): a step lies before or behind the
+// end of the axis as a whole, so that the scalar unit alone handles it, with a
+// buffer of no bytes; a lane's offsets never change.
 template <bool kFp4, int NT, bool kWide>
 __device__ __forceinline__ void load_weights(Weights<kFp4, NT, kWide>& r, const Tile& t, int k0, int K, int g)
 {
@@ -207,15 +211,20 @@ __device__ __forceinline__ void load_weights(Weights<kFp4, NT, kWide>& r, const 
     if (kFp4 && kWide) {
         const int k = k0 + 128 * (g & (X::S - 1));
         r.wide = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(
-            t.sc, k < K ? t.sc_at + k / 16 : kOutside, 0, 0));
+            buffer(t.sc, t.sc_bytes), k < K ? t.sc_at : kOutside, k0 / 16, 0));
     }
     for (int s = 0; s < X::S; ++s) {
         const int k = k0 + X::kRun * s;
-        const bool in = k + (kFp4 ? 32 : 8) * g < K;
-        r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-            t.w, in ? t.w_at + (kFp4 ? k / 2 : 2 * k) : kOutside, 0, 0));
-        if (kFp4 && !kWide)
-            r.sc[kFp4 && !kWide ? s : 0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(t.sc, in ? t.sc_at + k / 16 : kOutside, 0, 0);
+        if (kWide || !kFp4) {
+            r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+                buffer(t.w, k < K ? t.w_bytes : 0), t.w_at, kFp4 ? k / 2 : 2 * k, 0));
+        } else {
+            const bool in = k + 32 * g < K;
+            r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+                buffer(t.w, t.w_bytes), in ? t.w_at : kOutside, k / 2, 0));
+            r.sc[kFp4 && !kWide ? s : 0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+                buffer(t.sc, t.sc_bytes), in ? t.sc_at : kOutside, k / 16, 0);
+        }
     }
 }
 
@@ -261,28 +270,20 @@ struct Tokens {
     uint32_t v[R][kWords];
 };
 
-// `at`: byte offsets of the tokens that this lane loads, kOutside for none.
+// `at`: byte offsets of this lane's part of its tokens, kOutside for none.
 template <bool kFp4, bool kDown, int NT>
 __device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, __amdgpu_buffer_rsrc_t src,
                                             const uint32_t* at, int k0, int K, int lane)
 {
     using X = Tokens<kFp4, kDown, NT>;
-    const int k = k0 + 8 * (lane % X::kLanes);
-    for (int i = 0; i < X::R; ++i) {
-        const uint32_t from = k < K && at[i] != kOutside ? at[i] + (kDown ? 4 : 2) * k : kOutside;
+    const bool in = k0 + 8 * (lane % X::kLanes) < K;
+    for (int i = 0; i < X::R; ++i)
         for (int w = 0; w < X::kWords / 4; ++w) {
-            const uint4v u = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(src, from, 0, 0));
-            // the second half of a run out of range is out of range by itself
+            const uint4v u = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
+                src, (in ? at[i] : kOutside) + 16 * w, k0 * (kDown ? 4 : 2), 0));
             for (int j = 0; j < 4; ++j)
                 r.v[i][4 * w + j] = u[j];
-            if (w + 1 < X::kWords / 4) {
-                const uint4v u2 = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(src, from, 16, 0));
-                for (int j = 0; j < 4; ++j)
-                    r.v[i][4 + j] = u2[j];
-                break;
-            }
         }
-    }
 }
 
 // Largest over the lanes that share a token, in all of them: within rows of 16
@@ -333,11 +334,10 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     const bool mine = row0 < rows;
     const int64_t row = (int64_t)e * rows + (mine ? row0 : 0);
     const int pitch = kFp4 ? K / 2 : 2 * K;
-    Tile tile;
-    tile.w = buffer((const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch, 16 * pitch);
-    tile.sc = kFp4 ? buffer((kDown ? a.s2 : a.s1) + row * (K / 16), K) : tile.w;
-    tile.w_at = n * pitch + 16 * g;
-    tile.sc_at = n * (K / 16) + (kWide ? 0 : 2 * g);
+    const Tile tile = {(const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch,
+                       kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr, 16u * pitch, (uint32_t)K,
+                       (uint32_t)(n * pitch + 16 * g),
+                       (uint32_t)(n * (K / 16) + (kWide ? 8 * (g & (X::S - 1)) : 2 * g))};
     // x or h: at most 2^31 bytes, checked on the host
     const __amdgpu_buffer_rsrc_t src =
         kDown ? buffer(a.h, (uint32_t)(a.tokens * a.top_k) * K * 4)
@@ -364,7 +364,8 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
             const int col = (wave + 4 * i) * Tok::kAtOnce + lane / Tok::kLanes;
             at[i] = kOutside;
             if (col < count)
-                at[i] = kDown ? pairs[col] * K * 4 : (uint32_t)(pairs[col] / a.top_k * a.ld_x * 2);
+                at[i] = (kDown ? pairs[col] * K * 4 : (uint32_t)(pairs[col] / a.top_k * a.ld_x * 2)) +
+                        (lane % Tok::kLanes) * (kDown ? 32 : 16);
         }
         load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
         load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
@@ -557,7 +558,8 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
         !extent_ok(tokens, a.ld_out, 2))
         return NVFP4_ERROR_INVALID_VALUE;
     // rows are addressed with 31-bit offsets from the first one
-    if (tokens * a.top_k * inter * 4 > INT32_MAX || (tokens - 1) * a.ld_x + hidden > INT32_MAX / 2)
+    const int64_t most = INT32_MAX - 4096;
+    if (tokens * a.top_k * inter * 4 > most || (tokens - 1) * a.ld_x + hidden > most / 2)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     if (tokens == 0)
         return NVFP4_SUCCESS;
