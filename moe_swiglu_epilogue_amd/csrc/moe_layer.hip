@@ -31,7 +31,6 @@ struct Moe {
     float* weights;
     float* h;          // workspace: [tokens * top_k][inter]
     float* y;          // workspace: [tokens * top_k][hidden]
-    float* p;          // workspace: [tokens * top_k] probabilities
     int64_t ld_x, ld_out;
     int tokens, hidden, inter, experts, top_k, renormalize;
     int by_pair;       // workgroups go by (token, rank) pairs, not by experts
@@ -44,117 +43,92 @@ __device__ __forceinline__ float logit(const Moe& a, int t, int e)
     return v == v ? v : -INFINITY;
 }
 
-// How many experts stand before expert e (with logit v) for token t; by a wave.
-__device__ __forceinline__ int rank_of(const Moe& a, int t, int e, float v, int lane)
-{
-    int rank = 0;
-    for (int f0 = 0; f0 < a.experts; f0 += 64) {
-        const int f = f0 + lane;
-        bool before = false;
-        if (f < a.experts) {
-            const float u = logit(a, t, f);
-            before = u > v || (u == v && f < e);
-        }
-        rank += __popcll(__ballot(before));
-    }
-    return rank;
-}
-
-// softmax(logits[t])[e]; by a wave.
-__device__ __forceinline__ float probability(const Moe& a, int t, float v, int lane)
-{
-    float top = -INFINITY, sum = 0;
-    for (int f = lane; f < a.experts; f += 64)
-        top = fmaxf(top, logit(a, t, f));
-    for (int d = 32; d; d >>= 1)
-        top = fmaxf(top, __shfl_xor(top, d));
-    for (int f = lane; f < a.experts; f += 64) {
-        const float u = logit(a, t, f);
-        sum += u == top ? 1.0f : expf(u - top);       // +inf - +inf would be NaN
-    }
-    for (int d = 32; d; d >>= 1)
-        sum += __shfl_xor(sum, d);
-    return (v == top ? 1.0f : expf(v - top)) / sum;
-}
-
-// The expert of this workgroup and the pairs (token * top_k + rank) routed to
-// it, in the order of the tokens: `count` of them in pairs[]. Returns -1 when
-// there is none, or when another workgroup has this expert.
+// The pairs (token * top_k + rank) routed to a workgroup's expert, in the order
+// of the tokens.
 struct Group {
     int pairs[kMaxTokens];
-    int rank[kMaxTokens];
-    int expert, count;
+    int count, expert;
+    int part[kThreads / 64][kMaxTokens];
     float row[kMaxExperts];
 };
 
-// From the logits; workgroups of slice 0 also write ids and probabilities.
-__device__ int route(const Moe& a, Group& s, int slot, bool write, int tid)
+// The expert with rank slot % top_k for token slot / top_k: four lanes an
+// expert count the logits in front of its own.
+__device__ int expert_of_pair(const Moe& a, Group& s, int slot, int tid)
+{
+    const int t = slot / a.top_k, k = slot % a.top_k;
+    for (int f = tid; f < a.experts; f += kThreads)
+        s.row[f] = logit(a, t, f);
+    __syncthreads();
+    for (int f = tid >> 2; f < a.experts; f += kThreads / 4) {
+        const float v = s.row[f];
+        int rank = 0;
+#pragma unroll 4
+        for (int u = tid & 3; u < a.experts; u += 4) {
+            const float w = s.row[u];
+            rank += w > v || (w == v && u < f);
+        }
+        rank += __shfl_xor(rank, 1);
+        rank += __shfl_xor(rank, 2);
+        if (rank == k)
+            s.expert = f;
+    }
+    __syncthreads();
+    return s.expert;
+}
+
+// Collects the tokens that the lanes of wave 0 report (lane = token).
+__device__ __forceinline__ void collect(const Moe& a, Group& s, bool in, int rank, int lane)
+{
+    const uint64_t all = __ballot(in);
+    if (in)
+        s.pairs[__popcll(all & ((1ull << lane) - 1))] = lane * a.top_k + rank;
+    if (lane == 0)
+        s.count = __popcll(all);
+}
+
+// The pairs of expert e from the logits: lane = token, each wave counts a
+// quarter of the experts. A workgroup told to also writes the ids of its
+// expert (of its own pair alone, where it goes by pairs).
+__device__ void route(const Moe& a, Group& s, int slot, int e, bool write, int tid)
 {
     const int lane = tid & 63, wave = tid >> 6;
-    int e = slot;
-    if (a.by_pair) {
-        const int t = slot / a.top_k, k = slot % a.top_k;
-        for (int f = tid; f < a.experts; f += kThreads)
-            s.row[f] = logit(a, t, f);
-        __syncthreads();
-        for (int f = tid; f < a.experts; f += kThreads) {
-            const float v = s.row[f];
-            int rank = 0;
-            for (int u = 0; u < a.experts; ++u)
-                rank += s.row[u] > v || (s.row[u] == v && u < f);
-            if (rank == k)
-                s.expert = f;
+    const float v = lane < a.tokens ? logit(a, lane, e) : -INFINITY;
+    int rank = 0;
+    if (lane < a.tokens) {
+        const int quarter = (a.experts + 3) / 4, last = min(a.experts, (wave + 1) * quarter);
+#pragma unroll 8
+        for (int f = wave * quarter; f < last; ++f) {
+            const float u = logit(a, lane, f);
+            rank += u > v || (u == v && f < e);
         }
-        __syncthreads();
-        e = s.expert;
     }
-    for (int t = wave; t < a.tokens; t += kThreads / 64) {
-        const float v = logit(a, t, e);
-        int rank = rank_of(a, t, e, v, lane);
-        const bool here = rank < a.top_k && (!a.by_pair || t * a.top_k + rank == slot);
-        if (write && here) {
-            const float p = v == -INFINITY ? 0.0f : probability(a, t, v, lane);
-            if (lane == 0) {
-                a.ids[t * a.top_k + rank] = v == -INFINITY ? -1 : e;
-                a.p[t * a.top_k + rank] = p;
-            }
-        }
-        if (lane == 0)
-            s.rank[t] = v == -INFINITY ? kMaxTopK : rank;
-    }
+    s.part[wave][lane] = rank;
     __syncthreads();
     if (wave == 0) {
-        const bool in = lane < a.tokens && s.rank[lane] < a.top_k;
-        const uint64_t all = __ballot(in);
-        if (in)
-            s.pairs[__popcll(all & ((1ull << lane) - 1))] = lane * a.top_k + s.rank[lane];
-        if (lane == 0)
-            s.count = __popcll(all);
+        rank = s.part[0][lane] + s.part[1][lane] + s.part[2][lane] + s.part[3][lane];
+        const bool in = lane < a.tokens && rank < a.top_k;
+        if (write && in && (!a.by_pair || lane * a.top_k + rank == slot))
+            a.ids[lane * a.top_k + rank] = v == -INFINITY ? -1 : e;
+        collect(a, s, in && v != -INFINITY, rank, lane);
     }
     __syncthreads();
-    return s.count == 0 || (a.by_pair && s.pairs[0] != slot) ? -1 : e;
 }
 
 // The same from the ids that the first kernel wrote.
-__device__ int routed(const Moe& a, Group& s, int slot, int tid)
+__device__ void routed(const Moe& a, Group& s, int e, int tid)
 {
-    const int lane = tid & 63, wave = tid >> 6;
-    const int e = a.by_pair ? a.ids[slot] : slot;
-    if (wave == 0) {
+    const int lane = tid & 63;
+    if (tid < 64) {
         int rank = kMaxTopK;
         if (lane < a.tokens)
+#pragma unroll 8
             for (int k = 0; k < a.top_k; ++k)
                 if (a.ids[lane * a.top_k + k] == e)
                     rank = k;
-        const bool in = e >= 0 && rank < a.top_k;
-        const uint64_t all = __ballot(in);
-        if (in)
-            s.pairs[__popcll(all & ((1ull << lane) - 1))] = lane * a.top_k + rank;
-        if (lane == 0)
-            s.count = __popcll(all);
+        collect(a, s, e >= 0 && rank < a.top_k, rank, lane);
     }
     __syncthreads();
-    return s.count == 0 || (a.by_pair && s.pairs[0] != slot) ? -1 : e;
 }
 
 // Chunk of the summed axis that is staged at a time, and what a lane holds of
@@ -325,14 +299,12 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int e = kDown ? routed(a, s, blockIdx.y, tid)
-                        : route(a, s, blockIdx.y, blockIdx.x == 0, tid);
-    if (e < 0)
-        return;
+    const int slot = blockIdx.y;
+    const int e = !a.by_pair ? slot : kDown ? a.ids[slot] : expert_of_pair(a, s, slot, tid);
     const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
     const int row0 = blockIdx.x * 64 + 16 * wave;
     const bool mine = row0 < rows;
-    const int64_t row = (int64_t)e * rows + (mine ? row0 : 0);
+    const int64_t row = (int64_t)max(e, 0) * rows + (mine ? row0 : 0);
     const int pitch = kFp4 ? K / 2 : 2 * K;
     const Tile tile = {(const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch,
                        kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr, 16u * pitch, (uint32_t)K,
@@ -346,6 +318,20 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     using Tok = Tokens<kFp4, kDown, NT>;
     const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
 
+    // Two chunks of weights are in flight: a chunk's loads go out a whole chunk
+    // before they are waited for, behind the loads of its tokens, so that
+    // staging these does not wait for weights. The first go out before the
+    // tokens are known.
+    Weights<kFp4, NT, kWide> even, odd;
+    load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
+    if (kDown)
+        routed(a, s, e, tid);
+    else
+        route(a, s, slot, e, blockIdx.x == 0, tid);
+    // no token is here, or an earlier token's workgroup has this expert
+    if (s.count == 0 || (a.by_pair && s.pairs[0] != slot))
+        return;
+
     // Tokens beyond 16 NT take another pass over the weights.
     for (int col0 = 0; col0 < s.count; col0 += 16 * NT) {
         const int* pairs = s.pairs + col0;
@@ -354,10 +340,6 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
         for (int nt = 0; nt < NT; ++nt)
             acc[nt] = float4v{0, 0, 0, 0};
 
-        // Two chunks of weights are in flight: a chunk's loads go out a whole
-        // chunk before they are waited for, behind the loads of its tokens,
-        // so that staging these does not wait for weights.
-        Weights<kFp4, NT, kWide> even, odd;
         Tok tokens;
         uint32_t at[Tok::R];
         for (int i = 0; i < Tok::R; ++i) {
@@ -368,9 +350,10 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                         (lane % Tok::kLanes) * (kDown ? 32 : 16);
         }
         load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
-        load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
-        if (col0 > 0)
+        if (col0 > 0) {
+            load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
             __syncthreads();        // the pass before may still read either buffer
+        }
         auto chunk = [&](const Weights<kFp4, NT, kWide>& now, Weights<kFp4, NT, kWide>& next, int k0, int buf) {
             // this chunk's tokens into LDS
 #pragma unroll
@@ -475,33 +458,58 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
     }
 }
 
-// out[t] = sum_k w[t][k] y[t][k], in the order of k; the first workgroup of a
-// token also writes its weights.
+// out[t] = sum_k w[t][k] y[t][k], in the order of k, for a token and 1024
+// columns; the first workgroup of a token also writes its weights.
 __global__ __launch_bounds__(kThreads) void moe_sum_kernel(Moe a)
 {
-    __shared__ float w[kMaxTopK];
-    const int t = blockIdx.y, tid = threadIdx.x;
-    if (tid < 64) {
-        const int k = tid;
-        const float p = k < a.top_k ? a.p[t * a.top_k + k] : 0.0f;
-        float total = p;
-        for (int d = 32; d; d >>= 1)
-            total += __shfl_xor(total, d);
-        if (k < a.top_k) {
-            w[k] = a.renormalize && total > 0 ? p / total : p;
-            if (blockIdx.x == 0)
-                a.weights[t * a.top_k + k] = w[k];
+    __shared__ float w[kMaxTopK], wave_sum[kThreads / 64];
+    __shared__ int id[kMaxTopK];
+    const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int n = (blockIdx.x * kThreads + tid) * 4;
+    const float* y = a.y + (int64_t)t * a.top_k * a.hidden + min(n, a.hidden - 4);
+    float4v v[8];       // a row that no expert wrote is loaded, not added
+    for (int k = 0; k < 8; ++k)
+        v[k] = *(const float4v*)(y + (int64_t)min(k, a.top_k - 1) * a.hidden);
+
+    // The first choice has the largest logit. An infinite one would make
+    // inf - inf: equal logits are compared, not subtracted.
+    const int mine = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
+    const float l = mine >= 0 ? logit(a, t, mine) : -INFINITY;
+    const float top = __shfl(l, 0);
+    const float p = mine < 0 ? 0.0f : l == top ? 1.0f : expf(l - top);
+    float sum = 0;
+    if (a.renormalize) {
+        sum = p;
+    } else {
+        for (int f = tid; f < a.experts; f += kThreads) {
+            const float u = logit(a, t, f);
+            sum += u == -INFINITY ? 0.0f : u == top ? 1.0f : expf(u - top);
         }
     }
+    for (int d = 32; d; d >>= 1)
+        sum += __shfl_xor(sum, d);
+    if (lane == 0)
+        wave_sum[tid >> 6] = sum;
     __syncthreads();
-    const int n = (blockIdx.x * kThreads + tid) * 4;
-    if (n < a.hidden) {
-        float4v v = {0, 0, 0, 0};
-        for (int k = 0; k < a.top_k; ++k)
-            if (a.ids[t * a.top_k + k] >= 0)
-                v += w[k] * *(const float4v*)(a.y + (int64_t)(t * a.top_k + k) * a.hidden + n);
-        *(uint2v*)(a.out + t * a.ld_out + n) = uint2v{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+    if (!a.renormalize)
+        sum = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+    if (tid < a.top_k) {
+        w[tid] = mine < 0 ? 0.0f : p / sum;
+        id[tid] = mine;
+        if (blockIdx.x == 0)
+            a.weights[t * a.top_k + tid] = w[tid];
     }
+    __syncthreads();
+    if (n >= a.hidden)
+        return;
+    float4v o = {0, 0, 0, 0};
+    for (int k = 0; k < 8; ++k)
+        if (k < a.top_k && id[k] >= 0)
+            o += w[k] * v[k];
+    for (int k = 8; k < a.top_k; ++k)
+        if (id[k] >= 0)
+            o += w[k] * *(const float4v*)(y + (int64_t)k * a.hidden);
+    *(uint2v*)(a.out + t * a.ld_out + n) = uint2v{bf16x2(o[0], o[1]), bf16x2(o[2], o[3])};
 }
 
 nvfp4_status_t check_sizes(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts,
@@ -578,7 +586,6 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
     a.inter = (int)inter;
     a.h = (float*)workspace;
     a.y = a.h + tokens * a.top_k * inter;
-    a.p = a.y + tokens * a.top_k * hidden;
     // the reached experts are few: one workgroup column per pair, where pairs
     // with an expert that an earlier token has leave at once; else per expert
     a.by_pair = tokens * a.top_k <= a.experts;
@@ -597,7 +604,7 @@ extern "C" int64_t moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t i
 {
     if (check_sizes(tokens, hidden, inter, num_experts, top_k) != NVFP4_SUCCESS)
         return -1;
-    return tokens * top_k * (inter + hidden + 1) * 4;
+    return tokens * top_k * (inter + hidden) * 4;
 }
 
 extern "C" nvfp4_status_t moe_layer_nvfp4(
@@ -608,7 +615,7 @@ extern "C" nvfp4_status_t moe_layer_nvfp4(
     void* workspace, int64_t workspace_bytes, hipStream_t stream)
 {
     Moe a = {x, logits, w1_packed, w2_packed, w1_scales, w2_scales, gs1, gs2, out, topk_ids,
-             topk_weights, nullptr, nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
+             topk_weights, nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
     return run<true>(a, hidden, inter, workspace_bytes, tokens, workspace, stream);
 }
 
@@ -621,6 +628,6 @@ extern "C" nvfp4_status_t moe_layer_bf16(const uint16_t* x, int64_t tokens, int6
                                          int64_t workspace_bytes, hipStream_t stream)
 {
     Moe a = {x, logits, w1, w2, nullptr, nullptr, nullptr, nullptr, out, topk_ids, topk_weights,
-             nullptr, nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
+             nullptr, nullptr, ld_x, ld_out, 0, 0, 0, num_experts, top_k, renormalize};
     return run<false>(a, hidden, inter, workspace_bytes, tokens, workspace, stream);
 }
