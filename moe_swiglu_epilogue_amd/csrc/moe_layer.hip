@@ -131,13 +131,19 @@ __device__ void routed(const Moe& a, Group& s, int e, int tid)
     __syncthreads();
 }
 
-// Chunk of the summed axis that is staged at a time, and what a lane holds of
-// a 16-row weight tile for it. Lane (g = lane / 16, n = lane % 16) holds row
-// n; NVFP4: step s is 16 bytes, k = 128 s + 32 g .. + 31, with two scale
-// bytes; BF16: 16 bytes, k = 32 s + 8 g .. + 7.
-template <bool kFp4, int NT>
+// Chunk of the summed axis that is staged at a time, and what a lane (g = lane /
+// 16, n = lane % 16) feeds the matrix instructions of a 16-row weight tile:
+// row n; NVFP4: step s is 16 bytes, k = 128 s + 32 g .. + 31, with two scale
+// bytes; BF16: 16 bytes, k = 32 s + 8 g .. + 7. The loads are made by lane 4 n +
+// g instead, so that four neighbouring lanes read 64 bytes of one row, and
+// handed over in registers: loaded by the lane that needs them, neighbouring
+// lanes read 16 different rows and every load takes the L1 64 accesses for 16
+// (32 tokens: 218 and 128 us against 199 and 116 for the two products).
+template <bool kFp4, bool kDown, int NT>
 struct Shape {
-    static constexpr int KC = kFp4 && NT == 1 ? 512 : 256;
+    // the longer axis of the first product takes the longer chunk (one token:
+    // 28 us with 512, 32 with 256; second product 18 and 16)
+    static constexpr int KC = kFp4 && NT == 1 && !kDown ? 512 : 256;
     static constexpr int kRun = kFp4 ? 128 : 32;       // k of a step
     static constexpr int S = KC / kRun;
     static constexpr int kPitch = KC + 8;              // 16-bit elements: rows 4 banks apart
@@ -149,10 +155,10 @@ struct Shape {
 // step, the scales of 16 rows take 16 cache lines for 8 bytes each time, which
 // are gone from the L1 when the next step wants them (one token: 39 us against
 // 28 for the first product).
-template <bool kFp4, int NT, bool kWide>
+template <bool kFp4, bool kDown, int NT, bool kWide>
 struct Weights {
-    uint4v w[Shape<kFp4, NT>::S];
-    uint16_t sc[kFp4 && !kWide ? Shape<kFp4, NT>::S : 1];
+    uint4v w[Shape<kFp4, kDown, NT>::S];
+    uint16_t sc[kFp4 && !kWide ? Shape<kFp4, kDown, NT>::S : 1];
     uint2v wide;
 };
 
@@ -178,10 +184,10 @@ struct Tile {
 // kWide (and BF16, whose steps are 32 long): a step lies before or behind the
 // end of the axis as a whole, so that the scalar unit alone handles it, with a
 // buffer of no bytes; a lane's offsets never change.
-template <bool kFp4, int NT, bool kWide>
-__device__ __forceinline__ void load_weights(Weights<kFp4, NT, kWide>& r, const Tile& t, int k0, int K, int g)
+template <bool kFp4, bool kDown, int NT, bool kWide>
+__device__ __forceinline__ void load_weights(Weights<kFp4, kDown, NT, kWide>& r, const Tile& t, int k0, int K, int g)
 {
-    using X = Shape<kFp4, NT>;
+    using X = Shape<kFp4, kDown, NT>;
     if (kFp4 && kWide) {
         const int k = k0 + 128 * (g & (X::S - 1));
         r.wide = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(
@@ -202,20 +208,34 @@ __device__ __forceinline__ void load_weights(Weights<kFp4, NT, kWide>& r, const 
     }
 }
 
+// What lane 4 n + g loaded, in lane 16 g + n. The asm keeps the compiler from
+// moving the exchange in front of later loads, where it would wait for them.
+__device__ __forceinline__ uint32_t handed(uint32_t v, int from)
+{
+    asm volatile("" : "+v"(v));
+    return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v);
+}
+
+__device__ __forceinline__ uint4v handed(uint4v v, int from)
+{
+    for (int i = 0; i < 4; ++i)
+        v[i] = handed(v[i], from);
+    return v;
+}
+
 // The two scale bytes of each step for this lane (in the low half of sc[s]).
-template <bool kFp4, int NT, bool kWide>
-__device__ __forceinline__ void deal_scales(const Weights<kFp4, NT, kWide>& r, uint32_t* sc, int g)
+template <bool kFp4, bool kDown, int NT, bool kWide>
+__device__ __forceinline__ void deal_scales(const Weights<kFp4, kDown, NT, kWide>& r, uint32_t* sc, int g, int from)
 {
     if (!kWide) {
-        for (int s = 0; s < Shape<kFp4, NT>::S; ++s) {
+        for (int s = 0; s < Shape<kFp4, kDown, NT>::S; ++s) {
             uint16_t pair = r.sc[kFp4 && !kWide ? s : 0];
-            asm volatile("" : "+v"(pair));      // nothing is done with it further up
-            sc[s] = pair;
+            asm volatile("" : "+v"(pair));
+            sc[s] = handed((uint32_t)pair, from);
         }
         return;
     }
-    uint32_t x = r.wide[0], y = r.wide[1];
-    asm volatile("" : "+v"(x), "+v"(y));
+    const uint32_t x = handed(r.wide[0], from), y = handed(r.wide[1], from);
     // group s holds step s's pairs (0, 1) in x, (2, 3) in y. Upper half of x
     // against lower half of y: groups 0, 1 then have the pairs (0, 1) of
     // steps 0, 1 in x and of 2, 3 in y, groups 2, 3 the pairs (2, 3). Then
@@ -224,10 +244,10 @@ __device__ __forceinline__ void deal_scales(const Weights<kFp4, NT, kWide>& r, u
     const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
     sc[0] = a[0] >> (16 * (g & 1));
     sc[1] = a[1] >> (16 * (g & 1));
-    if (Shape<kFp4, NT>::S > 2) {
+    if (Shape<kFp4, kDown, NT>::S > 2) {
         const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-        sc[Shape<kFp4, NT>::S > 2 ? 2 : 0] = b[0] >> (16 * (g & 1));
-        sc[Shape<kFp4, NT>::S > 2 ? 3 : 0] = b[1] >> (16 * (g & 1));
+        sc[Shape<kFp4, kDown, NT>::S > 2 ? 2 : 0] = b[0] >> (16 * (g & 1));
+        sc[Shape<kFp4, kDown, NT>::S > 2 ? 3 : 0] = b[1] >> (16 * (g & 1));
     }
 }
 
@@ -237,7 +257,7 @@ __device__ __forceinline__ void deal_scales(const Weights<kFp4, NT, kWide>& r, u
 // reads.
 template <bool kFp4, bool kDown, int NT>
 struct Tokens {
-    static constexpr int kLanes = Shape<kFp4, NT>::KC / 8;
+    static constexpr int kLanes = Shape<kFp4, kDown, NT>::KC / 8;
     static constexpr int kAtOnce = 64 / kLanes;
     static constexpr int R = 4 * NT / kAtOnce;              // turns of a wave
     static constexpr int kWords = kDown ? 8 : 4;            // FP32 h or BF16 x
@@ -291,7 +311,7 @@ __device__ __forceinline__ void values(const uint32_t* v, float* f)
 template <bool kFp4, bool kDown, int NT, bool kWide>
 __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
 {
-    using X = Shape<kFp4, NT>;
+    using X = Shape<kFp4, kDown, NT>;
     constexpr bool kSplit = !kFp4 && kDown;      // h as a sum of two BF16 numbers
     __shared__ Group s;
     __shared__ __attribute__((aligned(16))) uint16_t tok_lds[2][kSplit ? 2 : 1][16 * NT][X::kPitch];
@@ -299,31 +319,31 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int from = 4 * (4 * n + g);
     const int slot = blockIdx.y;
+    // (a pair without an expert, id -1, finds no token below and leaves)
     const int e = !a.by_pair ? slot : kDown ? a.ids[slot] : expert_of_pair(a, s, slot, tid);
+    const int expert = max(e, 0);
     const int rows = kDown ? a.hidden : 2 * a.inter, K = kDown ? a.inter : a.hidden;
     const int row0 = blockIdx.x * 64 + 16 * wave;
     const bool mine = row0 < rows;
-    const int64_t row = (int64_t)max(e, 0) * rows + (mine ? row0 : 0);
+    const int64_t row = (int64_t)expert * rows + (mine ? row0 : 0);
     const int pitch = kFp4 ? K / 2 : 2 * K;
     const Tile tile = {(const uint8_t*)(kDown ? a.w2 : a.w1) + row * pitch,
                        kFp4 ? (kDown ? a.s2 : a.s1) + row * (K / 16) : nullptr, 16u * pitch, (uint32_t)K,
-                       (uint32_t)(n * pitch + 16 * g),
-                       (uint32_t)(n * (K / 16) + (kWide ? 8 * (g & (X::S - 1)) : 2 * g))};
+                       (uint32_t)((lane >> 2) * pitch + 16 * (lane & 3)),
+                       (uint32_t)((lane >> 2) * (K / 16) + (kWide ? 8 * (lane & 3 & (X::S - 1)) : 2 * (lane & 3)))};
     // x or h: at most 2^31 bytes, checked on the host
     const __amdgpu_buffer_rsrc_t src =
         kDown ? buffer(a.h, (uint32_t)(a.tokens * a.top_k) * K * 4)
               : buffer(a.x, (uint32_t)((a.tokens - 1) * a.ld_x + K) * 2);
 
     using Tok = Tokens<kFp4, kDown, NT>;
-    const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[e] : 1.0f) : (a.gs1 ? a.gs1[e] : 1.0f);
+    const float gs = !kFp4 ? 1.0f : kDown ? (a.gs2 ? a.gs2[expert] : 1.0f) : (a.gs1 ? a.gs1[expert] : 1.0f);
 
-    // Two chunks of weights are in flight: a chunk's loads go out a whole chunk
-    // before they are waited for, behind the loads of its tokens, so that
-    // staging these does not wait for weights. The first go out before the
-    // tokens are known.
-    Weights<kFp4, NT, kWide> even, odd;
-    load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
+    // the first weights are requested before the tokens are known
+    Weights<kFp4, kDown, NT, kWide> even, odd;
+    load_weights<kFp4, kDown, NT, kWide>(even, tile, 0, K, lane & 3);
     if (kDown)
         routed(a, s, e, tid);
     else
@@ -349,13 +369,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                 at[i] = (kDown ? pairs[col] * K * 4 : (uint32_t)(pairs[col] / a.top_k * a.ld_x * 2)) +
                         (lane % Tok::kLanes) * (kDown ? 32 : 16);
         }
-        load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
-        if (col0 > 0) {
-            load_weights<kFp4, NT, kWide>(even, tile, 0, K, g);
-            __syncthreads();        // the pass before may still read either buffer
-        }
-        auto chunk = [&](const Weights<kFp4, NT, kWide>& now, Weights<kFp4, NT, kWide>& next, int k0, int buf) {
-            // this chunk's tokens into LDS
+        auto stage = [&](int buf) {
 #pragma unroll
             for (int i = 0; i < Tok::R; ++i) {
                 const int first = (wave + 4 * i) * Tok::kAtOnce;
@@ -393,24 +407,29 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                     *(uint4v*)&tok_lds[buf][kSplit ? 1 : 0][col][at] = __builtin_bit_cast(uint4v, lo);
                 }
             }
-            load_tokens<kFp4, kDown, NT>(tokens, src, at, k0 + X::KC, K, lane);
-            load_weights<kFp4, NT, kWide>(next, tile, k0 + X::KC, K, g);
-            // no use of this chunk's weights moves in front of these loads,
-            // where it would wait for all of them
+        };
+        auto request = [&](Weights<kFp4, kDown, NT, kWide>& next, int k0) {
+            // The tokens first, as they are wanted first; and no use of
+            // other weights moves in front of these loads, where it would
+            // wait for all of them.
+            load_tokens<kFp4, kDown, NT>(tokens, src, at, k0, K, lane);
             __builtin_amdgcn_sched_barrier(0);
-            __syncthreads();
-
+            load_weights<kFp4, kDown, NT, kWide>(next, tile, k0, K, lane & 3);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto compute = [&](const Weights<kFp4, kDown, NT, kWide>& now, int buf) {
             float4v c[NT];
             for (int nt = 0; nt < NT; ++nt)
                 c[nt] = kFp4 ? float4v{0, 0, 0, 0} : acc[nt];
             uint32_t pair[X::S];
             if (kFp4)
-                deal_scales<kFp4, NT, kWide>(now, pair, g);
+                deal_scales<kFp4, kDown, NT, kWide>(now, pair, g, from);
             for (int st = 0; st < X::S; ++st) {
                 if (kFp4) {
                     const half2v sv = e4m3x2(pair[st]);
+                    const uint4v w = handed(now.w[st], from);
                     for (int i = 0; i < 4; ++i) {
-                        const half8v wf = fp4x8(now.w[st][i], sv[i >> 1]);
+                        const half8v wf = fp4x8(w[i], sv[i >> 1]);
                         for (int nt = 0; nt < NT; ++nt)
                             if (nt < tiles)
                                 c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
@@ -418,7 +437,7 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
                                     c[nt], 0, 0, 0);
                     }
                 } else {
-                    const bf8v wf = __builtin_bit_cast(bf8v, now.w[st]);
+                    const bf8v wf = __builtin_bit_cast(bf8v, handed(now.w[st], from));
                     for (int nt = 0; nt < NT; ++nt)
                         if (nt < tiles) {
                             c[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -433,9 +452,24 @@ __global__ __launch_bounds__(kThreads) void moe_product_kernel(Moe a)
             for (int nt = 0; nt < NT; ++nt)
                 acc[nt] = kFp4 ? acc[nt] + c[nt] * scale_lds[buf][16 * nt + n] : c[nt];
         };
+
+        // A chunk is staged in one LDS buffer while the other is in use, so
+        // one barrier a chunk suffices; its weights go out two chunks ahead,
+        // into the registers that the chunk in front has just left.
+        load_tokens<kFp4, kDown, NT>(tokens, src, at, 0, K, lane);
+        if (col0 > 0)
+            load_weights<kFp4, kDown, NT, kWide>(even, tile, 0, K, lane & 3);
+        stage(0);
+        request(odd, X::KC);
         for (int k0 = 0; k0 < K; k0 += 2 * X::KC) {
-            chunk(even, odd, k0, 0);
-            chunk(odd, even, k0 + X::KC, 1);      // zeros where the chunks are odd in number
+            __syncthreads();
+            compute(even, 0);
+            stage(1);
+            request(even, k0 + 2 * X::KC);
+            __syncthreads();
+            compute(odd, 1);                // zeros behind the end of the axis
+            stage(0);
+            request(odd, k0 + 3 * X::KC);
         }
 
         for (int nt = 0; nt < NT; ++nt) {
