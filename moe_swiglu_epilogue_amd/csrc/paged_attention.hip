@@ -10,6 +10,8 @@ namespace {
 
 using namespace fp4op;
 
+typedef _Float16 half4v __attribute__((ext_vector_type(4)));
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -441,6 +443,347 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
     }
 }
 
+// ---- many query rows -----------------------------------------------------------
+// One workgroup of eight waves per (request, block of 256 query rows, key/value
+// head, split), 32 rows a wave. A tile of keys and values (128 tokens; 64 for
+// head_dim 256) is converted to FP16 once for all of them and kept in LDS,
+// the values transposed; the next tile is converted into a second buffer while
+// the waves are at different places of this one, so a tile takes one barrier.
+//
+// v_mfma_f32_32x32x16_f16, S^T = K Q^T again: a lane holds query row lane % 32
+// and, with h = lane / 32, the tokens 8 (r / 4) + 4 h + r % 4 of 32 in its 16
+// registers r. The second product, O^T = V^T P^T, sums over 16 tokens at a time,
+// its right operand the registers 8 u .. 8 u + 7 as they stand; so a row of V^T
+// in LDS keeps each 16 tokens in the order 0-3, 8-11, 4-7, 12-15.
+template <int D>
+struct Prompt {
+    static constexpr int kTokens = D > 128 ? 64 : 128;      // of a tile
+    static constexpr int kGroups = kTokens / 32;
+    static constexpr int kKeyPitch = D + 8;                 // FP16 elements
+    // 16-byte units of a row of V^T are exchanged by a row's number, which
+    // keeps both the writes (rows 8 apart) and the reads (neighbouring rows) on
+    // different banks
+    static __device__ __forceinline__ int unit(int d, int u)
+    {
+        return D > 128 ? u ^ (((d >> 1) ^ (d >> 3)) & 7) : u ^ ((d ^ (d >> 3)) & 15);
+    }
+};
+
+// What a lane loads of a tile: 32 tokens' keys (as in Tile) or values, of one
+// 128-wide chunk.
+struct Part {
+    uint32_t w[8], sc;
+    bool shown;
+};
+
+template <int D, bool kPaged16>
+__device__ __forceinline__ void load_part(Part& t, const Attn& a, const int32_t* table, int h,
+                                          int t0, int begin, int end, int lane, bool values, int c)
+{
+    const int g = lane >> 4, n = lane & 15, tok = lane & 31;
+    const uint32_t row = a.kv_heads * (D / 2), srow = a.kv_heads * (D / 16);
+    const uint8_t* codes = (values ? a.vp : a.kp) + h * (D / 2) + 64 * c;
+    const uint8_t* scales = (values ? a.vs : a.ks) + h * (D / 16) + 8 * c;
+    const uint32_t scale_at = D > 64 ? 4 * (lane >> 5) : 0;
+    bool shown;
+    if (kPaged16) {
+        // one page a half tile: addresses are a scalar and a lane's fixed offset
+        const uint8_t* half[2];
+        int64_t base[2];
+        bool hid[2];
+        for (int hh = 0; hh < 2; ++hh) {
+            const int first = t0 + 16 * hh;
+            const int p = (int)page_of(a, first);
+            const int entry = p < a.max_pages && first < end ? table[p] : -1;
+            hid[hh] = entry < 0 || entry >= a.num_pages;
+            base[hh] = hid[hh] ? 0 : (int64_t)entry * a.page + (first - p * a.page);
+            half[hh] = codes + base[hh] * row;
+        }
+        shown = !(tok < 16 ? hid[0] : hid[1]);
+        t.sc = *(const uint32_t*)(scales + (tok < 16 ? base[0] : base[1]) * srow + (tok & 15) * srow + scale_at);
+        if (values) {
+            for (int j = 0; j < 8; ++j) {
+                const uint8_t* from = half[j >> 2] + (j & 3) * row;
+                t.w[j] = D > 64 ? *(const uint32_t*)(from + (4 * g * row + 4 * n))
+                                : *(const uint16_t*)(from + (4 * g * row + 2 * n));
+            }
+        } else {
+            for (int hh = 0; hh < 2; ++hh) {
+                if (D > 64) {
+                    const uint4v w = *(const uint4v*)(half[hh] + (n * row + 16 * g));
+                    for (int i = 0; i < 4; ++i)
+                        t.w[4 * hh + i] = w[i];
+                } else {
+                    const uint2v w = *(const uint2v*)(half[hh] + (n * row + 8 * g));
+                    t.w[2 * hh] = w[0];
+                    t.w[2 * hh + 1] = w[1];
+                }
+            }
+        }
+    } else {
+        const int at = t0 + tok;
+        const int p = (int)page_of(a, at);
+        const int entry = at < end ? table[p] : -1;
+        shown = entry >= 0 && entry < a.num_pages;
+        const uint32_t s = shown ? entry * a.page + (at - p * a.page) : 0;
+        t.sc = *(const uint32_t*)(scales + (uint64_t)s * srow + scale_at);
+        if (values) {
+            for (int j = 0; j < 8; ++j) {
+                const uint64_t from = (uint64_t)from_lane(s, 16 * (j >> 2) + 4 * g + (j & 3)) * row;
+                t.w[j] = D > 64 ? *(const uint32_t*)(codes + from + 4 * n) : *(const uint16_t*)(codes + from + 2 * n);
+            }
+        } else {
+            for (int hh = 0; hh < 2; ++hh) {
+                const uint64_t from = (uint64_t)from_lane(s, n + 16 * hh) * row;
+                if (D > 64) {
+                    const uint4v w = *(const uint4v*)(codes + from + 16 * g);
+                    for (int i = 0; i < 4; ++i)
+                        t.w[4 * hh + i] = w[i];
+                } else {
+                    const uint2v w = *(const uint2v*)(codes + from + 8 * g);
+                    t.w[2 * hh] = w[0];
+                    t.w[2 * hh + 1] = w[1];
+                }
+            }
+        }
+    }
+    t.shown = shown && t0 + tok >= begin && t0 + tok < end;
+}
+
+// Converts it into LDS: group `grp` of 32 tokens, chunk c.
+template <int D>
+__device__ __forceinline__ void store_part(const Part& t, _Float16* keys, _Float16* vals, int grp,
+                                           int lane, bool values, int c)
+{
+    using P = Prompt<D>;
+    const int g = lane >> 4, n = lane & 15;
+    const uint32_t mine = t.shown ? t.sc : 0;
+    if (values) {
+        constexpr int VM = D > 64 ? 8 : 4;
+        const uint32_t byte = D > 64 ? (n >> 1) & 3 : n >> 2;
+        const uint32_t sel = byte | (4 + byte) << 8 | 0x0c0c0000u;
+        half2v sv[4];
+        uint32_t even[4], odd[4];
+        for (int u = 0; u < 4; ++u) {
+            const int tok = 16 * (u >> 1) + 4 * g + 2 * (u & 1) + (D > 64 ? 32 * (n >> 3) : 0);
+            sv[u] = e4m3x2(__builtin_amdgcn_perm(from_lane(mine, tok + 1), from_lane(mine, tok), sel));
+            const uint32_t x = t.w[2 * u], y = t.w[2 * u + 1];
+            even[u] = (x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u);
+            odd[u] = (x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
+        }
+        for (int i = 0; i < VM; ++i) {
+            const uint32_t* w = i & 1 ? odd : even;
+            const int d = 128 * c + VM * n + i;
+            for (int hh = 0; hh < 2; ++hh) {
+                // tokens 4 g .. 4 g + 3 of 16: the first half of unit g & 1, or
+                // the second (the order 0-3, 8-11, 4-7, 12-15)
+                const half2v x = fp4x2(w[2 * hh], i >> 1) * sv[2 * hh];
+                const half2v y = fp4x2(w[2 * hh + 1], i >> 1) * sv[2 * hh + 1];
+                *(half4v*)(vals + d * P::kTokens + 8 * P::unit(d, 4 * grp + 2 * hh + (g & 1)) + 4 * (g >> 1)) =
+                    half4v{x[0], x[1], y[0], y[1]};
+            }
+        }
+    } else {
+        for (int hh = 0; hh < 2; ++hh) {
+            uint32_t w = from_lane(mine, n + 16 * hh + (D > 64 ? 32 * (g >> 1) : 0));
+            w >>= D > 64 ? 16 * (g & 1) : 8 * g;
+            const half2v sk = e4m3x2(w);
+            _Float16* dst = keys + (32 * grp + 16 * hh + n) * P::kKeyPitch + 128 * c + (D > 64 ? 32 : 16) * g;
+            for (int i = 0; i < (D > 64 ? 4 : 2); ++i)
+                *(half8v*)(dst + 8 * i) = fp4x8(t.w[(D > 64 ? 4 : 2) * hh + i], D > 64 ? sk[i >> 1] : sk[0]);
+        }
+    }
+}
+
+template <int D, bool kPaged16>
+__global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
+{
+    using P = Prompt<D>;
+    typedef float float16v __attribute__((ext_vector_type(16)));
+    constexpr int kRows = 256, KF = D / 16, MT = D / 32;
+    __shared__ __attribute__((aligned(16))) _Float16 keys[2][P::kTokens * P::kKeyPitch];
+    __shared__ __attribute__((aligned(16))) _Float16 vals[2][D * P::kTokens];
+    __shared__ uint32_t shown_lds[2][P::kGroups];
+
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = a.heads / a.kv_heads;
+    // the blocks with the most tokens in front of them, a prompt's last, go first
+    const int pairs = a.num_seqs * a.kv_heads;
+    const int h = blockIdx.x % a.kv_heads, b = blockIdx.x % pairs / a.kv_heads;
+    const int split = blockIdx.x / pairs % a.splits;
+    const int block = a.row_blocks - 1 - blockIdx.x / pairs / a.splits;
+    Span s = request_span(a, b, group);
+    const int32_t* table = a.table + b * a.ld_table;
+    const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
+    // this wave's share of a tile's conversion
+    const bool values = wave >= 4;
+    const int grp = wave % P::kGroups, chunk = D > 128 ? (wave & 3) >> 1 : 0;
+
+    for (int row0 = block * kRows; row0 < s.rows; row0 += a.row_blocks * kRows) {
+        block_span(a, s, group, row0, kRows);
+        const int first = s.begin + split * s.chunk;
+        const int last = min(first + s.chunk, s.end);
+        if (first >= last && split > 0)
+            continue;
+
+        const int r = row0 + 32 * wave + col;
+        half8v q[KF];
+        int lo = 0, hi = 0;
+        float factor;
+        {
+            uint4v w[KF];
+            uint32_t top = 0;
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+                w[f] = uint4v{0, 0, 0, 0};
+            if (r < s.rows) {
+                const uint16_t* src = a.q + (s.first + r / group) * a.ld_q + (h * group + r % group) * D;
+#pragma unroll
+                for (int f = 0; f < KF; ++f) {
+                    w[f] = *(const uint4v*)(src + 16 * f + 8 * half);
+                    top = largest_bits(w[f], top);
+                }
+                sees(a, s.len, s.rows / group, r / group, lo, hi);
+            }
+            top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+            const int e = fp16_exponent(top);
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+                q[f] = scaled_half8(w[f], e);
+            factor = ldexpf(k_scale, -e);
+        }
+        // the tokens that some, and that all, rows of this wave see
+        Span mine = s;
+        const bool any_row = row0 + 32 * wave < s.rows;
+        if (any_row)
+            block_span(a, mine, group, row0 + 32 * wave, 32);
+
+        float16v o[MT];
+        float m = -INFINITY, l = 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                o[i][j] = 0;
+
+        Part part;
+        auto load = [&](int t0) {
+            load_part<D, kPaged16>(part, a, table, h, t0 + 32 * grp, s.begin, s.end, lane, values, chunk);
+        };
+        auto store = [&](int buf) {
+            store_part<D>(part, keys[buf], vals[buf], grp, lane, values, chunk);
+            const uint32_t bits = (uint32_t)__ballot(part.shown);
+            if (!values && chunk == 0 && lane == 0)
+                shown_lds[buf][grp] = bits;
+        };
+        __syncthreads();            // the row block before may still read
+        if (first < last) {
+            load(first);
+            store(0);
+            if (first + P::kTokens < last)
+                load(first + P::kTokens);
+        }
+        for (int t0 = first, buf = 0; t0 < last; t0 += P::kTokens, buf ^= 1) {
+            __syncthreads();
+#pragma unroll 1
+            for (int sub = 0; sub < P::kGroups; ++sub) {
+                const int ts = t0 + 32 * sub;
+                if (!any_row || ts >= mine.end || ts + 32 <= mine.begin || ts >= last)
+                    continue;
+                float16v sc;
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    sc[j] = 0;
+                const _Float16* kf = keys[buf] + (32 * sub + col) * P::kKeyPitch + 8 * half;
+#pragma unroll
+                for (int f = 0; f < KF; ++f)
+                    sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8v*)(kf + 16 * f), q[f], sc, 0, 0, 0);
+
+                const uint32_t shown = shown_lds[buf][sub];
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    x[j] = sc[j] * factor;
+                if (__builtin_amdgcn_readfirstlane(shown) != 0xffffffffu || ts < mine.all_begin ||
+                    ts + 32 > mine.all_end) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int in = 8 * (j >> 2) + 4 * half + (j & 3);
+                        if (!(shown >> in & 1) || ts + in < lo || ts + in >= hi)
+                            x[j] = -INFINITY;
+                    }
+                }
+                float top = x[0];
+                for (int j = 1; j < 16; ++j)
+                    top = fmaxf(top, x[j]);
+                if (__any(top > m + kSlack)) {
+                    const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                    const float f = m == up ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+                    m = up;
+                    l *= f;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            o[i][j] *= f;
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                half8v p[2];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    x[j] = __builtin_amdgcn_exp2f(x[j] - base);
+                    l += x[j];
+                    p[j >> 3][j & 7] = (_Float16)x[j];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int d = 32 * i + col;
+                        const half8v vf = *(const half8v*)(vals[buf] + d * P::kTokens +
+                                                           8 * P::unit(d, 4 * sub + 2 * u + half));
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[u], o[i], 0, 0, 0);
+                    }
+            }
+            if (t0 + P::kTokens < last) {
+                store(buf ^ 1);
+                if (t0 + 2 * P::kTokens < last)
+                    load(t0 + 2 * P::kTokens);
+            }
+        }
+
+        const float total = l + __shfl_xor(l, 32);
+        if (r < s.rows) {
+            const int64_t token = s.first + r / group;
+            const int head = h * group + r % group;
+            const bool whole_row = a.splits == 1;
+            const float norm = whole_row ? (total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int d = 32 * i + 8 * j + 4 * half;
+                    const float4v v = float4v{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]} * norm;
+                    if (whole_row)
+                        *(uint2v*)(a.out + token * a.ld_out + head * D + d) = uint2v{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+                    else
+                        *(float4v*)(a.part + (((int64_t)split * a.tokens + token) * a.heads + head) * D + d) = v;
+                }
+            if (half == 0) {
+                if (!whole_row) {
+                    float* ml = a.part + (int64_t)a.splits * a.tokens * a.heads * D +
+                                2 * (((int64_t)split * a.tokens + token) * a.heads + head);
+                    ml[0] = m;
+                    ml[1] = total;
+                } else if (a.lse) {
+                    a.lse[token * a.heads + head] = total > 0 ? (m + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+    }
+}
+
 // Joins the splits of one query row: a workgroup per (token, head), whose four
 // waves take a share of the splits each.
 template <int D>
@@ -513,7 +856,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int block)
 
 // ---- host -------------------------------------------------------------------
 struct Plan {
-    int tiles;         // 16-row tiles of a workgroup
+    int block;         // query rows of a workgroup: 16, 32, 64, or 256 (the prompt kernel)
     int row_blocks;    // workgroups over a request's rows
     int splits, chunk; // of the tokens
 };
@@ -525,21 +868,26 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
     Plan p;
     const int64_t group = heads / kv_heads;
     const int64_t rows = (max_query_len < 1 ? 1 : max_query_len > (1 << 20) ? 1 << 20 : max_query_len) * group;
-    p.tiles = rows <= 16 || head_dim > 128 ? 1 : rows <= 32 ? 2 : 4;
-    int64_t blocks = ceil_div(rows, (int64_t)16 * p.tiles);
-    p.row_blocks = (int)(blocks > 1024 ? 1024 : blocks);
+    if (head_dim > 128)
+        p.block = rows <= 32 ? 16 : 256;
+    else
+        p.block = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 64 : 256;
+    int64_t blocks = ceil_div(rows, (int64_t)p.block);
+    p.row_blocks = (int)(blocks > 4096 ? 4096 : blocks);
     int64_t range = max_seq_len > INT32_MAX ? INT32_MAX : max_seq_len;
     if (window > 0 && window + max_query_len + 32 < range)
         range = window + max_query_len + 32;
     const int64_t items = (num_seqs < 1 ? 1 : num_seqs) * kv_heads * p.row_blocks;
-    int64_t want = ceil_div((int64_t)1024, items);
-    const int64_t least = ceil_div(range, (int64_t)1024);
-    if (want < least)
-        want = least;
-    int64_t chunk = ceil_div(ceil_div(range, want), (int64_t)128) * 128;
-    if (chunk < 128)
-        chunk = 128;
-    int64_t splits = ceil_div(range < 1 ? 1 : range, chunk);
+    // Enough workgroups to fill the card, four a compute unit (prompt kernel:
+    // one); for few rows also splits short enough that ragged requests balance.
+    const bool prompt = p.block == 256;
+    int64_t want = ceil_div((int64_t)(prompt ? 256 : 1024), items);
+    if (!prompt && want < ceil_div(range, (int64_t)1024))
+        want = ceil_div(range, (int64_t)1024);
+    int64_t splits = want;
+    const int64_t shortest = prompt ? 1024 : 128;
+    if (splits > ceil_div(range < 1 ? 1 : range, shortest))
+        splits = ceil_div(range < 1 ? 1 : range, shortest);
     if (splits > 256)
         splits = 256;
     // grids stay below 2^24 workgroups (rows and splits left out are looped over)
@@ -551,11 +899,9 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
         if (p.row_blocks > most)
             p.row_blocks = (int)(most < 1 ? 1 : most);
     }
-    chunk = ceil_div(ceil_div(range, splits), (int64_t)128) * 128;
-    if (chunk < 128)
-        chunk = 128;
-    p.splits = (int)splits;
-    p.chunk = (int)chunk;
+    const int64_t chunk = ceil_div(ceil_div(range, splits), (int64_t)128) * 128;
+    p.chunk = (int)(chunk < 128 ? 128 : chunk);
+    p.splits = (int)ceil_div(range < 1 ? 1 : range, (int64_t)p.chunk);
     return p;
 }
 
@@ -569,21 +915,27 @@ void launch_rows(const Attn& a, dim3 grid, hipStream_t stream)
 }
 
 template <int D>
-void launch(const Attn& a, int tiles, hipStream_t stream)
+void launch(const Attn& a, int block, hipStream_t stream)
 {
     const int64_t work = (int64_t)a.num_seqs * a.row_blocks * a.splits;
     const dim3 grid((unsigned)((work + 7) / 8 * 8 * a.kv_heads));
-    if (tiles == 1)
+    if (block == 256) {
+        const dim3 all((unsigned)(work * a.kv_heads));
+        if (a.page % 16 == 0)
+            hipLaunchKernelGGL((attn_prompt_kernel<D, true>), all, dim3(512), 0, stream, a);
+        else
+            hipLaunchKernelGGL((attn_prompt_kernel<D, false>), all, dim3(512), 0, stream, a);
+    } else if (block == 16) {
         launch_rows<D, 1>(a, grid, stream);
-    if constexpr (D <= 128) {
-        if (tiles == 2)
+    } else if constexpr (D <= 128) {
+        if (block == 32)
             launch_rows<D, 2>(a, grid, stream);
-        else if (tiles == 4)
+        else
             launch_rows<D, 4>(a, grid, stream);
     }
     if (a.splits > 1)
         hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)a.tokens * a.heads), dim3(256), 0, stream, a,
-                           16 * tiles);
+                           block);
 }
 
 bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,
@@ -669,10 +1021,10 @@ extern "C" nvfp4_status_t nvfp4_paged_attention(
     a.chunk = p.chunk;
     a.row_blocks = p.row_blocks;
     if (head_dim == 64)
-        launch<64>(a, p.tiles, stream);
+        launch<64>(a, p.block, stream);
     else if (head_dim == 128)
-        launch<128>(a, p.tiles, stream);
+        launch<128>(a, p.block, stream);
     else
-        launch<256>(a, p.tiles, stream);
+        launch<256>(a, p.block, stream);
     return launched();
 }
