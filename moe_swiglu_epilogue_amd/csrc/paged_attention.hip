@@ -11,6 +11,7 @@ namespace {
 using namespace fp4op;
 
 typedef _Float16 half4v __attribute__((ext_vector_type(4)));
+typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
@@ -95,14 +96,34 @@ __device__ __forceinline__ float row_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// A query row's values for one matrix operand: BF16 to FP16 with the row's
-// power of two 2^e.
-__device__ __forceinline__ half8v scaled_half8(uint4v w, int e)
+// Largest of a matrix result's registers. The asm keeps it where it is written,
+// right behind the matrix instructions: compiled code that first reads their
+// result behind a branch has been seen to read it too early (the wait states
+// on the path that takes the branch were missing), with wrong scores.
+template <int N, class T>
+__device__ __forceinline__ float largest_of(const T& v)
 {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        top = fmaxf(top, v[i]);
+    asm volatile("" : "+v"(top));
+    return top;
+}
+
+__device__ __forceinline__ float largest(const float (&v)[8]) { return largest_of<8>(v); }
+__device__ __forceinline__ float largest(const float16v& v) { return largest_of<16>(v); }
+
+// A query row's values for one matrix operand: BF16 to FP16 with the row's
+// power of two 2^e and, for a negative scale, its sign.
+__device__ __forceinline__ half8v scaled_half8(uint4v w, int e, bool negative)
+{
+    const float f = negative ? -ldexpf(1.0f, e) : ldexpf(1.0f, e);
     half8v r;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        r[2 * i] = (_Float16)ldexpf(__uint_as_float(w[i] << 16), e);
-        r[2 * i + 1] = (_Float16)ldexpf(__uint_as_float(w[i] & 0xffff0000u), e);
+        r[2 * i] = (_Float16)(__uint_as_float(w[i] << 16) * f);
+        r[2 * i + 1] = (_Float16)(__uint_as_float(w[i] & 0xffff0000u) * f);
     }
     return r;
 }
@@ -284,8 +305,10 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
             const int e = fp16_exponent(top);
             for (int f = 0; f < KF; ++f)
-                q[rt][f] = scaled_half8(w[f], e);
-            factor[rt] = ldexpf(k_scale, -e);
+                q[rt][f] = scaled_half8(w[f], e, k_scale < 0);
+            // positive, so that the largest product gives the largest score, and
+            // not 0, which would turn a hidden token's -inf into NaN
+            factor[rt] = fmaxf(ldexpf(fabsf(k_scale), -e), 0x1p-126f);
         }
 
         float4v o[RT][C][VM];
@@ -337,7 +360,8 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
             for (int rt = 0; rt < RT; ++rt) {
                 float x[8];
                 for (int i = 0; i < 8; ++i)
-                    x[i] = sc[rt][i >> 2][i & 3] * factor[rt];
+                    x[i] = sc[rt][i >> 2][i & 3];
+                float top = largest(x);
                 if (!whole) {
                     for (int i = 0; i < 8; ++i) {
                         const int in = 16 * (i >> 2) + 4 * g + (i & 3);
@@ -345,10 +369,9 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                         if (gone || t0 + in < lo[rt] || t0 + in >= hi[rt])
                             x[i] = -INFINITY;
                     }
+                    top = largest(x);
                 }
-                float top = x[0];
-                for (int i = 1; i < 8; ++i)
-                    top = fmaxf(top, x[i]);
+                top *= factor[rt];
                 if (__any(top > m[rt] + kSlack)) {
                     const float up = fmaxf(m[rt], row_max(top));
                     const float f = m[rt] == up ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - up);
@@ -361,7 +384,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                 // a row that has seen nothing keeps m = -inf: its terms are 0
                 const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
                 for (int i = 0; i < 8; ++i) {
-                    x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+                    x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], factor[rt], -base));
                     l[rt] += x[i];
                     p[rt][i] = (_Float16)x[i];
                 }
@@ -459,14 +482,14 @@ template <int D>
 struct Prompt {
     static constexpr int kTokens = D > 128 ? 64 : 128;      // of a tile
     static constexpr int kGroups = kTokens / 32;
+    static constexpr int kStep = D > 128 ? 1 : 2;           // groups of 32 tokens a wave takes at once
+    // Rows of keys lie 4 banks apart (of 64). Rows of V^T lie 8 banks apart and
+    // every eight of them another 4, so that neighbouring rows (reads) as well
+    // as every eighth (writes) cover all banks.
     static constexpr int kKeyPitch = D + 8;                 // FP16 elements
-    // 16-byte units of a row of V^T are exchanged by a row's number, which
-    // keeps both the writes (rows 8 apart) and the reads (neighbouring rows) on
-    // different banks
-    static __device__ __forceinline__ int unit(int d, int u)
-    {
-        return D > 128 ? u ^ (((d >> 1) ^ (d >> 3)) & 7) : u ^ ((d ^ (d >> 3)) & 15);
-    }
+    static constexpr int kValPitch = kTokens + 16;
+    static constexpr int kVals = D * kValPitch + D;
+    static __device__ __forceinline__ int val(int d) { return d * kValPitch + (d >> 3) * 8; }
 };
 
 // What a lane loads of a tile: 32 tokens' keys (as in Tile) or values, of one
@@ -579,7 +602,7 @@ __device__ __forceinline__ void store_part(const Part& t, _Float16* keys, _Float
                 // the second (the order 0-3, 8-11, 4-7, 12-15)
                 const half2v x = fp4x2(w[2 * hh], i >> 1) * sv[2 * hh];
                 const half2v y = fp4x2(w[2 * hh + 1], i >> 1) * sv[2 * hh + 1];
-                *(half4v*)(vals + d * P::kTokens + 8 * P::unit(d, 4 * grp + 2 * hh + (g & 1)) + 4 * (g >> 1)) =
+                *(half4v*)(vals + P::val(d) + 32 * grp + 16 * hh + 8 * (g & 1) + 4 * (g >> 1)) =
                     half4v{x[0], x[1], y[0], y[1]};
             }
         }
@@ -599,10 +622,9 @@ template <int D, bool kPaged16>
 __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
 {
     using P = Prompt<D>;
-    typedef float float16v __attribute__((ext_vector_type(16)));
     constexpr int kRows = 256, KF = D / 16, MT = D / 32;
     __shared__ __attribute__((aligned(16))) _Float16 keys[2][P::kTokens * P::kKeyPitch];
-    __shared__ __attribute__((aligned(16))) _Float16 vals[2][D * P::kTokens];
+    __shared__ __attribute__((aligned(16))) _Float16 vals[2][P::kVals];
     __shared__ uint32_t shown_lds[2][P::kGroups];
 
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
@@ -650,8 +672,10 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
             const int e = fp16_exponent(top);
 #pragma unroll
             for (int f = 0; f < KF; ++f)
-                q[f] = scaled_half8(w[f], e);
-            factor = ldexpf(k_scale, -e);
+                q[f] = scaled_half8(w[f], e, k_scale < 0);
+            // positive, so that the largest product gives the largest score, and
+            // not 0, which would turn a hidden token's -inf into NaN
+            factor = fmaxf(ldexpf(fabsf(k_scale), -e), 0x1p-126f);
         }
         // the tokens that some, and that all, rows of this wave see
         Span mine = s;
@@ -687,36 +711,50 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
         for (int t0 = first, buf = 0; t0 < last; t0 += P::kTokens, buf ^= 1) {
             __syncthreads();
 #pragma unroll 1
-            for (int sub = 0; sub < P::kGroups; ++sub) {
+            for (int sub = 0; sub < P::kGroups; sub += P::kStep) {
+                constexpr int N = P::kStep;
                 const int ts = t0 + 32 * sub;
-                if (!any_row || ts >= mine.end || ts + 32 <= mine.begin || ts >= last)
+                if (!any_row || ts >= mine.end || ts + 32 * N <= mine.begin || ts >= last)
                     continue;
-                float16v sc;
+                float16v sc[N];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    sc[j] = 0;
+                for (int t = 0; t < N; ++t)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        sc[t][j] = 0;
                 const _Float16* kf = keys[buf] + (32 * sub + col) * P::kKeyPitch + 8 * half;
 #pragma unroll
                 for (int f = 0; f < KF; ++f)
-                    sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8v*)(kf + 16 * f), q[f], sc, 0, 0, 0);
+#pragma unroll
+                    for (int t = 0; t < N; ++t)
+                        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            *(const half8v*)(kf + 32 * t * P::kKeyPitch + 16 * f), q[f], sc[t], 0, 0, 0);
 
-                const uint32_t shown = shown_lds[buf][sub];
-                float x[16];
+                uint32_t shown[N];
+                bool whole = ts >= mine.all_begin && ts + 32 * N <= mine.all_end;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = sc[j] * factor;
-                if (__builtin_amdgcn_readfirstlane(shown) != 0xffffffffu || ts < mine.all_begin ||
-                    ts + 32 > mine.all_end) {
+                for (int t = 0; t < N; ++t) {
+                    shown[t] = __builtin_amdgcn_readfirstlane(shown_lds[buf][sub + t]);
+                    whole = whole && shown[t] == 0xffffffffu;
+                }
+                float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int in = 8 * (j >> 2) + 4 * half + (j & 3);
-                        if (!(shown >> in & 1) || ts + in < lo || ts + in >= hi)
-                            x[j] = -INFINITY;
+                for (int t = 0; t < N; ++t)
+                    top = fmaxf(top, largest(sc[t]));
+                if (!whole) {
+                    top = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < N; ++t) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int in = 8 * (j >> 2) + 4 * half + (j & 3);
+                            if (!(shown[t] >> in & 1) || ts + 32 * t + in < lo || ts + 32 * t + in >= hi)
+                                sc[t][j] = -INFINITY;
+                        }
+                        top = fmaxf(top, largest(sc[t]));
                     }
                 }
-                float top = x[0];
-                for (int j = 1; j < 16; ++j)
-                    top = fmaxf(top, x[j]);
+                top *= factor;
                 if (__any(top > m + kSlack)) {
                     const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
                     const float f = m == up ? 1.0f : __builtin_amdgcn_exp2f(m - up);
@@ -729,22 +767,24 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                             o[i][j] *= f;
                 }
                 const float base = m == -INFINITY ? 0.0f : m;
-                half8v p[2];
+                half8v p[N][2];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    x[j] = __builtin_amdgcn_exp2f(x[j] - base);
-                    l += x[j];
-                    p[j >> 3][j & 7] = (_Float16)x[j];
-                }
+                for (int t = 0; t < N; ++t)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int d = 32 * i + col;
-                        const half8v vf = *(const half8v*)(vals[buf] + d * P::kTokens +
-                                                           8 * P::unit(d, 4 * sub + 2 * u + half));
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, p[u], o[i], 0, 0, 0);
+                    for (int j = 0; j < 16; ++j) {
+                        const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][j], factor, -base));
+                        l += e;
+                        p[t][j >> 3][j & 7] = (_Float16)e;
                     }
+                const _Float16* vf = vals[buf] + P::val(col) + 32 * sub + 8 * half;
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                *(const half8v*)(vf + P::val(32 * i) + 32 * t + 16 * u), p[t][u], o[i], 0, 0, 0);
             }
             if (t0 + P::kTokens < last) {
                 store(buf ^ 1);
