@@ -23,7 +23,7 @@ struct Attn {
     const float *k_gs, *v_gs;
     uint16_t* out;
     float* lse;
-    float* part;       // workspace: [splits][tokens * heads][D], then [splits][tokens * heads] pairs (m, l)
+    float* part;       // workspace
     int64_t ld_q, ld_out, ld_table, window;
     int tokens, heads, kv_heads, page, num_pages, max_pages, num_seqs, causal;
     float scale;
@@ -71,6 +71,22 @@ __device__ __forceinline__ void block_span(const Attn& a, Span& s, int group, in
     // splits of a.chunk tokens, of more where the range is longer than promised
     const int total = s.end - s.begin;
     s.chunk = max(a.chunk, ((total + a.splits - 1) / a.splits + 127) & ~127);
+}
+
+// The workspace: each split's output rows, its (maximum, sum) pairs, and, written
+// by split 0, how many splits a row has.
+__device__ __forceinline__ int* used_splits(const Attn& a, int D)
+{
+    return (int*)(a.part + (int64_t)a.splits * a.tokens * a.heads * (D + 2));
+}
+
+__device__ __forceinline__ void write_split(const Attn& a, const Span& s, int D, int split, int64_t row,
+                                            float m, float l)
+{
+    const int64_t rows = (int64_t)a.tokens * a.heads;
+    *(float2*)(a.part + a.splits * rows * D + 2 * (split * rows + row)) = make_float2(m, l);
+    if (split == 0)
+        used_splits(a, D)[row] = max(1, (s.end - s.begin + s.chunk - 1) / s.chunk);
 }
 
 __device__ __forceinline__ uint32_t page_of(const Attn& a, uint32_t t)
@@ -168,76 +184,77 @@ struct Tile {
     bool hidden0, hidden1;                            // uniform: a whole half is hidden
 };
 
+// Where a half tile of 16 tokens stands if it lies in one page (page_size a
+// multiple of 16): the slot of its first token, 0 with `hidden` set where the
+// page does not count (its loads then read the cache's first slots).
+struct Half {
+    int64_t slot;
+    bool hidden;
+};
+
+__device__ __forceinline__ Half half_tile(const Attn& a, const int32_t* table, int first, int end)
+{
+    const int p = (int)page_of(a, first);
+    const int entry = p < a.max_pages && first < end ? table[p] : -1;
+    Half h;
+    h.hidden = entry < 0 || entry >= a.num_pages;
+    h.slot = h.hidden ? 0 : (int64_t)entry * a.page + (first - p * a.page);
+    return h;
+}
+
 template <int D, bool kPaged16>
 __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32_t* table, int h,
                                           int t0, int begin, int end, int lane)
 {
     using T = Tile<D>;
     const int g = lane >> 4, n = lane & 15, tok = lane & 31;
-    const int64_t row = (int64_t)a.kv_heads * (D / 2), srow = (int64_t)a.kv_heads * (D / 16);
+    const uint32_t row = a.kv_heads * (D / 2), srow = a.kv_heads * (D / 16);
     const uint8_t* kp = a.kp + h * (D / 2);
     const uint8_t* vp = a.vp + h * (D / 2);
     const uint8_t* ks = a.ks + h * (D / 16);
     const uint8_t* vs = a.vs + h * (D / 16);
-    int64_t mine;                 // slot of this lane's token
-    int64_t slot_k[2], slot_v[8];
-    bool shown;
+    Half half[2];                  // kPaged16: addresses are a scalar and a lane's fixed offset
+    uint32_t slot = 0;             // else: the slot of this lane's token
     if (kPaged16) {
-        // 16 tokens of a half tile stand in one page: one entry a half
-        int64_t base[2];
-        bool hid[2];
-        for (int hh = 0; hh < 2; ++hh) {
-            const int first = t0 + 16 * hh;
-            const int p = (int)page_of(a, first);
-            const int entry = p < a.max_pages && first < end ? table[p] : -1;
-            hid[hh] = entry < 0 || entry >= a.num_pages;
-            base[hh] = hid[hh] ? 0 : (int64_t)entry * a.page + (first - p * a.page);
-        }
-        t.hidden0 = hid[0];
-        t.hidden1 = hid[1];
-        // a hidden half reads the cache's first slots instead (a page holds 16 or more)
-        for (int hh = 0; hh < 2; ++hh)
-            slot_k[hh] = base[hh] + n;
-        for (int j = 0; j < 8; ++j)
-            slot_v[j] = base[j >> 2] + 4 * g + (j & 3);
-        mine = base[tok >> 4] + (tok & 15);
-        shown = !(tok < 16 ? hid[0] : hid[1]);
+        half[0] = half_tile(a, table, t0, end);
+        half[1] = half_tile(a, table, t0 + 16, end);
+        t.hidden0 = half[0].hidden;
+        t.hidden1 = half[1].hidden;
+        t.shown = !(tok < 16 ? t.hidden0 : t.hidden1);
     } else {
         const int at = t0 + tok;
         const int p = (int)page_of(a, at);
         const int entry = at < end ? table[p] : -1;
-        shown = entry >= 0 && entry < a.num_pages;
-        const int slot = shown ? entry * a.page + (at - p * a.page) : 0;
-        mine = slot;
-        for (int hh = 0; hh < 2; ++hh)
-            slot_k[hh] = (int)from_lane(slot, n + 16 * hh);
-        for (int j = 0; j < 8; ++j)
-            slot_v[j] = (int)from_lane(slot, 16 * (j >> 2) + 4 * g + (j & 3));
+        t.shown = entry >= 0 && entry < a.num_pages;
+        slot = t.shown ? entry * a.page + (at - p * a.page) : 0;
         t.hidden0 = t.hidden1 = false;
     }
-    t.shown = shown && t0 + tok >= begin && t0 + tok < end;
+    t.shown = t.shown && t0 + tok >= begin && t0 + tok < end;
     for (int c = 0; c < T::C; ++c) {
         for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* from = kPaged16 ? kp + half[hh].slot * row + 64 * c + (n * row + (D > 64 ? 16 : 8) * g)
+                                           : kp + (uint64_t)from_lane(slot, n + 16 * hh) * row + 64 * c + (D > 64 ? 16 : 8) * g;
             if (D > 64) {
-                const uint4v w = *(const uint4v*)(kp + slot_k[hh] * row + 64 * c + 16 * g);
+                const uint4v w = *(const uint4v*)from;
                 for (int i = 0; i < 4; ++i)
                     t.k[hh][c][i % T::KW] = w[i];
             } else {
-                const uint2v w = *(const uint2v*)(kp + slot_k[hh] * row + 8 * g);
+                const uint2v w = *(const uint2v*)from;
                 t.k[hh][c][0] = w[0];
                 t.k[hh][c][1] = w[1];
             }
         }
         // scales: a lane takes 4 bytes of its token (the second half of the
         // wave the next 4), handed to the lanes that need them when used
-        const int64_t at = mine * srow + (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
+        const uint64_t at = (kPaged16 ? (uint64_t)((tok < 16 ? half[0].slot : half[1].slot) + (tok & 15)) : (uint64_t)slot) * srow +
+                            (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
         t.ks[c] = *(const uint32_t*)(ks + at);
         t.vs[c] = *(const uint32_t*)(vs + at);
         for (int j = 0; j < 8; ++j) {
-            if (D > 64)
-                t.v[j][c] = *(const uint32_t*)(vp + slot_v[j] * row + 64 * c + 4 * n);
-            else
-                t.v[j][c] = *(const uint16_t*)(vp + slot_v[j] * row + 2 * n);
+            const uint8_t* from =
+                kPaged16 ? vp + half[j >> 2].slot * row + (j & 3) * row + 64 * c + (4 * g * row + (D > 64 ? 4 : 2) * n)
+                         : vp + (uint64_t)from_lane(slot, 16 * (j >> 2) + 4 * g + (j & 3)) * row + 64 * c + (D > 64 ? 4 : 2) * n;
+            t.v[j][c] = D > 64 ? *(const uint32_t*)from : *(const uint16_t*)from;
         }
     }
 }
@@ -454,10 +471,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
             }
             if ((tid & 15) == 0) {
                 if (!whole_row) {
-                    float* ml = a.part + (int64_t)a.splits * a.tokens * a.heads * D +
-                                2 * (((int64_t)split * a.tokens + token) * a.heads + head);
-                    ml[0] = top;
-                    ml[1] = total;
+                    write_split(a, s, D, split, token * a.heads + head, top, total);
                 } else if (a.lse) {
                     a.lse[token * a.heads + head] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
                 }
@@ -510,20 +524,11 @@ __device__ __forceinline__ void load_part(Part& t, const Attn& a, const int32_t*
     const uint32_t scale_at = D > 64 ? 4 * (lane >> 5) : 0;
     bool shown;
     if (kPaged16) {
-        // one page a half tile: addresses are a scalar and a lane's fixed offset
-        const uint8_t* half[2];
-        int64_t base[2];
-        bool hid[2];
-        for (int hh = 0; hh < 2; ++hh) {
-            const int first = t0 + 16 * hh;
-            const int p = (int)page_of(a, first);
-            const int entry = p < a.max_pages && first < end ? table[p] : -1;
-            hid[hh] = entry < 0 || entry >= a.num_pages;
-            base[hh] = hid[hh] ? 0 : (int64_t)entry * a.page + (first - p * a.page);
-            half[hh] = codes + base[hh] * row;
-        }
-        shown = !(tok < 16 ? hid[0] : hid[1]);
-        t.sc = *(const uint32_t*)(scales + (tok < 16 ? base[0] : base[1]) * srow + (tok & 15) * srow + scale_at);
+        // addresses are a scalar and a lane's fixed offset
+        const Half at[2] = {half_tile(a, table, t0, end), half_tile(a, table, t0 + 16, end)};
+        const uint8_t* half[2] = {codes + at[0].slot * row, codes + at[1].slot * row};
+        shown = !(tok < 16 ? at[0].hidden : at[1].hidden);
+        t.sc = *(const uint32_t*)(scales + (tok < 16 ? at[0].slot : at[1].slot) * srow + (tok & 15) * srow + scale_at);
         if (values) {
             for (int j = 0; j < 8; ++j) {
                 const uint8_t* from = half[j >> 2] + (j & 3) * row;
@@ -630,11 +635,11 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
     const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = a.heads / a.kv_heads;
-    // the blocks with the most tokens in front of them, a prompt's last, go first
+    // each request's blocks from its end: those with the most tokens to see go
+    // first, and the short ones fill up the end
     const int pairs = a.num_seqs * a.kv_heads;
     const int h = blockIdx.x % a.kv_heads, b = blockIdx.x % pairs / a.kv_heads;
     const int split = blockIdx.x / pairs % a.splits;
-    const int block = a.row_blocks - 1 - blockIdx.x / pairs / a.splits;
     Span s = request_span(a, b, group);
     const int32_t* table = a.table + b * a.ld_table;
     const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
@@ -642,7 +647,8 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
     const bool values = wave >= 4;
     const int grp = wave % P::kGroups, chunk = D > 128 ? (wave & 3) >> 1 : 0;
 
-    for (int row0 = block * kRows; row0 < s.rows; row0 += a.row_blocks * kRows) {
+    for (int row0 = (s.rows - 1) / kRows * kRows - blockIdx.x / pairs / a.splits * kRows; row0 >= 0 && s.rows > 0;
+         row0 -= a.row_blocks * kRows) {
         block_span(a, s, group, row0, kRows);
         const int first = s.begin + split * s.chunk;
         const int last = min(first + s.chunk, s.end);
@@ -812,10 +818,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                 }
             if (half == 0) {
                 if (!whole_row) {
-                    float* ml = a.part + (int64_t)a.splits * a.tokens * a.heads * D +
-                                2 * (((int64_t)split * a.tokens + token) * a.heads + head);
-                    ml[0] = m;
-                    ml[1] = total;
+                    write_split(a, s, D, split, token * a.heads + head, m, total);
                 } else if (a.lse) {
                     a.lse[token * a.heads + head] = total > 0 ? (m + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
                 }
@@ -824,72 +827,82 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
     }
 }
 
-// Joins the splits of one query row: a workgroup per (token, head), whose four
-// waves take a share of the splits each.
-template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(Attn a, int block)
+// Joins the splits of the query rows: kWaves waves a (token, head), which take a
+// share of the splits each. Bound by latency: everything it needs to know, which
+// rows count and how many splits they have, is loaded at once.
+template <int D, int kWaves>
+__global__ __launch_bounds__(256) void attn_join_kernel(Attn a)
 {
-    constexpr int kLanes = D / 4, kShares = 256 / kLanes;     // lanes across a row; splits read at once
-    __shared__ float4v o_lds[kShares][kLanes];
-    __shared__ float f_lds[256];
-    __shared__ float wave_top[4], wave_sum[4];
-    const int tid = threadIdx.x, head = blockIdx.x % a.heads, token = blockIdx.x / a.heads;
-    const int group = a.heads / a.kv_heads;
-    // the last request whose first row is at or before this one
-    int lo = 0, hi = a.num_seqs + 1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.offsets[mid] <= token)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    if (lo == a.num_seqs || token < a.offsets[0])
-        return;
-    Span s = request_span(a, lo, group);
-    const int r = (token - s.first) * group + head % group;
-    if (r < 0 || r >= s.rows)
-        return;
-    block_span(a, s, group, r / block * block, block);
-    const int used = max(1, (s.end - s.begin + s.chunk - 1) / s.chunk);   // at most a.splits <= 256
-    const int64_t rows = (int64_t)a.tokens * a.heads, row = (int64_t)token * a.heads + head;
+    constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes * kWaves;    // lanes a row of D; splits read at once
+    constexpr int kRows = 4 / kWaves;
+    __shared__ float4v o_lds[4][kLanes];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t rows = (int64_t)a.tokens * a.heads;
+    const int64_t row = (int64_t)blockIdx.x * kRows + wave / kWaves;
+    const bool mine = row < rows;
+    const int64_t at = mine ? row : 0;
+    const int token = (int)(at / a.heads), head = (int)(at % a.heads);
+    const int used = min(max(used_splits(a, D)[at], 0), a.splits);
     const float* ml = a.part + a.splits * rows * D;
-
-    float m = -INFINITY, l = 0;
-    if (tid < used) {
-        m = ml[2 * (tid * rows + row)];
-        l = ml[2 * (tid * rows + row) + 1];
+    float m[4], l[4], top = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+        const int split = 64 * i + lane;
+        m[i] = -INFINITY;
+        l[i] = 0;
+        if (split < a.splits) {
+            const float2 v = *(const float2*)(ml + 2 * (split * rows + at));
+            m[i] = split < used ? v.x : -INFINITY;
+            l[i] = split < used ? v.y : 0.0f;
+        }
+        top = fmaxf(top, m[i]);
     }
-    float top = m;
+    const bool shown = mine && token >= a.offsets[0] && token < a.offsets[a.num_seqs];
     for (int d = 32; d; d >>= 1)
         top = fmaxf(top, __shfl_xor(top, d));
-    if ((tid & 63) == 0)
-        wave_top[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
-    const float f = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-    f_lds[tid] = f;
-    float sum = f * l;
+    float total = 0;
+    for (int i = 0; i < 4; ++i) {
+        m[i] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
+        total += m[i] * l[i];
+    }
     for (int d = 32; d; d >>= 1)
-        sum += __shfl_xor(sum, d);
-    if ((tid & 63) == 0)
-        wave_sum[tid >> 6] = sum;
-    __syncthreads();
-    const float total = wave_sum[0] + wave_sum[1] + wave_sum[2] + wave_sum[3];
+        total += __shfl_xor(total, d);
 
-    const int share = tid / kLanes, x = tid % kLanes;
+    const int x = lane % kLanes, first = wave % kWaves * (64 / kLanes) + lane / kLanes;
     float4v o = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int i = share; i < used; i += kShares)
-        o += f_lds[i] * *(const float4v*)(a.part + (i * rows + row) * D + 4 * x);
-    o_lds[share][x] = o;
-    __syncthreads();
-    if (tid < kLanes) {
-        for (int i = 1; i < kShares; ++i)
-            o += o_lds[i][tid];
+    for (int i = 0; i < 4; ++i) {
+        // the splits 64 i .. 64 i + 63, whose weights the lanes' m[i] hold
+        const int n = min(used - 64 * i, 64);
+        for (int base = 0; base < n; base += 4 * kAtOnce) {
+            float4v v[4];
+            float f[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = base + u * kAtOnce + first;
+                f[u] = __shfl(m[i], k & 63);
+                v[u] = float4v{0, 0, 0, 0};
+                if (k < n)
+                    v[u] = *(const float4v*)(a.part + ((64 * i + k) * rows + at) * D + 4 * x);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                o += f[u] * v[u];
+        }
+    }
+    for (int d = kLanes; d < 64; d <<= 1)
+        for (int j = 0; j < 4; ++j)
+            o[j] += __shfl_xor(o[j], d);
+    if (kWaves > 1) {
+        if (lane < kLanes)
+            o_lds[wave][lane] = o;
+        __syncthreads();
+        o = float4v{0, 0, 0, 0};
+        for (int w = 0; w < kWaves; ++w)
+            o += o_lds[wave / kWaves * kWaves + w][x];
+    }
+    if (shown && wave % kWaves == 0 && lane < kLanes) {
         o *= total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f;
-        *(uint2v*)(a.out + token * a.ld_out + head * D + 4 * tid) = uint2v{bf16x2(o[0], o[1]), bf16x2(o[2], o[3])};
-        if (tid == 0 && a.lse)
+        *(uint2v*)(a.out + token * a.ld_out + head * D + 4 * x) = uint2v{bf16x2(o[0], o[1]), bf16x2(o[2], o[3])};
+        if (x == 0 && a.lse)
             a.lse[row] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
     }
 }
@@ -973,9 +986,10 @@ void launch(const Attn& a, int block, hipStream_t stream)
         else
             launch_rows<D, 4>(a, grid, stream);
     }
-    if (a.splits > 1)
-        hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)a.tokens * a.heads), dim3(256), 0, stream, a,
-                           block);
+    if (a.splits > 16)
+        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);
+    else if (a.splits > 1)
+        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)(a.tokens * a.heads + 3) / 4), dim3(256), 0, stream, a);
 }
 
 bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,
@@ -1004,8 +1018,8 @@ extern "C" int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads
         !sizes_supported(tokens, heads, kv_heads, head_dim, num_seqs))
         return -1;
     const Plan p = make_plan(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len, window);
-    // a split's outputs and (maximum, sum) pairs of every row
-    return p.splits > 1 ? tokens * heads * (head_dim + 2) * 4 * p.splits : 0;
+    // a split's outputs and (maximum, sum) pairs of every row, and the rows' splits
+    return p.splits > 1 ? tokens * heads * 4 * ((head_dim + 2) * p.splits + 1) : 0;
 }
 
 extern "C" nvfp4_status_t nvfp4_paged_attention(
