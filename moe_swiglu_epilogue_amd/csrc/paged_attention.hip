@@ -181,30 +181,57 @@ struct Tile {
     uint32_t v[8][C];
     uint32_t ks[C], vs[C];
     bool shown;                                       // this lane's token (lane % 32) counts
-    bool hidden0, hidden1;                            // uniform: a whole half is hidden
 };
 
-// Where a half tile of 16 tokens stands if it lies in one page (page_size a
-// multiple of 16): the slot of its first token, 0 with `hidden` set where the
-// page does not count (its loads then read the cache's first slots).
+// The table entries of a tile's two halves of 16 tokens if each lies in one page
+// (page_size a multiple of 16), -1 behind `last`. Read through the scalar
+// cache (the table does not change while a kernel runs): a vector load of
+// them would have to wait for every load of keys and values before it.
+struct Entries {
+    int e[2];
+};
+
+__device__ __forceinline__ Entries entries_of(const Attn& a, const int32_t* table, int t0, int last)
+{
+    typedef const int32_t __attribute__((address_space(4)))* scalar_ptr;
+    Entries r;
+    for (int hh = 0; hh < 2; ++hh) {
+        const int t = t0 + 16 * hh;
+        const int p = (int)page_of(a, max(t, 0));
+        const bool in = t < last && p < a.max_pages;
+        const int entry = ((scalar_ptr)table)[in ? p : 0];
+        r.e[hh] = in ? entry : -1;
+    }
+    return r;
+}
+
+// The slot of a half's first token; 0 with `hidden` set where its page does not
+// count.
 struct Half {
     int64_t slot;
     bool hidden;
 };
 
-__device__ __forceinline__ Half half_tile(const Attn& a, const int32_t* table, int first, int end)
+__device__ __forceinline__ Half half_tile(const Attn& a, int entry, int first)
 {
-    const int p = (int)page_of(a, first);
-    const int entry = p < a.max_pages && first < end ? table[p] : -1;
     Half h;
     h.hidden = entry < 0 || entry >= a.num_pages;
-    h.slot = h.hidden ? 0 : (int64_t)entry * a.page + (first - p * a.page);
+    h.slot = h.hidden ? 0 : (int64_t)entry * a.page + (first - (int)page_of(a, first) * a.page);
     return h;
 }
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+
+// Loads the tile at t0. kPaged16: codes through a buffer of the half's 16 slots,
+// or of none where it is hidden, which reads as 0 without a memory access; so a
+// tile behind the last one can be requested without a branch. (Scales of a
+// hidden half come from the cache's first slots and are not used.)
 template <int D, bool kPaged16>
-__device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32_t* table, int h,
-                                          int t0, int begin, int end, int lane)
+__device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32_t* table, Entries e,
+                                          int h, int t0, int begin, int end, int lane)
 {
     using T = Tile<D>;
     const int g = lane >> 4, n = lane & 15, tok = lane & 31;
@@ -213,49 +240,65 @@ __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32
     const uint8_t* vp = a.vp + h * (D / 2);
     const uint8_t* ks = a.ks + h * (D / 16);
     const uint8_t* vs = a.vs + h * (D / 16);
-    Half half[2];                  // kPaged16: addresses are a scalar and a lane's fixed offset
-    uint32_t slot = 0;             // else: the slot of this lane's token
+    uint64_t mine;                 // slot of this lane's token
     if (kPaged16) {
-        half[0] = half_tile(a, table, t0, end);
-        half[1] = half_tile(a, table, t0 + 16, end);
-        t.hidden0 = half[0].hidden;
-        t.hidden1 = half[1].hidden;
-        t.shown = !(tok < 16 ? t.hidden0 : t.hidden1);
+        const Half half[2] = {half_tile(a, e.e[0], t0), half_tile(a, e.e[1], t0 + 16)};
+        t.shown = !(tok < 16 ? half[0].hidden : half[1].hidden);
+        mine = (uint64_t)(tok < 16 ? half[0].slot : half[1].slot) + (tok & 15);
+        for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t bytes = half[hh].hidden ? 0 : 16 * row;
+            const __amdgpu_buffer_rsrc_t k = buffer(kp + half[hh].slot * row, bytes);
+            const __amdgpu_buffer_rsrc_t v = buffer(vp + half[hh].slot * row, bytes);
+            for (int c = 0; c < T::C; ++c) {
+                if (D > 64) {
+                    const auto w = __builtin_amdgcn_raw_buffer_load_b128(k, n * row + 16 * g + 64 * c, 0, 0);
+                    for (int i = 0; i < 4; ++i)
+                        t.k[hh][c][i % T::KW] = w[i];
+                } else {
+                    const auto w = __builtin_amdgcn_raw_buffer_load_b64(k, n * row + 8 * g, 0, 0);
+                    t.k[hh][c][0] = w[0];
+                    t.k[hh][c][1] = w[1];
+                }
+                for (int j = 0; j < 4; ++j)
+                    t.v[4 * hh + j][c] =
+                        D > 64 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(v, 4 * g * row + 4 * n + 64 * c, j * row, 0)
+                               : (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(v, 4 * g * row + 2 * n, j * row, 0);
+            }
+        }
     } else {
         const int at = t0 + tok;
         const int p = (int)page_of(a, at);
         const int entry = at < end ? table[p] : -1;
         t.shown = entry >= 0 && entry < a.num_pages;
-        slot = t.shown ? entry * a.page + (at - p * a.page) : 0;
-        t.hidden0 = t.hidden1 = false;
-    }
-    t.shown = t.shown && t0 + tok >= begin && t0 + tok < end;
-    for (int c = 0; c < T::C; ++c) {
-        for (int hh = 0; hh < 2; ++hh) {
-            const uint8_t* from = kPaged16 ? kp + half[hh].slot * row + 64 * c + (n * row + (D > 64 ? 16 : 8) * g)
-                                           : kp + (uint64_t)from_lane(slot, n + 16 * hh) * row + 64 * c + (D > 64 ? 16 : 8) * g;
-            if (D > 64) {
-                const uint4v w = *(const uint4v*)from;
-                for (int i = 0; i < 4; ++i)
-                    t.k[hh][c][i % T::KW] = w[i];
-            } else {
-                const uint2v w = *(const uint2v*)from;
-                t.k[hh][c][0] = w[0];
-                t.k[hh][c][1] = w[1];
+        const uint32_t slot = t.shown ? entry * a.page + (at - p * a.page) : 0;
+        mine = slot;
+        for (int c = 0; c < T::C; ++c) {
+            for (int hh = 0; hh < 2; ++hh) {
+                const uint8_t* from = kp + (uint64_t)from_lane(slot, n + 16 * hh) * row + 64 * c + (D > 64 ? 16 : 8) * g;
+                if (D > 64) {
+                    const uint4v w = *(const uint4v*)from;
+                    for (int i = 0; i < 4; ++i)
+                        t.k[hh][c][i % T::KW] = w[i];
+                } else {
+                    const uint2v w = *(const uint2v*)from;
+                    t.k[hh][c][0] = w[0];
+                    t.k[hh][c][1] = w[1];
+                }
+            }
+            for (int j = 0; j < 8; ++j) {
+                const uint8_t* from = vp + (uint64_t)from_lane(slot, 16 * (j >> 2) + 4 * g + (j & 3)) * row + 64 * c +
+                                      (D > 64 ? 4 : 2) * n;
+                t.v[j][c] = D > 64 ? *(const uint32_t*)from : *(const uint16_t*)from;
             }
         }
-        // scales: a lane takes 4 bytes of its token (the second half of the
-        // wave the next 4), handed to the lanes that need them when used
-        const uint64_t at = (kPaged16 ? (uint64_t)((tok < 16 ? half[0].slot : half[1].slot) + (tok & 15)) : (uint64_t)slot) * srow +
-                            (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
+    }
+    t.shown = t.shown && t0 + tok >= begin && t0 + tok < end;
+    // scales: a lane takes 4 bytes of its token (the second half of the wave the
+    // next 4), handed to the lanes that need them when used
+    for (int c = 0; c < T::C; ++c) {
+        const uint64_t at = mine * srow + (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
         t.ks[c] = *(const uint32_t*)(ks + at);
         t.vs[c] = *(const uint32_t*)(vs + at);
-        for (int j = 0; j < 8; ++j) {
-            const uint8_t* from =
-                kPaged16 ? vp + half[j >> 2].slot * row + (j & 3) * row + 64 * c + (4 * g * row + (D > 64 ? 4 : 2) * n)
-                         : vp + (uint64_t)from_lane(slot, 16 * (j >> 2) + 4 * g + (j & 3)) * row + 64 * c + (D > 64 ? 4 : 2) * n;
-            t.v[j][c] = D > 64 ? *(const uint32_t*)from : *(const uint16_t*)from;
-        }
     }
 }
 
@@ -338,15 +381,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                     o[rt][c][i] = float4v{0, 0, 0, 0};
         }
 
-        int t0 = first + 32 * wave;
-        Tile<D> next;
-        if (t0 < last)
-            load_tile<D, kPaged16>(next, a, table, h, t0, s.begin, s.end, lane);
-        for (; t0 < last; t0 += 128) {
-            Tile<D> t = next;
-            if (t0 + 128 < last)
-                load_tile<D, kPaged16>(next, a, table, h, t0 + 128, s.begin, s.end, lane);
-
+        auto compute = [&](const Tile<D>& t, int t0) {
             // S^T = K Q^T
             float4v sc[RT][2];
             for (int hh = 0; hh < 2; ++hh)
@@ -368,11 +403,8 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
             }
 
             // exponentials: base 2, against the row's lazily raised maximum
-            const bool whole = t0 >= s.all_begin && t0 + 32 <= s.all_end &&
-                               !(kPaged16 ? t.hidden0 || t.hidden1 : __any(!t.shown));
-            uint32_t hid = 0;      // bit j: token j of the tile does not count
-            if (!kPaged16)
-                hid = ~(uint32_t)__ballot(t.shown);
+            const uint32_t hid = ~(uint32_t)__ballot(t.shown);     // bit j: token j does not count
+            const bool whole = hid == 0 && t0 >= s.all_begin && t0 + 32 <= s.all_end;
             half8v p[RT];
             for (int rt = 0; rt < RT; ++rt) {
                 float x[8];
@@ -382,8 +414,7 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                 if (!whole) {
                     for (int i = 0; i < 8; ++i) {
                         const int in = 16 * (i >> 2) + 4 * g + (i & 3);
-                        const bool gone = kPaged16 ? (i < 4 ? t.hidden0 : t.hidden1) : (hid >> in & 1);
-                        if (gone || t0 + in < lo[rt] || t0 + in >= hi[rt])
+                        if ((hid >> in & 1) || t0 + in < lo[rt] || t0 + in >= hi[rt])
                             x[i] = -INFINITY;
                     }
                     top = largest(x);
@@ -428,6 +459,33 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                     for (int rt = 0; rt < RT; ++rt)
                         o[rt][c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[rt][c][i], 0, 0, 0);
                 }
+            }
+        };
+        // Two tiles a wave are in flight, in registers of their own; a tile is
+        // requested as soon as the one before in its registers is used up.
+        auto entries = [&](int t0) { return kPaged16 ? entries_of(a, table, t0, last) : Entries{}; };
+        auto request = [&](Tile<D>& t, Entries e, int t0) {
+            if (!kPaged16 && t0 >= last)
+                return;
+            load_tile<D, kPaged16>(t, a, table, e, h, t0, s.begin, s.end, lane);
+            __builtin_amdgcn_sched_barrier(0);      // no use of the other tile moves up here
+        };
+        int t0 = first + 32 * wave;
+        if (t0 < last) {
+            Tile<D> even, odd;
+            Entries e0 = entries(t0), e1 = entries(t0 + 128);
+            request(even, e0, t0);
+            request(odd, e1, t0 + 128);
+            e0 = entries(t0 + 256);
+            e1 = entries(t0 + 384);
+            for (; t0 < last; t0 += 256) {
+                compute(even, t0);
+                request(even, e0, t0 + 256);
+                e0 = entries(t0 + 512);
+                if (t0 + 128 < last)
+                    compute(odd, t0 + 128);
+                request(odd, e1, t0 + 384);
+                e1 = entries(t0 + 640);
             }
         }
 
@@ -525,7 +583,8 @@ __device__ __forceinline__ void load_part(Part& t, const Attn& a, const int32_t*
     bool shown;
     if (kPaged16) {
         // addresses are a scalar and a lane's fixed offset
-        const Half at[2] = {half_tile(a, table, t0, end), half_tile(a, table, t0 + 16, end)};
+        const Entries e = entries_of(a, table, t0, end);
+        const Half at[2] = {half_tile(a, e.e[0], t0), half_tile(a, e.e[1], t0 + 16)};
         const uint8_t* half[2] = {codes + at[0].slot * row, codes + at[1].slot * row};
         shown = !(tok < 16 ? at[0].hidden : at[1].hidden);
         t.sc = *(const uint32_t*)(scales + (tok < 16 ? at[0].slot : at[1].slot) * srow + (tok & 15) * srow + scale_at);
