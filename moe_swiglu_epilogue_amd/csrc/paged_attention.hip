@@ -302,8 +302,14 @@ __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, const int32
     }
 }
 
+// Waves a SIMD (workgroups a compute unit) that the registers allow without
+// spilling (one row tile of head_dim 128: 62 us for 64 requests with three, 72 with
+// two or four).
 template <int D, int RT, bool kPaged16>
-__global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
+constexpr int kRowsWaves = RT == 1 && D <= 128 && kPaged16 ? 3 : D * RT <= 256 ? 2 : 1;
+
+template <int D, int RT, bool kPaged16>
+__global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_kernel(Attn a)
 {
     using T = Tile<D>;
     constexpr int C = T::C, KF = D / 32, VM = T::VM;
@@ -340,32 +346,55 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
         if (first >= last && split > 0)
             continue;
 
-        // the query rows as the right operand: lane = row, 8 values a register
-        half8v q[RT][KF];
-        float factor[RT];
+        // What is loaded goes out in the order in which it is wanted: table
+        // entries, query rows, the first tiles; then the rows are converted.
+        // Two tiles a wave are in flight, in registers of their own; a tile is
+        // requested as soon as the one before in its registers is used up.
+        auto entries = [&](int t0) { return kPaged16 ? entries_of(a, table, t0, last) : Entries{}; };
+        auto request = [&](Tile<D>& t, Entries e, int t0) {
+            if (!kPaged16 && t0 >= last)
+                return;
+            load_tile<D, kPaged16>(t, a, table, e, h, t0, s.begin, s.end, lane);
+            __builtin_amdgcn_sched_barrier(0);      // no use of the other tile moves up here
+        };
+        int t0 = first + 32 * wave;
+        Entries e0 = entries(t0), e1 = entries(t0 + 128);
+
+        uint4v w[RT][KF];
         int lo[RT], hi[RT];
         for (int rt = 0; rt < RT; ++rt) {
             const int r = row0 + 16 * rt + n;
             lo[rt] = hi[rt] = 0;
-            uint4v w[KF];
+            // a row behind the last one: the last one's values, nothing to see
+            const int rr = min(r, s.rows - 1);
+            const uint16_t* src = a.q + (s.first + rr / group) * a.ld_q + (h * group + rr % group) * D;
+            for (int f = 0; f < KF; ++f) {
+                // D > 64: chunk f / 4, dimensions 32 g + 8 (f % 4); else 16 g + 8 f
+                const int d = D > 64 ? 128 * (f / 4) + 32 * g + 8 * (f % 4) : 16 * g + 8 * f;
+                w[rt][f] = *(const uint4v*)(src + d);
+            }
+            if (r < s.rows)
+                sees(a, s.len, s.rows / group, r / group, lo[rt], hi[rt]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        Tile<D> even, odd;
+        request(even, e0, t0);
+        request(odd, e1, t0 + 128);
+        e0 = entries(t0 + 256);
+        e1 = entries(t0 + 384);
+
+        // the query rows as the right operand: lane = row, 8 values a register
+        half8v q[RT][KF];
+        float factor[RT];
+        for (int rt = 0; rt < RT; ++rt) {
             uint32_t top = 0;
             for (int f = 0; f < KF; ++f)
-                w[f] = uint4v{0, 0, 0, 0};
-            if (r < s.rows) {
-                const uint16_t* src = a.q + (s.first + r / group) * a.ld_q + (h * group + r % group) * D;
-                for (int f = 0; f < KF; ++f) {
-                    // D > 64: chunk f / 4, dimensions 32 g + 8 (f % 4); else 16 g + 8 f
-                    const int d = D > 64 ? 128 * (f / 4) + 32 * g + 8 * (f % 4) : 16 * g + 8 * f;
-                    w[f] = *(const uint4v*)(src + d);
-                    top = largest_bits(w[f], top);
-                }
-                sees(a, s.len, s.rows / group, r / group, lo[rt], hi[rt]);
-            }
+                top = largest_bits(w[rt][f], top);
             top = max(top, (uint32_t)__shfl_xor((int)top, 16));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
             const int e = fp16_exponent(top);
             for (int f = 0; f < KF; ++f)
-                q[rt][f] = scaled_half8(w[f], e, k_scale < 0);
+                q[rt][f] = scaled_half8(w[rt][f], e, k_scale < 0);
             // positive, so that the largest product gives the largest score, and
             // not 0, which would turn a hidden token's -inf into NaN
             factor[rt] = fmaxf(ldexpf(fabsf(k_scale), -e), 0x1p-126f);
@@ -461,32 +490,14 @@ __global__ __launch_bounds__(256) void attn_rows_kernel(Attn a)
                 }
             }
         };
-        // Two tiles a wave are in flight, in registers of their own; a tile is
-        // requested as soon as the one before in its registers is used up.
-        auto entries = [&](int t0) { return kPaged16 ? entries_of(a, table, t0, last) : Entries{}; };
-        auto request = [&](Tile<D>& t, Entries e, int t0) {
-            if (!kPaged16 && t0 >= last)
-                return;
-            load_tile<D, kPaged16>(t, a, table, e, h, t0, s.begin, s.end, lane);
-            __builtin_amdgcn_sched_barrier(0);      // no use of the other tile moves up here
-        };
-        int t0 = first + 32 * wave;
-        if (t0 < last) {
-            Tile<D> even, odd;
-            Entries e0 = entries(t0), e1 = entries(t0 + 128);
-            request(even, e0, t0);
-            request(odd, e1, t0 + 128);
-            e0 = entries(t0 + 256);
-            e1 = entries(t0 + 384);
-            for (; t0 < last; t0 += 256) {
-                compute(even, t0);
-                request(even, e0, t0 + 256);
-                e0 = entries(t0 + 512);
-                if (t0 + 128 < last)
-                    compute(odd, t0 + 128);
-                request(odd, e1, t0 + 384);
-                e1 = entries(t0 + 640);
-            }
+        for (; t0 < last; t0 += 256) {
+            compute(even, t0);
+            request(even, e0, t0 + 256);
+            e0 = entries(t0 + 512);
+            if (t0 + 128 < last)
+                compute(odd, t0 + 128);
+            request(odd, e1, t0 + 384);
+            e1 = entries(t0 + 640);
         }
 
         // Join the four waves, a row tile at a time.
@@ -696,9 +707,11 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
     const int group = a.heads / a.kv_heads;
     // each request's blocks from its end: those with the most tokens to see go
     // first, and the short ones fill up the end
-    const int pairs = a.num_seqs * a.kv_heads;
-    const int h = blockIdx.x % a.kv_heads, b = blockIdx.x % pairs / a.kv_heads;
-    const int split = blockIdx.x / pairs % a.splits;
+    // Workgroups go to the 8 XCDs in turn: requests and heads rotate from one
+    // block to the next, so that a long request's do not share an XCD.
+    const int pairs = a.num_seqs * a.kv_heads, turn = blockIdx.x / pairs;
+    const int pair = (blockIdx.x + turn) % pairs, h = pair % a.kv_heads, b = pair / a.kv_heads;
+    const int split = turn % a.splits;
     Span s = request_span(a, b, group);
     const int32_t* table = a.table + b * a.ld_table;
     const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
@@ -706,7 +719,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
     const bool values = wave >= 4;
     const int grp = wave % P::kGroups, chunk = D > 128 ? (wave & 3) >> 1 : 0;
 
-    for (int row0 = (s.rows - 1) / kRows * kRows - blockIdx.x / pairs / a.splits * kRows; row0 >= 0 && s.rows > 0;
+    for (int row0 = ((s.rows - 1) / kRows - turn / a.splits) * kRows; row0 >= 0 && s.rows > 0;
          row0 -= a.row_blocks * kRows) {
         block_span(a, s, group, row0, kRows);
         const int first = s.begin + split * s.chunk;
@@ -990,14 +1003,16 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
     if (window > 0 && window + max_query_len + 32 < range)
         range = window + max_query_len + 32;
     const int64_t items = (num_seqs < 1 ? 1 : num_seqs) * kv_heads * p.row_blocks;
-    // Enough workgroups to fill the card, four a compute unit (prompt kernel:
-    // one); for few rows also splits short enough that ragged requests balance.
+    // One round of workgroups on the card's 256 compute units, as many on each
+    // as its registers hold, by splits of at least `shortest` tokens; for few rows
+    // also splits short enough that ragged requests balance (prompt kernel: half
+    // as many workgroups again, as most blocks see less than the longest).
     const bool prompt = p.block == 256;
-    int64_t want = ceil_div((int64_t)(prompt ? 256 : 1024), items);
-    if (!prompt && want < ceil_div(range, (int64_t)1024))
-        want = ceil_div(range, (int64_t)1024);
-    int64_t splits = want;
+    const int64_t slots = prompt ? 384 : 256 * (p.block == 16 && head_dim <= 128 ? 3 : head_dim * p.block <= 4096 ? 2 : 1);
     const int64_t shortest = prompt ? 1024 : 128;
+    int64_t splits = slots / items < 1 ? 1 : slots / items;
+    if (!prompt && splits < ceil_div(range, (int64_t)2048))
+        splits = ceil_div(range, (int64_t)2048);
     if (splits > ceil_div(range < 1 ? 1 : range, shortest))
         splits = ceil_div(range < 1 ? 1 : range, shortest);
     if (splits > 256)
