@@ -53,9 +53,14 @@ def raw():
 
 
 # ---- marshalling helpers -----------------------------------------------------
+# A decoding step makes these calls for a few microseconds of GPU work each, so
+# the checks below are written to be cheap: identity of dtypes, one comparison
+# of shapes, and torch's raw stream handle in place of a Stream object.
 _ptr = _b._ptr
 _pitch = _b._pitch
-_call = _b._call
+Nvfp4Error = _b.Nvfp4Error
+_empty = torch.empty
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
 @contextlib.contextmanager
@@ -74,11 +79,17 @@ def _elsewhere(device, stream):
                 yield stream.cuda_stream
 
 
-def _launch(device, stream):
-    """Context of the allocations and the launch; gives the raw stream."""
+def _current(device, stream):
+    """torch's raw current stream where nothing has to be set or restored for a
+    launch on `device`, else None (the default stream's handle is 0)."""
     if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(torch.cuda.current_stream(device).cuda_stream)
-    return _elsewhere(device, stream)
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
+
+
+def _check(status, what):
+    if status != 0:
+        raise Nvfp4Error(status, what)
 
 
 def _cuda(t, name):
@@ -88,46 +99,52 @@ def _cuda(t, name):
 
 
 def _vector(t, name, dtype, device, n=None):
-    if t.dtype != dtype or t.device != device or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.dim() != 1 or not t.is_contiguous():
         raise TypeError("%s must be a contiguous 1-D %s tensor on the input's device" % (name, dtype))
     if n is not None and t.numel() != n:
         raise ValueError("%s must hold %d values" % (name, n))
-    return t
+    return t.data_ptr()
 
 
 def _scalar(t, name, dtype, device):
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or t.numel() != 1:
+    if t.dtype is not dtype or t.device != device or t.numel() != 1:
         raise TypeError("%s must be a %s tensor of one value on the input's device" % (name, dtype))
-    return t
+    return t.data_ptr()
 
 
 def _new(t, shape, dtype, device, name):
-    return torch.empty(shape, dtype=dtype, device=device) if t is None else _b._out(t, shape, dtype, device, name)
+    return _empty(shape, dtype=dtype, device=device) if t is None else _b._out(t, shape, dtype, device, name)
 
 
 def _table(t, rows, device):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise TypeError("block_table must be a 2-D int32 tensor with unit column stride on the input's device")
-    if t.shape[0] != rows:
+    """Row pitch and columns of a block table."""
+    if t.dtype is not _I32 or t.device != device or t.dim() != 2:
+        raise TypeError("block_table must be a 2-D int32 tensor on the input's device")
+    n, width = t.shape
+    if n != rows:
         raise ValueError("block_table must have one row per request")
-    pitch = t.stride(0) if rows > 1 else t.shape[1]
-    if pitch < t.shape[1]:
+    if t.is_contiguous():
+        return width, width
+    if width > 1 and t.stride(1) != 1:
+        raise TypeError("block_table must have unit column stride")
+    pitch = t.stride(0) if rows > 1 else width
+    if pitch < width:
         raise ValueError("block_table's rows must not overlap")
-    return pitch
+    return pitch, width
 
 
 def _workspace(t, need, device):
+    """The workspace's tensor (to be kept until the launch), pointer and bytes."""
     if t is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+        if need <= 0:
+            return None, None, 0
+        t = _empty(need, dtype=_U8, device=device)
+        return t, t.data_ptr(), need
     if t.device != device or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
-    return t
-
-
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+    return t, t.data_ptr(), t.numel() * t.element_size()
 
 
 # ---- entry points --------------------------------------------------------------
@@ -144,41 +161,64 @@ def kv_block_tables(context_lens: torch.Tensor | None, query_lens: torch.Tensor,
     already). Returns (slots int64 [max_tokens], -1 behind the last token;
     query_offsets int32 [B + 1]; seq_lens int32 [B]; free_end int32 [1])."""
     device = _cuda(query_lens, "query_lens")
-    _vector(query_lens, "query_lens", torch.int32, device)
+    query = _vector(query_lens, "query_lens", _I32, device)
     n = query_lens.numel()
-    if context_lens is not None:
-        _vector(context_lens, "context_lens", torch.int32, device, n)
-    ld = _table(block_table, n, device)
+    context = None if context_lens is None else _vector(context_lens, "context_lens", _I32, device, n)
+    ld, width = _table(block_table, n, device)
+    free, num_free = None, -1
     if free_pages is not None:
-        _vector(free_pages, "free_pages", torch.int32, device)
-    _scalar(free_begin, "free_begin", torch.int32, device)
+        free, num_free = _vector(free_pages, "free_pages", _I32, device), free_pages.numel()
+    begin = _scalar(free_begin, "free_begin", _I32, device)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    with _launch(device, stream) as st:
-        slots = _new(slots, (max_tokens,), torch.int64, device, "slots")
-        query_offsets = _new(query_offsets, (n + 1,), torch.int32, device, "query_offsets")
-        seq_lens = _new(seq_lens, (n,), torch.int32, device, "seq_lens")
-        free_end = _new(free_end, (1,), torch.int32, device, "free_end")
-        if n and (seq_lens.data_ptr() in (query_lens.data_ptr(), 0 if context_lens is None else context_lens.data_ptr())
-                  or (free_begin is not None and free_end.data_ptr() == free_begin.data_ptr())):
+
+    def launch(st, slots, query_offsets, seq_lens, free_end):
+        if slots is None:
+            slots = _empty(max_tokens, dtype=_I64, device=device)
+        else:
+            _b._out(slots, (max_tokens,), _I64, device, "slots")
+        if query_offsets is None and seq_lens is None and free_end is None:
+            query_offsets, seq_lens, free_end = _empty(2 * n + 2, dtype=_I32, device=device).split_with_sizes((n + 1, n, 1))
+        else:
+            query_offsets = _new(query_offsets, (n + 1,), _I32, device, "query_offsets")
+            seq_lens = _new(seq_lens, (n,), _I32, device, "seq_lens")
+            free_end = _new(free_end, (1,), _I32, device, "free_end")
+        lens, end = seq_lens.data_ptr(), free_end.data_ptr()
+        if n and (lens == query or lens == context or end == begin):
             raise ValueError("outputs must not share memory with the lengths or free_begin")
-        _call(_lib().kv_block_tables, "kv_block_tables", _ptr(context_lens), query_lens.data_ptr(), n,
-              page_size, _ptr(free_pages), -1 if free_pages is None else free_pages.numel(), _ptr(free_begin),
-              block_table.data_ptr(), ld, block_table.shape[1], query_offsets.data_ptr(), seq_lens.data_ptr(),
-              slots.data_ptr(), max_tokens, free_end.data_ptr(), st)
-    return slots, query_offsets, seq_lens, free_end
+        _check(_lib().kv_block_tables(context, query, n, page_size, free, num_free, begin, block_table.data_ptr(), ld, width,
+                                      query_offsets.data_ptr(), lens, slots.data_ptr(), max_tokens, end, st),
+               "kv_block_tables")
+        return slots, query_offsets, seq_lens, free_end
+
+    st = _current(device, stream)
+    if st is not None:
+        return launch(st, slots, query_offsets, seq_lens, free_end)
+    with _elsewhere(device, stream) as st:
+        return launch(st, slots, query_offsets, seq_lens, free_end)
 
 
 def _heads(t, name, device):
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 3:
+    """Pitch of the rows of [tokens, heads, head_dim]."""
+    if t.dtype is not _BF16 or t.device != device or t.dim() != 3:
         raise TypeError("%s must be a bfloat16 tensor [tokens, heads, head_dim] on the input's device" % name)
     n, h, d = t.shape
+    if t.is_contiguous():
+        return h * d
     if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
         raise ValueError("%s must have packed heads (only the token stride is free)" % name)
     pitch = t.stride(0) if n > 1 else h * d
     if pitch < h * d:
         raise ValueError("%s's rows must not overlap" % name)
     return pitch
+
+
+def _codes(t, name, device, shape):
+    if t.dtype is not _U8 or t.device != device or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous uint8 tensor on the input's device" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s" % (name, shape))
+    return t.data_ptr()
 
 
 def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor,
@@ -202,52 +242,61 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
     device = _cuda(q, "q")
     ld_q = _heads(q, "q", device)
     tokens, heads, dim = q.shape
-    for t, name, w in ((k_packed, "k_packed", 2), (k_scales, "k_scales", 16), (v_packed, "v_packed", 2),
-                       (v_scales, "v_scales", 16)):
-        if t.dtype != torch.uint8 or t.device != device or t.dim() != 2 or not t.is_contiguous():
-            raise TypeError("%s must be a contiguous 2-D uint8 tensor on the input's device" % name)
-        if t.shape[0] != k_packed.shape[0] or t.shape[1] != kv_heads * dim // w:
-            raise ValueError("%s must be [num_slots, kv_heads * head_dim / %d]" % (name, w))
-    num_slots = k_packed.shape[0]
-    _vector(seq_lens, "seq_lens", torch.int32, device)
+    if k_packed.dim() != 2:
+        raise ValueError("k_packed must be [num_slots, kv_heads * head_dim / 2]")
+    slots, cols = k_packed.shape[0], kv_heads * dim
+    codes, scales = (slots, cols // 2), (slots, cols // 16)
+    kp = _codes(k_packed, "k_packed", device, codes)
+    ks = _codes(k_scales, "k_scales", device, scales)
+    vp = _codes(v_packed, "v_packed", device, codes)
+    vs = _codes(v_scales, "v_scales", device, scales)
+    lens = _vector(seq_lens, "seq_lens", _I32, device)
     n = seq_lens.numel()
-    _vector(query_offsets, "query_offsets", torch.int32, device, n + 1)
-    ld_table = _table(block_table, n, device)
-    max_pages = block_table.shape[1]
-    _scalar(k_gs, "k_gs", torch.float32, device)
-    _scalar(v_gs, "v_gs", torch.float32, device)
+    offsets = _vector(query_offsets, "query_offsets", _I32, device, n + 1)
+    ld_table, max_pages = _table(block_table, n, device)
+    kg = _scalar(k_gs, "k_gs", _F32, device)
+    vg = _scalar(v_gs, "v_gs", _F32, device)
     if max_seq_len is None:
         max_seq_len = max_pages * page_size
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
     L = _lib()
     need = L.nvfp4_paged_attention_workspace(tokens, heads, kv_heads, dim, n, max_query_len, max_seq_len, window)
-    with _launch(device, stream) as st:
+
+    def launch(st, out, lse):
         if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=device)
-        ld_out = _heads(out, "out", device)
-        if out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        z = None
-        if lse is True:
-            z = torch.empty((tokens, heads), dtype=torch.float32, device=device)
-        elif isinstance(lse, torch.Tensor):
-            z = _b._out(lse, (tokens, heads), torch.float32, device, "lse")
-        work = _workspace(workspace, need, device)
-        _call(L.nvfp4_paged_attention, "nvfp4_paged_attention", q.data_ptr(), tokens, ld_q, heads, kv_heads, dim,
-              k_packed.data_ptr(), k_scales.data_ptr(), v_packed.data_ptr(), v_scales.data_ptr(), num_slots,
-              page_size, block_table.data_ptr(), ld_table, max_pages, seq_lens.data_ptr(),
-              query_offsets.data_ptr(), n, max_query_len, max_seq_len, scale, int(causal), window, _ptr(k_gs),
-              _ptr(v_gs), out.data_ptr(), ld_out, _ptr(z), _ptr(work), _bytes(work), st)
-    return out if z is None else (out, z)
+            out = _empty((tokens, heads, dim), dtype=_BF16, device=device)
+            ld_out = heads * dim
+        else:
+            ld_out = _heads(out, "out", device)
+            if out.shape != q.shape:
+                raise ValueError("out must have q's shape")
+        zp = None
+        if lse is None or lse is False:
+            lse = None
+        else:
+            lse = _new(None if lse is True else lse, (tokens, heads), _F32, device, "lse")
+            zp = lse.data_ptr()
+        work, wp, size = _workspace(workspace, need, device)
+        _check(L.nvfp4_paged_attention(q.data_ptr(), tokens, ld_q, heads, kv_heads, dim, kp, ks, vp, vs, slots, page_size,
+                                       block_table.data_ptr(), ld_table, max_pages, lens, offsets, n, max_query_len,
+                                       max_seq_len, scale, 1 if causal else 0, window, kg, vg, out.data_ptr(), ld_out, zp,
+                                       wp, size, st), "nvfp4_paged_attention")
+        return out if lse is None else (out, lse)
+
+    st = _current(device, stream)
+    if st is not None:
+        return launch(st, out, lse)
+    with _elsewhere(device, stream) as st:
+        return launch(st, out, lse)
 
 
-def _matrix(t, name, dtype, device, shape):
-    if t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous %s tensor on the input's device" % (name, dtype))
-    if tuple(t.shape) != shape:
+def _bf16_weights(t, name, device, shape):
+    if t.dtype is not _BF16 or t.device != device or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous bfloat16 tensor on the input's device" % name)
+    if t.shape != shape:
         raise ValueError("%s must have shape %s" % (name, shape))
-    return t
+    return t.data_ptr()
 
 
 def _moe(fn, what, x, logits, top_k, inter, weights, renormalize, out, topk_ids, topk_weights, workspace, stream):
@@ -255,28 +304,36 @@ def _moe(fn, what, x, logits, top_k, inter, weights, renormalize, out, topk_ids,
     tokens, hidden = x.shape
     experts = logits.shape[1]
     need = _lib().moe_layer_workspace(tokens, hidden, inter, experts, top_k)
-    with _launch(device, stream) as st:
+
+    def launch(st, out, topk_ids, topk_weights):
         if out is None:
-            out = torch.empty((tokens, hidden), dtype=torch.bfloat16, device=device)
-        if (out.dtype != torch.bfloat16 or out.device != device or tuple(out.shape) != (tokens, hidden)
-                or (hidden > 1 and out.stride(1) != 1)):
+            out = _empty((tokens, hidden), dtype=_BF16, device=device)
+        elif (out.dtype is not _BF16 or out.device != device or out.shape != (tokens, hidden)
+              or (hidden > 1 and out.stride(1) != 1)):
             raise ValueError("out must be a bfloat16 tensor of shape (tokens, hidden) with unit column stride")
-        topk_ids = _new(topk_ids, (tokens, max(top_k, 0)), torch.int32, device, "topk_ids")
-        topk_weights = _new(topk_weights, (tokens, max(top_k, 0)), torch.float32, device, "topk_weights")
-        work = _workspace(workspace, need, device)
-        _call(fn, what, x.data_ptr(), tokens, _pitch(x), logits.data_ptr(), *[_ptr(w) for w in weights], hidden,
-              inter, experts, top_k, int(renormalize), out.data_ptr(), _pitch(out), topk_ids.data_ptr(),
-              topk_weights.data_ptr(), _ptr(work), _bytes(work), st)
-    return out, topk_ids, topk_weights
+        topk_ids = _new(topk_ids, (tokens, max(top_k, 0)), _I32, device, "topk_ids")
+        topk_weights = _new(topk_weights, (tokens, max(top_k, 0)), _F32, device, "topk_weights")
+        work, wp, size = _workspace(workspace, need, device)
+        _check(fn(x.data_ptr(), tokens, _pitch(x), logits.data_ptr(), *weights, hidden, inter, experts, top_k,
+                  1 if renormalize else 0, out.data_ptr(), _pitch(out), topk_ids.data_ptr(), topk_weights.data_ptr(), wp,
+                  size, st), what)
+        return out, topk_ids, topk_weights
+
+    st = _current(device, stream)
+    if st is not None:
+        return launch(st, out, topk_ids, topk_weights)
+    with _elsewhere(device, stream) as st:
+        return launch(st, out, topk_ids, topk_weights)
 
 
 def _moe_inputs(x, logits):
     device = _cuda(x, "x")
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    if x.dtype is not _BF16 or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise TypeError("x must be a 2-D bfloat16 tensor with unit column stride")
     if logits.dim() != 2 or logits.shape[0] != x.shape[0]:
         raise ValueError("logits must be [tokens, num_experts]")
-    _matrix(logits, "logits", torch.float32, device, tuple(logits.shape))
+    if logits.dtype is not _F32 or logits.device != device or not logits.is_contiguous():
+        raise TypeError("logits must be a contiguous float32 tensor on x's device")
     return device
 
 
@@ -297,17 +354,14 @@ def moe_layer_nvfp4(x: torch.Tensor, logits: torch.Tensor, w1_packed: torch.Tens
     if w1_packed.dim() != 3 or w1_packed.shape[1] % 2:
         raise ValueError("w1_packed must be [E, 2I, H / 2]")
     inter = w1_packed.shape[1] // 2
-    for t, name, shape in ((w1_packed, "w1_packed", (e, 2 * inter, hidden // 2)),
-                           (w1_scales, "w1_scales", (e, 2 * inter, hidden // 16)),
-                           (w2_packed, "w2_packed", (e, hidden, inter // 2)),
-                           (w2_scales, "w2_scales", (e, hidden, inter // 16))):
-        _matrix(t, name, torch.uint8, device, shape)
-    for t, name in ((gs1, "gs1"), (gs2, "gs2")):
-        if t is not None:
-            _vector(t, name, torch.float32, device, e)
-    return _moe(_lib().moe_layer_nvfp4, "moe_layer_nvfp4", x, logits, top_k, inter,
-                (w1_packed, w1_scales, gs1, w2_packed, w2_scales, gs2), renormalize, out, topk_ids, topk_weights,
-                workspace, stream)
+    weights = (_codes(w1_packed, "w1_packed", device, (e, 2 * inter, hidden // 2)),
+               _codes(w1_scales, "w1_scales", device, (e, 2 * inter, hidden // 16)),
+               None if gs1 is None else _vector(gs1, "gs1", _F32, device, e),
+               _codes(w2_packed, "w2_packed", device, (e, hidden, inter // 2)),
+               _codes(w2_scales, "w2_scales", device, (e, hidden, inter // 16)),
+               None if gs2 is None else _vector(gs2, "gs2", _F32, device, e))
+    return _moe(_lib().moe_layer_nvfp4, "moe_layer_nvfp4", x, logits, top_k, inter, weights, renormalize, out, topk_ids,
+                topk_weights, workspace, stream)
 
 
 def moe_layer_bf16(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor, top_k: int, *,
@@ -321,7 +375,6 @@ def moe_layer_bf16(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w2: 
     if w1.dim() != 3 or w1.shape[1] % 2:
         raise ValueError("w1 must be [E, 2I, H]")
     inter = w1.shape[1] // 2
-    _matrix(w1, "w1", torch.bfloat16, device, (e, 2 * inter, hidden))
-    _matrix(w2, "w2", torch.bfloat16, device, (e, hidden, inter))
-    return _moe(_lib().moe_layer_bf16, "moe_layer_bf16", x, logits, top_k, inter, (w1, w2), renormalize, out, topk_ids,
+    weights = (_bf16_weights(w1, "w1", device, (e, 2 * inter, hidden)), _bf16_weights(w2, "w2", device, (e, hidden, inter)))
+    return _moe(_lib().moe_layer_bf16, "moe_layer_bf16", x, logits, top_k, inter, weights, renormalize, out, topk_ids,
                 topk_weights, workspace, stream)
