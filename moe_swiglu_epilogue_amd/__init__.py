@@ -21,9 +21,11 @@ _SERVING = ("kv_block_tables", "nvfp4_paged_attention", "moe_layer_nvfp4", "moe_
 
 def __getattr__(name):
     if name == "serving" or name in _SERVING:
-        serving = importlib.import_module(__name__ + ".serving")
-        return serving if name == "serving" else getattr(serving, name)
-    if name == "binding" or name in __all__:
-        binding = importlib.import_module(__name__ + ".binding")
-        return binding if name == "binding" else getattr(binding, name)
-    raise AttributeError(name)
+        module = importlib.import_module(__name__ + ".serving")
+    elif name == "binding" or name in __all__:
+        module = importlib.import_module(__name__ + ".binding")
+    else:
+        raise AttributeError(name)
+    value = module if name in ("binding", "serving") else getattr(module, name)
+    globals()[name] = value      # found at once from now on
+    return value

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import math
 
 import torch
@@ -104,6 +105,20 @@ def _vector(t, name, dtype, device, n=None):
     if n is not None and t.numel() != n:
         raise ValueError("%s must hold %d values" % (name, n))
     return t.data_ptr()
+
+
+def _all(tensors, names, dtype, device, shapes):
+    """Pointers of contiguous tensors of one dtype with these shapes."""
+    for t, shape in zip(tensors, shapes):
+        if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+            break
+    else:
+        return [t.data_ptr() for t in tensors]
+    for t, name, shape in zip(tensors, names, shapes):
+        if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+            raise TypeError("%s must be a contiguous %s tensor on the input's device" % (name, dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s" % (name, shape))
 
 
 def _scalar(t, name, dtype, device):
@@ -213,12 +228,14 @@ def _heads(t, name, device):
     return pitch
 
 
-def _codes(t, name, device, shape):
-    if t.dtype is not _U8 or t.device != device or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous uint8 tensor on the input's device" % name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s" % (name, shape))
-    return t.data_ptr()
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(*sizes):
+    return _lib().nvfp4_paged_attention_workspace(*sizes)
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_workspace(*sizes):
+    return _lib().moe_layer_workspace(*sizes)
 
 
 def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor,
@@ -246,10 +263,8 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
         raise ValueError("k_packed must be [num_slots, kv_heads * head_dim / 2]")
     slots, cols = k_packed.shape[0], kv_heads * dim
     codes, scales = (slots, cols // 2), (slots, cols // 16)
-    kp = _codes(k_packed, "k_packed", device, codes)
-    ks = _codes(k_scales, "k_scales", device, scales)
-    vp = _codes(v_packed, "v_packed", device, codes)
-    vs = _codes(v_scales, "v_scales", device, scales)
+    kp, ks, vp, vs = _all((k_packed, k_scales, v_packed, v_scales), ("k_packed", "k_scales", "v_packed", "v_scales"), _U8,
+                          device, (codes, scales, codes, scales))
     lens = _vector(seq_lens, "seq_lens", _I32, device)
     n = seq_lens.numel()
     offsets = _vector(query_offsets, "query_offsets", _I32, device, n + 1)
@@ -261,7 +276,7 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
     L = _lib()
-    need = L.nvfp4_paged_attention_workspace(tokens, heads, kv_heads, dim, n, max_query_len, max_seq_len, window)
+    need = _attention_workspace(tokens, heads, kv_heads, dim, n, max_query_len, max_seq_len, window)
 
     def launch(st, out, lse):
         if out is None:
@@ -291,19 +306,11 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
         return launch(st, out, lse)
 
 
-def _bf16_weights(t, name, device, shape):
-    if t.dtype is not _BF16 or t.device != device or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous bfloat16 tensor on the input's device" % name)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s" % (name, shape))
-    return t.data_ptr()
-
-
 def _moe(fn, what, x, logits, top_k, inter, weights, renormalize, out, topk_ids, topk_weights, workspace, stream):
     device = x.device
     tokens, hidden = x.shape
     experts = logits.shape[1]
-    need = _lib().moe_layer_workspace(tokens, hidden, inter, experts, top_k)
+    need = _moe_workspace(tokens, hidden, inter, experts, top_k)
 
     def launch(st, out, topk_ids, topk_weights):
         if out is None:
@@ -354,12 +361,11 @@ def moe_layer_nvfp4(x: torch.Tensor, logits: torch.Tensor, w1_packed: torch.Tens
     if w1_packed.dim() != 3 or w1_packed.shape[1] % 2:
         raise ValueError("w1_packed must be [E, 2I, H / 2]")
     inter = w1_packed.shape[1] // 2
-    weights = (_codes(w1_packed, "w1_packed", device, (e, 2 * inter, hidden // 2)),
-               _codes(w1_scales, "w1_scales", device, (e, 2 * inter, hidden // 16)),
-               None if gs1 is None else _vector(gs1, "gs1", _F32, device, e),
-               _codes(w2_packed, "w2_packed", device, (e, hidden, inter // 2)),
-               _codes(w2_scales, "w2_scales", device, (e, hidden, inter // 16)),
-               None if gs2 is None else _vector(gs2, "gs2", _F32, device, e))
+    w1p, w1s, w2p, w2s = _all((w1_packed, w1_scales, w2_packed, w2_scales), ("w1_packed", "w1_scales", "w2_packed", "w2_scales"),
+                              _U8, device, ((e, 2 * inter, hidden // 2), (e, 2 * inter, hidden // 16),
+                                            (e, hidden, inter // 2), (e, hidden, inter // 16)))
+    weights = (w1p, w1s, None if gs1 is None else _vector(gs1, "gs1", _F32, device, e),
+               w2p, w2s, None if gs2 is None else _vector(gs2, "gs2", _F32, device, e))
     return _moe(_lib().moe_layer_nvfp4, "moe_layer_nvfp4", x, logits, top_k, inter, weights, renormalize, out, topk_ids,
                 topk_weights, workspace, stream)
 
@@ -375,6 +381,6 @@ def moe_layer_bf16(x: torch.Tensor, logits: torch.Tensor, w1: torch.Tensor, w2: 
     if w1.dim() != 3 or w1.shape[1] % 2:
         raise ValueError("w1 must be [E, 2I, H]")
     inter = w1.shape[1] // 2
-    weights = (_bf16_weights(w1, "w1", device, (e, 2 * inter, hidden)), _bf16_weights(w2, "w2", device, (e, hidden, inter)))
+    weights = _all((w1, w2), ("w1", "w2"), _BF16, device, ((e, 2 * inter, hidden), (e, hidden, inter)))
     return _moe(_lib().moe_layer_bf16, "moe_layer_bf16", x, logits, top_k, inter, weights, renormalize, out, topk_ids,
                 topk_weights, workspace, stream)
