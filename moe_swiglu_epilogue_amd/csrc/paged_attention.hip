@@ -151,6 +151,13 @@ __device__ __forceinline__ uint32_t largest_bits(uint4v w, uint32_t top)
     return top;
 }
 
+// The bits from, ..., to - 1 of 32.
+__device__ __forceinline__ uint32_t bits_between(int from, int to)
+{
+    const uint32_t below_to = to <= 0 ? 0 : ~0u >> (32 - min(to, 32));
+    return from >= 32 ? 0 : below_to & (~0u << max(from, 0));
+}
+
 // ---- few query rows ----------------------------------------------------------
 // One workgroup per (request, block of 16 RT query rows, key/value head,
 // split of the tokens); query rows are tokens x the heads that share the
@@ -441,10 +448,10 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
                     x[i] = sc[rt][i >> 2][i & 3];
                 float top = largest(x);
                 if (!whole) {
+                    const uint32_t seen = ~hid & bits_between(lo[rt] - t0, hi[rt] - t0);
                     for (int i = 0; i < 8; ++i) {
                         const int in = 16 * (i >> 2) + 4 * g + (i & 3);
-                        if ((hid >> in & 1) || t0 + in < lo[rt] || t0 + in >= hi[rt])
-                            x[i] = -INFINITY;
+                        x[i] = seen >> in & 1 ? x[i] : -INFINITY;
                     }
                     top = largest(x);
                 }
@@ -823,11 +830,11 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                     top = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < N; ++t) {
+                        const uint32_t seen = shown[t] & bits_between(lo - ts - 32 * t, hi - ts - 32 * t);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const int in = 8 * (j >> 2) + 4 * half + (j & 3);
-                            if (!(shown[t] >> in & 1) || ts + 32 * t + in < lo || ts + 32 * t + in >= hi)
-                                sc[t][j] = -INFINITY;
+                            sc[t][j] = seen >> in & 1 ? sc[t][j] : -INFINITY;
                         }
                         top = fmaxf(top, largest(sc[t]));
                     }
