@@ -700,11 +700,36 @@ __device__ __forceinline__ void store_part(const Part& t, _Float16* keys, _Float
     }
 }
 
+// count matrix instructions, each with an operand read from LDS, `ahead` reads in
+// flight before each; left alone, the compiler waits for every read right behind
+// it. Vector and scalar arithmetic may move between them.
+template <int count, int ahead, typename Read, typename Use>
+__device__ __forceinline__ void in_turn(Read read, Use use)
+{
+    constexpr int kArithmetic = 0x6;
+    half8v ring[ahead];
+#pragma unroll
+    for (int x = 0; x < ahead; ++x)
+        ring[x] = read(x);
+    __builtin_amdgcn_sched_barrier(kArithmetic);
+#pragma unroll
+    for (int x = 0; x < count; ++x) {
+        use(x, ring[x % ahead]);
+        if (x + ahead < count)
+            ring[x % ahead] = read(x + ahead);
+        __builtin_amdgcn_sched_barrier(kArithmetic);
+    }
+}
+
 template <int D, bool kPaged16>
 __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
 {
     using P = Prompt<D>;
     constexpr int kRows = 256, KF = D / 16, MT = D / 32;
+    // head_dim 256 has no registers left for more: spilled values are loaded back
+    // behind the tile that is in flight, and wait for it (16000 cached tokens, 2000
+    // rows of 16 heads: 494 us; two and four reads 524, three and three 580)
+    constexpr int kKeysAhead = D > 128 ? 1 : 6, kValsAhead = D > 128 ? 2 : 6;
     __shared__ __attribute__((aligned(16))) _Float16 keys[2][P::kTokens * P::kKeyPitch];
     __shared__ __attribute__((aligned(16))) _Float16 vals[2][P::kVals];
     __shared__ uint32_t shown_lds[2][P::kGroups];
@@ -781,7 +806,12 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
             load_part<D, kPaged16>(part, a, table, h, t0 + 32 * grp, s.begin, s.end, lane, values, chunk);
         };
         auto store = [&](int buf) {
-            store_part<D>(part, keys[buf], vals[buf], grp, lane, values, chunk);
+            // head_dim 256: LDS addresses are formed anew for each tile, from a lane
+            // number that the compiler cannot see through; kept, they would spill
+            int x = lane;
+            if (D > 128)
+                asm volatile("" : "+v"(x));
+            store_part<D>(part, keys[buf], vals[buf], grp, x, values, chunk);
             const uint32_t bits = (uint32_t)__ballot(part.shown);
             if (!values && chunk == 0 && lane == 0)
                 shown_lds[buf][grp] = bits;
@@ -808,12 +838,11 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                     for (int j = 0; j < 16; ++j)
                         sc[t][j] = 0;
                 const _Float16* kf = keys[buf] + (32 * sub + col) * P::kKeyPitch + 8 * half;
-#pragma unroll
-                for (int f = 0; f < KF; ++f)
-#pragma unroll
-                    for (int t = 0; t < N; ++t)
-                        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            *(const half8v*)(kf + 32 * t * P::kKeyPitch + 16 * f), q[f], sc[t], 0, 0, 0);
+                in_turn<KF * N, kKeysAhead>(
+                    [&](int x) { return *(const half8v*)(kf + 32 * (x % N) * P::kKeyPitch + 16 * (x / N)); },
+                    [&](int x, half8v k) {
+                        sc[x % N] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[x / N], sc[x % N], 0, 0, 0);
+                    });
 
                 uint32_t shown[N];
                 bool whole = ts >= mine.all_begin && ts + 32 * N <= mine.all_end;
@@ -862,14 +891,13 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                         p[t][j >> 3][j & 7] = (_Float16)e;
                     }
                 const _Float16* vf = vals[buf] + P::val(col) + 32 * sub + 8 * half;
-#pragma unroll
-                for (int t = 0; t < N; ++t)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < MT; ++i)
-                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                *(const half8v*)(vf + P::val(32 * i) + 32 * t + 16 * u), p[t][u], o[i], 0, 0, 0);
+                in_turn<2 * MT * N, kValsAhead>(
+                    [&](int x) {
+                        return *(const half8v*)(vf + P::val(32 * (x % MT)) + 32 * (x / MT >> 1) + 16 * (x / MT & 1));
+                    },
+                    [&](int x, half8v v) {
+                        o[x % MT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[x / MT >> 1][x / MT & 1], o[x % MT], 0, 0, 0);
+                    });
             }
             if (t0 + P::kTokens < last) {
                 store(buf ^ 1);
