@@ -1067,10 +1067,14 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
     return p;
 }
 
+// Pages of whole 16 tokens are read a half tile at a time, also where nothing is
+// there to see; so there must be a page and a table entry.
+bool whole_halves(const Attn& a) { return a.page % 16 == 0 && a.num_pages > 0 && a.max_pages > 0; }
+
 template <int D, int RT>
 void launch_rows(const Attn& a, dim3 grid, hipStream_t stream)
 {
-    if (a.page % 16 == 0)
+    if (whole_halves(a))
         hipLaunchKernelGGL((attn_rows_kernel<D, RT, true>), grid, dim3(256), 0, stream, a);
     else
         hipLaunchKernelGGL((attn_rows_kernel<D, RT, false>), grid, dim3(256), 0, stream, a);
@@ -1083,7 +1087,7 @@ void launch(const Attn& a, int block, hipStream_t stream)
     const dim3 grid((unsigned)((work + 7) / 8 * 8 * a.kv_heads));
     if (block == 256) {
         const dim3 all((unsigned)(work * a.kv_heads));
-        if (a.page % 16 == 0)
+        if (whole_halves(a))
             hipLaunchKernelGGL((attn_prompt_kernel<D, true>), all, dim3(512), 0, stream, a);
         else
             hipLaunchKernelGGL((attn_prompt_kernel<D, false>), all, dim3(512), 0, stream, a);

@@ -252,6 +252,24 @@ def test_attention_table_narrower_than_length(M):
     check_attention(M, c)
 
 
+@pytest.mark.parametrize("news", [[1, 2], [60, 70]])
+@pytest.mark.parametrize("empty", ["cache", "table"])
+def test_attention_without_cache_or_table(M, empty, news):
+    """A cache of no slots, a table of no columns: every row sees nothing, and
+    the null pointers of empty tensors are not read."""
+    c = attn_case(12, 8, 2, 128, 16, [40, 70], news)
+    if empty == "cache":
+        for k in ("kp", "ks", "vp", "vs"):
+            c[k] = c[k][:0]
+    else:
+        c["table"] = c["table"][:, :0]
+    dev = device(c)
+    say("attention without", empty, news)
+    for window in (0, 9):
+        out, lse = call_attention(M, c, dev, window=window)
+        assert bool((host(out) == 0).all()) and bool((host(lse) == -math.inf).all())
+
+
 def test_attention_large_and_small_values(M):
     """q over BF16's range (rows scaled by 2^100 and 2^-100) with scores kept
     moderate by `scale`; scores far apart (one key takes all the weight)."""
