@@ -1035,8 +1035,8 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
     int64_t blocks = ceil_div(rows, (int64_t)p.block);
     p.row_blocks = (int)(blocks > 4096 ? 4096 : blocks);
     int64_t range = max_seq_len > INT32_MAX ? INT32_MAX : max_seq_len;
-    if (window > 0 && window + max_query_len + 32 < range)
-        range = window + max_query_len + 32;
+    if (window > 0 && window < range && window + rows / group + 32 < range)
+        range = window + rows / group + 32;
     const int64_t items = (num_seqs < 1 ? 1 : num_seqs) * kv_heads * p.row_blocks;
     // One round of workgroups on the card's 256 compute units, as many on each
     // as its registers hold, by splits of at least `shortest` tokens; for few rows
@@ -1176,7 +1176,9 @@ extern "C" nvfp4_status_t nvfp4_paged_attention(
         return NVFP4_ERROR_INVALID_VALUE;
     const Plan p = make_plan(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len, window);
     Attn a = {q, k_packed, k_scales, v_packed, v_scales, block_table, seq_lens, query_offsets,
-              k_gs, v_gs, out, lse, (float*)workspace, ld_q, ld_out, ld_table, window, (int)tokens,
+              k_gs, v_gs, out, lse, (float*)workspace, ld_q, ld_out, ld_table,
+              window > INT32_MAX ? 0 : window,      // which hides nothing
+              (int)tokens,
               heads, kv_heads, page_size, (int)(num_slots / page_size), (int)max_pages,
               (int)num_seqs, causal, scale};
     int shift = 0;

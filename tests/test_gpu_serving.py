@@ -270,6 +270,19 @@ def test_attention_without_cache_or_table(M, empty, news):
         assert bool((host(out) == 0).all()) and bool((host(lse) == -math.inf).all())
 
 
+def test_attention_widest_window(M):
+    """Windows up to the type's largest value hide nothing, also for queries in
+    front of the context (positions below 0)."""
+    for news in ([1, 5], [30, 90]):
+        c = attn_case(13, 8, 2, 64, 16, [200, 3], news)
+        dev = device(c)
+        say("attention wide windows", news)
+        want = call_attention(M, c, dev, causal=False)
+        for window in (2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1):
+            got = call_attention(M, c, dev, causal=False, window=window)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), window
+
+
 def test_attention_large_and_small_values(M):
     """q over BF16's range (rows scaled by 2^100 and 2^-100) with scores kept
     moderate by `scale`; scores far apart (one key takes all the weight)."""

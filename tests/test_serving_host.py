@@ -93,6 +93,9 @@ def test_attention_workspace(lib):
     assert 0 < long < 2 ** 28                  # a split context needs room
     assert f(1, 32, 8, 128, 1, 1, 131072, 100) <= long
     assert f(8192, 32, 8, 128, 4, 2048, 2048, 0) < 2 ** 31
+    # the largest window and hints stand for no limit
+    assert f(1, 32, 8, 128, 1, 2 ** 62, 131072, 2 ** 63 - 1) == f(1, 32, 8, 128, 1, 2 ** 62, 131072, 0)
+    assert f(1, 32, 8, 128, 1, 1, 131072, 2 ** 63 - 1) == long
 
 
 def mo(lib, fp4, x=A, tokens=4, ld_x=128, logits=A, w1=A, s1=A, g1=None, w2=A, s2=A, g2=None, hidden=128, inter=64, e=8,
