@@ -106,9 +106,9 @@ nvfp4_status_t kv_block_tables(const int32_t *context_lens, const int32_t *query
  * finite. head_dim is 64, 128 or 256; heads a multiple of kv_heads, at most
  * 1024; ld_q, ld_out multiples of 8; q, out, packed caches 16-byte aligned,
  * scale caches 4-byte (8 for head_dim 128, 16 for 256); num_slots < 2^31,
- * num_seqs <= 65535, num_seqs * kv_heads <= 2^22, max_pages * page_size <=
- * 2^30. One kernel, or two where a long context is split over
- * workgroups.
+ * tokens * heads <= 2^30, num_seqs <= 65535, num_seqs * kv_heads <= 2^22,
+ * max_pages * page_size <= 2^30; window >= 2^31 hides nothing. One kernel,
+ * or two where a long context is split over workgroups.
  */
 nvfp4_status_t nvfp4_paged_attention(const uint16_t *q, int64_t tokens, int64_t ld_q,
                                      int32_t heads, int32_t kv_heads, int32_t head_dim,

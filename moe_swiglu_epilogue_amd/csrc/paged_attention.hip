@@ -1052,10 +1052,11 @@ Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim
         splits = ceil_div(range < 1 ? 1 : range, shortest);
     if (splits > 256)
         splits = 256;
-    // grids stay below 2^24 workgroups (rows and splits left out are looped over)
+    // grids stay below 2^32 work-items, 2^23 workgroups of 512 (rows and splits left
+    // out are looped over; 8 kv_heads for the rounding in launch)
     if (tokens * heads > (1 << 22))
         splits = 1;
-    const int64_t most = ((1 << 24) - 16) / ((num_seqs < 1 ? 1 : num_seqs) * kv_heads);
+    const int64_t most = ((1 << 23) - 8 * 1024 - 1) / ((num_seqs < 1 ? 1 : num_seqs) * kv_heads);
     if (splits * p.row_blocks > most) {
         splits = 1;
         if (p.row_blocks > most)
@@ -1116,7 +1117,7 @@ bool sizes_supported(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t he
                      int64_t num_seqs)
 {
     return (head_dim == 64 || head_dim == 128 || head_dim == 256) && heads <= 1024 &&
-           num_seqs <= 65535 && num_seqs * kv_heads <= (1 << 22) && tokens <= INT32_MAX;
+           num_seqs <= 65535 && num_seqs * kv_heads <= (1 << 22) && tokens <= (1 << 30) / heads;
 }
 
 }  // namespace

@@ -270,6 +270,31 @@ def test_attention_without_cache_or_table(M, empty, news):
         assert bool((host(out) == 0).all()) and bool((host(lse) == -math.inf).all())
 
 
+@pytest.mark.parametrize("hint", [1, 600])
+def test_attention_most_requests(M, hint):
+    """The most (request, key/value head) pairs that are taken, nearly all of
+    them without a query: grids stay inside what a launch takes."""
+    n, totals, news = 65535, [5, 40], [1, 2]
+    c = attn_case(14, 64, 64, 64, 16, totals, news)
+    dev = device(c)
+    want = call_attention(M, c, dev)
+    offsets = torch.full((n + 1,), 3, dtype=torch.int32)
+    offsets[:n - 1] = 0
+    offsets[n - 1] = 1
+    lens = torch.zeros(n, dtype=torch.int32)
+    lens[n - 2:] = c["lens"]
+    table = torch.full((n, c["table"].shape[1]), -1, dtype=torch.int32)
+    table[n - 2:] = c["table"]
+    dev.update(offsets=offsets.cuda(), lens=lens.cuda(), table=table.cuda())
+    say("attention most requests", hint)
+    got = call_attention(M, c, dev, max_query_len=hint)
+    # the same sums in another order, where another kernel takes the rows: out
+    # has BF16's rounding (2^-8) and FP16 probabilities (2^-11 each way)
+    for a, b in zip(got, want):
+        a, b = host(a).double(), host(b).double()
+        assert float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
+
+
 def test_attention_widest_window(M):
     """Windows up to the type's largest value hide nothing, also for queries in
     front of the context (positions below 0)."""

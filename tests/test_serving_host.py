@@ -74,6 +74,7 @@ def test_attention_validation(lib):
         assert at(lib, **bad) == INVALID, bad
     for bad in (dict(dim=96, ld_q=2048, ld_o=2048), dict(dim=512, ld_q=8192, ld_o=8192), dict(dim=0),
                 dict(heads=2048, kv=1, ld_q=2 ** 19, ld_o=2 ** 19), dict(n=65536), dict(tokens=2 ** 31), dict(ns=2 ** 31),
+                dict(tokens=2 ** 27 + 1),
                 dict(mp=2 ** 30 // 16 + 1, ld_t=2 ** 31)):
         assert at(lib, **bad) == SHAPE, bad
     for bad in (dict(q=A + 8), dict(out=A + 8), dict(ld_q=1028), dict(ld_o=1028), dict(kp=A + 8), dict(vp=A + 8),
