@@ -288,11 +288,52 @@ def test_attention_most_requests(M, hint):
     dev.update(offsets=offsets.cuda(), lens=lens.cuda(), table=table.cuda())
     say("attention most requests", hint)
     got = call_attention(M, c, dev, max_query_len=hint)
-    # the same sums in another order, where another kernel takes the rows: out
-    # has BF16's rounding (2^-8) and FP16 probabilities (2^-11 each way)
-    for a, b in zip(got, want):
-        a, b = host(a).double(), host(b).double()
-        assert float((a - b).abs().max()) <= 2.0 ** -7 * float(b.abs().max())
+    ref, ref_lse, tol, lse_tol = R.paged_attention(
+        c["q"], c["kp"], c["ks"], c["vp"], c["vs"], c["table"], c["lens"], c["offsets"], 64, 16, c["scale"], True, 0, 1.0, 1.0)
+    for out, lse in (want, got):
+        assert bool(((host(out).double() - ref).abs() <= tol).all())
+        assert bool(((host(lse).double() - ref_lse).abs() <= lse_tol).all())
+
+
+@pytest.mark.parametrize("page,news", [(16, [1, 1, 1]), (10, [1, 1, 1]), (16, [5, 30, 100]), (6, [5, 30, 100])])
+def test_attention_unseen_slots_may_hold_anything(M, page, news):
+    """Slots behind a request's tokens, of hidden pages and of no request: NaN
+    scales and any code there change no byte of the result."""
+    c = attn_case(15, 8, 2, 128, page, [200, 37, 111], news, hide=[(0, 1, -1), (2, 0, 10 ** 7)])
+    say("attention unseen slots", page, news)
+    want = call_attention(M, c, device(c))
+    mine = torch.zeros(c["kp"].shape[0], dtype=torch.bool)
+    for b, n in enumerate(c["lens"].tolist()):
+        for t in range(n):
+            entry = int(c["table"][b, t // page])
+            if 0 <= entry < len(mine) // page:
+                mine[entry * page + t % page] = True
+    for k, v in (("kp", 0xff), ("ks", 0x7f), ("vp", 0x77), ("vs", 0xff)):
+        c[k] = c[k].clone()
+        c[k][~mine] = v
+    got = call_attention(M, c, device(c))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_attention(M, c)
+
+
+def test_attention_on_two_streams_at_once(M):
+    """Two calls that split their rows, each with a workspace and stream of its own."""
+    cases = [attn_case(16 + i, 16, 2, 128, 16, [3500, 900], [1, 1]) for i in range(2)]
+    devs = [device(c) for c in cases]
+    want = [call_attention(M, c, d) for c, d in zip(cases, devs)]
+    need = M.serving.raw().nvfp4_paged_attention_workspace(2, 16, 2, 128, 2, 1, 3500, 0)
+    assert need > 0
+    work = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    say("attention on two streams")
+    got = []
+    for _ in range(4):
+        for c, d, w, s in zip(cases, devs, work, streams):
+            got.append(call_attention(M, c, d, workspace=w, stream=s))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
 
 
 def test_attention_widest_window(M):
@@ -386,6 +427,16 @@ def test_moe_layer(M, kind, tokens, hidden, inter, experts, top_k):
     for renormalize in (True, False):
         say("moe", kind, tokens, hidden, inter, experts, top_k, renormalize)
         check_moe(M, c, top_k, renormalize)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+@pytest.mark.parametrize("tokens,top_k", [(64, 1), (50, 2), (33, 3)])
+def test_moe_one_expert_takes_all(M, kind, tokens, top_k):
+    """Far more tokens on one expert than its share: several passes."""
+    c = moe_case(78, kind, tokens, 96, 64, 48)
+    c["logits"][:, 41] = 20.0
+    say("moe one expert", kind, tokens, top_k)
+    check_moe(M, c, top_k, True)
 
 
 @pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
