@@ -102,8 +102,10 @@ nvfp4_status_t kv_block_tables(const int32_t *context_lens, const int32_t *query
  * Products are exact products of the BF16 q and the NVFP4 values, summed in
  * FP32; a query row is scaled by a power of two into FP16's range, where its
  * values below 2^-39 of the row's largest lose bits. Probabilities are
- * rounded to FP16 (2^-11) for the product with v; sums are FP32. q must be
- * finite. head_dim is 64, 128 or 256; heads a multiple of kv_heads, at most
+ * rounded to FP16 (2^-11) for the product with v; sums are FP32. q and the
+ * scales of a request's L tokens must be finite (nvfp4_quantize_paged writes no
+ * others from finite values); slots that no row can see (behind L, of hidden
+ * pages, of no request) may hold anything. head_dim is 64, 128 or 256; heads a multiple of kv_heads, at most
  * 1024; ld_q, ld_out multiples of 8; q, out, packed caches 16-byte aligned,
  * scale caches 4-byte (8 for head_dim 128, 16 for 256); num_slots < 2^31,
  * tokens * heads <= 2^30, num_seqs <= 65535, num_seqs * kv_heads <= 2^22,
@@ -150,15 +152,21 @@ int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads, int32_t k
  * moe_layer_nvfp4: the same matrices as nvfp4_quantize writes them: packed
  *   codes [..][cols / 2], scales [..][cols / 16] and a global scale per
  *   expert (gs1, gs2 [E], NULL: 1.0), cols along the summed axis.
- * Every product is exact, sums are FP32. In the second product h (BF16
- * weights) is the sum of two BF16 numbers (2^-17 relative); with NVFP4 weights
- * activations are scaled by a power of two into FP16's range (x: exact down
- * to 2^-28 of the largest value of its group; h: 2^-11 relative).
- * hidden and inter are multiples of 32, at least 32; num_experts <= 512;
- * top_k <= 32 and <= num_experts; ld_x, ld_out multiples of 8; x, out, weights
- * and scales... 16-byte aligned (scales 2-byte, logits, ids, weights 4-byte).
- * tokens == 0 is a no-op. workspace: moe_layer_workspace(...) bytes, 16-byte
- * aligned. Three kernels.
+ * Every product is exact and sums are FP32. The activations of both products
+ * (x, then h in FP32) are brought to the matrix instructions' types:
+ *   NVFP4 weights: each token's values in a run of the summed axis (256 or 512)
+ *   are scaled by a power of two into FP16's range; x keeps every bit down to
+ *   2^-28 of the largest value of its run, h is rounded (2^-11 relative);
+ *   BF16 weights: x as it is, h as the sum of two BF16 numbers (2^-17 relative).
+ * x must be finite, and h inside the BF16 range: a token's row of out is infinite
+ * or NaN otherwise; other tokens' rows are not touched by it.
+ * hidden and inter are multiples of 32, at least 32, at most 2^20;
+ * num_experts <= 512; top_k <= 32 and <= num_experts; tokens * top_k * inter * 4
+ * and the bytes that x spans ((tokens - 1) * ld_x + hidden, times 2) below
+ * 2^31 - 4096; ld_x, ld_out multiples of 8. x, out, packed codes, BF16 weights
+ * and workspace are 16-byte aligned, scales 2-byte, logits, gs, ids and
+ * topk_weights 4-byte. tokens == 0 is a no-op. workspace:
+ * moe_layer_workspace(...) bytes. Three kernels.
  */
 nvfp4_status_t moe_layer_nvfp4(const uint16_t *x, int64_t tokens, int64_t ld_x,
                                const float *logits, const uint8_t *w1_packed,

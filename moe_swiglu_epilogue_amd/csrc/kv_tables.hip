@@ -7,7 +7,9 @@
 // most 4096 of them, out of L2) into LDS and then maps its own share of the
 // tokens, pages and requests with binary searches there. Bound by latency:
 // a launch, two rounds of dependent loads (lengths; table or free list) and
-// the stores.
+// the stores. 256 requests of one new token take 5.2 us, 48 prompts of up to
+// 8192 tokens 8.3 us on the GPU, where a launch of nothing takes about 3; a
+// call from Python about 10.6, most of it the host's.
 #include "serving_common.hpp"
 
 namespace {
