@@ -252,6 +252,16 @@ def test_attention_table_narrower_than_length(M):
     check_attention(M, c)
 
 
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 9), (128, 32), (128, 5)])
+@pytest.mark.parametrize("news", [16, 17, 32, 33, 41, 48, 49, 64, 65, 96, 97, 128, 129])
+def test_attention_row_blocks(M, dim, page, news):
+    """Every size of a block of query rows, full and with a ragged end."""
+    c = attn_case(news + dim, 2, 2, dim, page, [333, 140, 64], [news, 3, 1], pad=1)
+    say("attention row blocks", dim, page, news)
+    check_attention(M, c)
+    check_attention(M, c, window=70)
+
+
 @pytest.mark.parametrize("news", [[1, 2], [60, 70]])
 @pytest.mark.parametrize("empty", ["cache", "table"])
 def test_attention_without_cache_or_table(M, empty, news):
