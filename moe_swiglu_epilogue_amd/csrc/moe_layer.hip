@@ -142,8 +142,10 @@ __device__ void routed(const Moe& a, Group& s, int e, int tid)
 template <bool kFp4, bool kDown, int NT>
 struct Shape {
     // the longer axis of the first product takes the longer chunk (one token:
-    // 28 us with 512, 32 with 256; second product 18 and 16)
-    static constexpr int KC = kFp4 && NT == 1 && !kDown ? 512 : 256;
+    // 28 us with 512, 32 with 256; second product 18 and 16); the two halves of h
+    // a shorter one, so that more workgroups fit into LDS (57 tokens, BF16: 46 us
+    // with 256, 40 with 128; no difference for 3 tokens)
+    static constexpr int KC = kFp4 ? (NT == 1 && !kDown ? 512 : 256) : kDown ? 128 : 256;
     static constexpr int kRun = kFp4 ? 128 : 32;       // k of a step
     static constexpr int S = KC / kRun;
     static constexpr int kPitch = KC + 8;              // 16-bit elements: rows 4 banks apart
