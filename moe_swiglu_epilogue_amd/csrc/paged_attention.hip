@@ -3,12 +3,14 @@
 // Both products run on the FP16 matrix cores with FP32 sums, on cache values
 // converted in registers (exact in FP16). Global scales are folded into the
 // softmax scale and the output.
+#include "attention_plan.hpp"
 #include "fp4_operand.hpp"
-#include "serving_common.hpp"
 
 namespace {
 
 using namespace fp4op;
+using attention::make_plan;
+using attention::Plan;
 
 typedef _Float16 half4v __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
@@ -68,9 +70,7 @@ __device__ __forceinline__ void block_span(const Attn& a, Span& s, int group, in
     s.end = max(hi1, s.begin);
     s.all_begin = lo1;
     s.all_end = hi0;
-    // splits of a.chunk tokens, of more where the range is longer than promised
-    const int total = s.end - s.begin;
-    s.chunk = max(a.chunk, ((total + a.splits - 1) / a.splits + 127) & ~127);
+    s.chunk = attention::chunk_of(a.chunk, a.splits, s.end - s.begin);
 }
 
 // The workspace: each split's output rows, its (maximum, sum) pairs, and, written
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
          row0 += a.row_blocks * 16 * RT) {
         block_span(a, s, group, row0, 16 * RT);
         const int first = s.begin + split * s.chunk;
-        const int last = min(first + s.chunk, s.end);
+        const int last = attention::last_of(first, s.chunk, s.end);
         if (first >= last && split > 0)
             continue;
 
@@ -755,7 +755,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
          row0 -= a.row_blocks * kRows) {
         block_span(a, s, group, row0, kRows);
         const int first = s.begin + split * s.chunk;
-        const int last = min(first + s.chunk, s.end);
+        const int last = attention::last_of(first, s.chunk, s.end);
         if (first >= last && split > 0)
             continue;
 
@@ -1015,64 +1015,6 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a)
 }
 
 // ---- host -------------------------------------------------------------------
-struct Plan {
-    int block;         // query rows of a workgroup: 16, 32, 48, 64, or 256 (the prompt kernel)
-    int row_blocks;    // workgroups over a request's rows
-    int splits, chunk; // of the tokens
-};
-
-Plan make_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,
-               int64_t max_query_len, int64_t max_seq_len, int64_t window)
-{
-    using serving::ceil_div;
-    Plan p;
-    const int64_t group = heads / kv_heads;
-    const int64_t rows = (max_query_len < 1 ? 1 : max_query_len > (1 << 20) ? 1 << 20 : max_query_len) * group;
-    // Few rows go to the rows kernel in one or two equal blocks of whole 16 (24
-    // requests of 5 tokens, 40 rows, head_dim 64: 21 us with a block of 48, 24 with
-    // one of 64), for head_dim 256 in one or two of 16, as its registers hold no
-    // more.
-    if (head_dim > 128)
-        p.block = rows <= 32 ? 16 : 256;
-    else
-        p.block = rows <= 64 ? (int)ceil_div(rows, (int64_t)16) * 16
-                  : rows <= 128 ? (int)ceil_div(rows, (int64_t)32) * 16 : 256;
-    int64_t blocks = ceil_div(rows, (int64_t)p.block);
-    p.row_blocks = (int)(blocks > 4096 ? 4096 : blocks);
-    int64_t range = max_seq_len > INT32_MAX ? INT32_MAX : max_seq_len;
-    if (window > 0 && window < range && window + rows / group + 32 < range)
-        range = window + rows / group + 32;
-    const int64_t items = (num_seqs < 1 ? 1 : num_seqs) * kv_heads * p.row_blocks;
-    // One round of workgroups on the card's 256 compute units, as many on each
-    // as its registers hold, by splits of at least `shortest` tokens; for few rows
-    // also splits short enough that ragged requests balance (prompt kernel: half
-    // as many workgroups again, as most blocks see less than the longest).
-    const bool prompt = p.block == 256;
-    const int64_t slots = prompt ? 384 : 256 * (p.block == 16 && head_dim <= 128 ? 3 : head_dim * p.block <= 4096 ? 2 : 1);
-    const int64_t shortest = prompt ? 1024 : 128;
-    int64_t splits = slots / items < 1 ? 1 : slots / items;
-    if (!prompt && splits < ceil_div(range, (int64_t)2048))
-        splits = ceil_div(range, (int64_t)2048);
-    if (splits > ceil_div(range < 1 ? 1 : range, shortest))
-        splits = ceil_div(range < 1 ? 1 : range, shortest);
-    if (splits > 256)
-        splits = 256;
-    // grids stay below 2^32 work-items, 2^23 workgroups of 512 (rows and splits left
-    // out are looped over; 8 kv_heads for the rounding in launch)
-    if (tokens * heads > (1 << 22))
-        splits = 1;
-    const int64_t most = ((1 << 23) - 8 * 1024 - 1) / ((num_seqs < 1 ? 1 : num_seqs) * kv_heads);
-    if (splits * p.row_blocks > most) {
-        splits = 1;
-        if (p.row_blocks > most)
-            p.row_blocks = (int)(most < 1 ? 1 : most);
-    }
-    const int64_t chunk = ceil_div(ceil_div(range, splits), (int64_t)128) * 128;
-    p.chunk = (int)(chunk < 128 ? 128 : chunk);
-    p.splits = (int)ceil_div(range < 1 ? 1 : range, (int64_t)p.chunk);
-    return p;
-}
-
 // Pages of whole 16 tokens are read a half tile at a time, also where nothing is
 // there to see; so there must be a page and a table entry.
 bool whole_halves(const Attn& a) { return a.page % 16 == 0 && a.num_pages > 0 && a.max_pages > 0; }
