@@ -73,7 +73,7 @@ __device__ __forceinline__ void block_span(const Attn& a, Span& s, int group, in
     s.chunk = attention::chunk_of(a.chunk, a.splits, s.end - s.begin);
 }
 
-// The workspace: each split's output rows, its (maximum, sum) pairs, and, written
+// The workspace: each split's output rows, its (reference, sum) pairs, and, written
 // by split 0, how many splits a row has.
 __device__ __forceinline__ int* used_splits(const Attn& a, int D)
 {
@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t bits_between(int from, int to)
 // One workgroup per (request, block of 16 RT query rows, key/value head,
 // split of the tokens); query rows are tokens x the heads that share the
 // key/value head. Its four waves take tiles of 32 tokens in turn, each with
-// its own running maximum, sum and output, joined through LDS at the end.
+// its own reference, sum and output, joined through LDS at the end.
 //
 // Scores are computed transposed, S^T = K Q^T (v_mfma_f32_16x16x32_f16): a lane
 // holds one query row (lane % 16) and the tokens 4 (lane / 16) + r of each
@@ -174,10 +174,17 @@ __device__ __forceinline__ uint32_t bits_between(int from, int to)
 // conversion then picks a byte (a dimension) of each pair. So nothing crosses
 // lanes but the scale bytes.
 //
-// The maximum is kept lazily: a row's exponentials are taken against a maximum
-// that is raised only when a score exceeds it by 2^kSlack or more, which FP16
-// holds without loss; most tiles then need no rescaling and no exchange.
-constexpr float kSlack = 8.0f;
+// Exponentials are taken in base 2 against a reference of each row that stands
+// kHeadroom below the largest score at the time it was set, and that is raised
+// only when a score exceeds that score by more than kSlack; most tiles then need
+// no rescaling and no exchange. Probabilities therefore reach 2^15, what FP16
+// holds, and they lose bits only below 2^-14: their rounding is off by at most
+// 2^-11 relative or 2^-25 absolute, 2^-36 of the row's largest. Without the
+// headroom whatever lies 25 powers of two below the largest would vanish from
+// the product with v, however many tokens there are, and stay in the sum. (A
+// slack of 4 costs nothing against 8; 2 takes 2000 rows of head_dim 256 behind
+// 16000 tokens from 455 to 463 us.)
+constexpr float kSlack = 4.0f, kHeadroom = 15.0f - kSlack;
 
 template <int D>
 struct Tile {
@@ -438,7 +445,7 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
                 }
             }
 
-            // exponentials: base 2, against the row's lazily raised maximum
+            // exponentials: base 2, against the row's reference
             const uint32_t hid = ~(uint32_t)__ballot(t.shown);     // bit j: token j does not count
             const bool whole = hid == 0 && t0 >= s.all_begin && t0 + 32 <= s.all_end;
             half8v p[RT];
@@ -456,8 +463,8 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
                     top = largest(x);
                 }
                 top *= factor[rt];
-                if (__any(top > m[rt] + kSlack)) {
-                    const float up = fmaxf(m[rt], row_max(top));
+                if (__any(top > m[rt] + (kHeadroom + kSlack))) {
+                    const float up = fmaxf(m[rt], row_max(top) - kHeadroom);
                     const float f = m[rt] == up ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - up);
                     m[rt] = up;
                     l[rt] *= f;
@@ -869,8 +876,8 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                     }
                 }
                 top *= factor;
-                if (__any(top > m + kSlack)) {
-                    const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                if (__any(top > m + (kHeadroom + kSlack))) {
+                    const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)) - kHeadroom);
                     const float f = m == up ? 1.0f : __builtin_amdgcn_exp2f(m - up);
                     m = up;
                     l *= f;
@@ -1081,7 +1088,7 @@ extern "C" int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads
         !sizes_supported(tokens, heads, kv_heads, head_dim, num_seqs))
         return -1;
     const Plan p = make_plan(tokens, heads, kv_heads, head_dim, num_seqs, max_query_len, max_seq_len, window);
-    // a split's outputs and (maximum, sum) pairs of every row, and the rows' splits
+    // a split's outputs and (reference, sum) pairs of every row, and the rows' splits
     return p.splits > 1 ? tokens * heads * 4 * ((head_dim + 2) * p.splits + 1) : 0;
 }
 

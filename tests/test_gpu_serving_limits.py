@@ -74,3 +74,44 @@ def test_attention_window_at_the_end_of_the_longest_table(M, page, news):
                 short["q"], kp, ks, vp, vs, short["table"], short["lens"], short["offsets"], 1, page, 0.04, True, window)
             assert bool(((host(out).double() - ref).abs() <= tol).all())
             assert bool(((host(lse).double() - ref_lse).abs() <= lse_tol).all())
+
+
+# ---- one token that takes nearly all the weight ------------------------------------
+@pytest.mark.parametrize("octaves", [23.4, 25.2, 30.0])
+@pytest.mark.parametrize("dim,page,news,hint", [
+    (128, 16, 1, 100), (128, 16, 1, 65536), (64, 16, 40, 100), (64, 24, 3, 100), (256, 16, 2, 100), (256, 64, 50, 65536),
+    (128, 16, 300, 100), (64, 32, 129, 65536), (256, 16, 60, 100), (128, 24, 130, 100)])
+def test_attention_tail_behind_dominant_tokens(M, octaves, dim, page, news, hint):
+    """Four tokens with values of zero take the weight, one of each of a
+    workgroup's four waves (tokens 0, 32, 64, 96), and 65000 others stand `octaves`
+    powers of two below: the result is the others' share alone.
+
+    Bound: a probability is a hardware exponential (d, as in serving_ref), rounded
+    to FP16 relative to a reference at least 2^11 below the row's largest: off by 2^-11
+    relative or, where that is more, by 2^-25 of the reference, 2^-36 of the largest.
+    Sums run in FP32 over n tokens; BF16 rounds by 2^-8."""
+    heads, kv_heads, n = 4, 2, 65000
+    pages = -(-n // page)
+    g = torch.Generator().manual_seed(24)
+    cols = kv_heads * dim
+    sinks = torch.tensor([0, 32, 64, 96])
+    kp, vp = torch.zeros(pages * page, cols // 2, dtype=torch.uint8), torch.randint(0, 256, (pages * page, cols // 2), generator=g)
+    vp = (vp & 0x77).to(torch.uint8)                                # no negative values, so nothing cancels
+    kp[sinks], vp[sinks] = 0x22, 0                                  # keys of ones, values of zero
+    ks = torch.full((pages * page, cols // 16), 0x38, dtype=torch.uint8)       # scales of 1
+    c = dict(q=torch.ones(news, heads, dim, dtype=torch.bfloat16), kp=kp, ks=ks, vp=vp, vs=ks, kv_heads=kv_heads, page=page,
+             table=torch.arange(pages, dtype=torch.int32)[None], lens=torch.tensor([n], dtype=torch.int32),
+             offsets=torch.tensor([0, news], dtype=torch.int32), scale=octaves * math.log(2) / dim)
+    say("attention tail", octaves, dim, page, news, hint)
+    out, lse = call_attention(M, c, device(c), max_seq_len=hint)
+    v = R.nvfp4_values(vp[:n], ks[:n]).view(n, kv_heads, dim).cumsum(0)[n - news:].repeat_interleave(heads // kv_heads, 1)
+    seen = torch.arange(n - news + 1, n + 1).double().view(-1, 1, 1)          # tokens that each row sees
+    small = 2.0 ** -octaves
+    total = 4 + (seen - 4) * small
+    want = v * small / total
+    d = (dim + 8) * 2.0 ** -24 * octaves * math.log(2) + 2.0 ** -21
+    tol = want * (2.0 ** -8 + 2.0 ** -11 + 2 * d + (seen + 8) * 2.0 ** -24) + seen * 2.0 ** -36 * 6 / total
+    worst = ((host(out).double() - want).abs() / tol).max()
+    assert worst <= 1, worst
+    exact = octaves * math.log(2) + torch.log(total[..., 0])
+    assert bool(((host(lse).double() - exact).abs() <= d + (seen[..., 0] + 8) * 2.0 ** -24 + 2.0 ** -22 * (1 + exact)).all())
