@@ -54,8 +54,9 @@ extern "C" {
  * block_table [num_seqs][ld_table] int32, max_pages columns used;
  * free_begin[0] outside [0, num_free] counts as an empty list and is taken as
  * 0 in free_end. query_offsets, seq_lens, free_end and slots are all
- * required. Lengths must not share memory with the outputs (every workgroup
- * reads all of them).
+ * required. No output (block_table among them, the columns used) may share
+ * memory with an input or another output; such a call is refused with
+ * NVFP4_ERROR_INVALID_VALUE.
  * num_seqs <= 4096, max_tokens < 2^31, page_size >= 1. num_seqs == 0 is no
  * error: the outputs are written. One kernel.
  */

@@ -162,6 +162,27 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(Tables a)
     }
 }
 
+// `rows` rows of `bytes` bytes, `pitch` bytes apart; one row for a vector.
+struct Memory {
+    uintptr_t at;
+    int64_t rows, pitch, bytes;
+};
+
+Memory vector(const void* p, int64_t bytes) { return {(uintptr_t)p, 1, bytes, p ? bytes : 0}; }
+
+// Whether a vector touches some row of m.
+bool shared(const Memory& v, const Memory& m)
+{
+    if (v.bytes == 0 || m.rows == 0 || m.bytes == 0)
+        return false;
+    if (v.at < m.at)
+        return m.at - v.at < (uintptr_t)v.bytes;
+    const uintptr_t off = v.at - m.at;       // in row off / pitch, or in the gap behind it
+    const int64_t row = off / (uintptr_t)m.pitch < (uintptr_t)m.rows ? (int64_t)(off / (uintptr_t)m.pitch) : m.rows - 1;
+    const uintptr_t in_row = off - (uintptr_t)row * m.pitch;
+    return in_row < (uintptr_t)m.bytes || (row + 1 < m.rows && m.pitch - in_row < (uintptr_t)v.bytes);
+}
+
 }  // namespace
 
 extern "C" nvfp4_status_t kv_block_tables(const int32_t* context_lens, const int32_t* query_lens,
@@ -187,6 +208,20 @@ extern "C" nvfp4_status_t kv_block_tables(const int32_t* context_lens, const int
         !aligned(free_begin, 4) || !aligned(block_table, 4) || !aligned(query_offsets, 4) ||
         !aligned(seq_lens, 4) || !aligned(slots, 8) || !aligned(free_end, 4))
         return NVFP4_ERROR_MISALIGNED;
+    // Every workgroup reads all lengths and what it needs of the lists, and none
+    // waits for another: a written value must not be one that is read.
+    const Memory in[] = {vector(context_lens, 4 * num_seqs), vector(query_lens, 4 * num_seqs),
+                         vector(free_pages, num_free > 0 ? 4 * num_free : 0), vector(free_begin, 4)};
+    const Memory out[] = {vector(query_offsets, 4 * num_seqs + 4), vector(seq_lens, 4 * num_seqs),
+                          vector(slots, 8 * max_tokens), vector(free_end, 4)};
+    const Memory table = {(uintptr_t)block_table, num_seqs, 4 * ld_table, 4 * max_pages};
+    for (int i = 0; num_seqs > 0 && i < 4; ++i) {
+        if (shared(out[i], table) || shared(in[i], table))
+            return NVFP4_ERROR_INVALID_VALUE;
+        for (int j = 0; j < 4; ++j)
+            if (shared(out[i], in[j]) || (j < i && shared(out[i], out[j])))
+                return NVFP4_ERROR_INVALID_VALUE;
+    }
     Tables a = {context_lens, query_lens, free_pages, free_begin, block_table, query_offsets,
                 seq_lens, slots, free_end, ld_table, (int)num_seqs, page_size, (int)num_free,
                 (int)max_pages, (int)max_tokens};

@@ -115,3 +115,55 @@ def test_attention_tail_behind_dominant_tokens(M, octaves, dim, page, news, hint
     assert worst <= 1, worst
     exact = octaves * math.log(2) + torch.log(total[..., 0])
     assert bool(((host(lse).double() - exact).abs() <= d + (seen[..., 0] + 8) * 2.0 ** -24 + 2.0 ** -22 * (1 + exact)).all())
+
+
+# ---- memory side by side -------------------------------------------------------------
+def test_block_tables_in_one_buffer(M):
+    """Every array in one allocation, one right behind the other, and the free
+    list's end in a gap between two rows of the table: no overlap, not refused."""
+    context, query, table, free = S.table_case(31, 7, 200, 16, "prompts")
+    n, width, total = len(query), len(table[0]), sum(max(q, 0) for q in query)
+    buf = torch.full((2 * (total + 3) + 4 * n + 2 + len(free) + n * (width + 3),), -9, dtype=torch.int32).cuda()
+    at = [0]
+
+    def take(count):
+        at[0] += count
+        return buf[at[0] - count:at[0]]
+
+    slots = take(2 * (total + 3)).view(torch.int64)
+    c, q, lens, offsets, f, begin = take(n), take(n), take(n), take(n + 1), take(len(free)), take(1)
+    rows = take(n * (width + 3)).view(n, width + 3)
+    c.copy_(torch.tensor(context))
+    q.copy_(torch.tensor(query))
+    f.copy_(torch.tensor(free))
+    begin.fill_(2)
+    rows[:, :width] = torch.tensor(table, dtype=torch.int32)
+    end = rows[2, width + 1:width + 2]
+    say("block tables in one buffer")
+    M.kv_block_tables(c, q, rows[:, :width], 16, total + 3, free_pages=f, free_begin=begin, slots=slots, query_offsets=offsets,
+                      seq_lens=lens, free_end=end)
+    want = [list(r) for r in table]
+    want_slots, want_offsets, want_lens, want_end = R.kv_block_tables(context, query, want, 16, total + 3, free, 2)
+    assert host(slots).tolist() == want_slots and host(offsets).tolist() == want_offsets
+    assert host(lens).tolist() == want_lens and host(end).tolist() == [want_end]
+    gap = torch.full((n, 3), -9, dtype=torch.int32)
+    gap[2, 1] = want_end
+    assert torch.equal(host(rows), torch.cat([torch.tensor(want, dtype=torch.int32), gap], 1))
+
+
+def test_block_tables_refuses_shared_memory(M):
+    """From Python: views that overlap, and the pairs that start together."""
+    n = 5
+    buf = torch.zeros(4 * n, dtype=torch.int32).cuda()
+    table = torch.zeros(n, 4, dtype=torch.int32).cuda()
+    free = torch.arange(9, dtype=torch.int32).cuda()
+    lens, query = buf[:n], buf[n:2 * n]
+    say("block tables, shared memory")
+    for more in (dict(query_offsets=buf[:n + 1]), dict(query_offsets=buf[2 * n - 1:3 * n]), dict(seq_lens=buf[1:n + 1]),
+                 dict(free_end=buf[3:4]), dict(free_end=table[1, 1:2]), dict(free_end=free[8:]), dict(seq_lens=table.view(-1)[:n]),
+                 dict(query_offsets=buf[2 * n:3 * n + 1], seq_lens=buf[3 * n:])):
+        with pytest.raises(M.Nvfp4Error):
+            M.kv_block_tables(lens, query, table, 4, 8, free_pages=free, **more)
+    with pytest.raises(ValueError):
+        M.kv_block_tables(lens, query, table, 4, 8, free_pages=free, seq_lens=lens)
+    assert bool((host(buf) == 0).all())
