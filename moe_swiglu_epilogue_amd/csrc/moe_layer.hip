@@ -168,7 +168,9 @@ struct Weights {
 // is something to load: what lies behind the summed axis or the last token
 // gets an offset out of the buffer's range, which reads as 0 without a memory
 // access. So the loop has no branch around a load, behind which the compiler
-// would have to wait for everything in flight.
+// would have to wait for everything in flight. The scalar offset, k's part, is
+// 0 behind the axis: it never passes the buffer's end, so that a lane's offset
+// alone is out of range whichever way the range check counts the scalar one.
 constexpr uint32_t kOutside = 0x7fffff00u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes)
@@ -193,19 +195,19 @@ __device__ __forceinline__ void load_weights(Weights<kFp4, kDown, NT, kWide>& r,
     if (kFp4 && kWide) {
         const int k = k0 + 128 * (g & (X::S - 1));
         r.wide = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(
-            buffer(t.sc, t.sc_bytes), k < K ? t.sc_at : kOutside, k0 / 16, 0));
+            buffer(t.sc, t.sc_bytes), k < K ? t.sc_at : kOutside, k0 < K ? k0 / 16 : 0, 0));
     }
     for (int s = 0; s < X::S; ++s) {
-        const int k = k0 + X::kRun * s;
+        const int k = k0 + X::kRun * s, at = k < K ? k : 0;
         if (kWide || !kFp4) {
             r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-                buffer(t.w, k < K ? t.w_bytes : 0), t.w_at, kFp4 ? k / 2 : 2 * k, 0));
+                buffer(t.w, k < K ? t.w_bytes : 0), t.w_at, kFp4 ? at / 2 : 2 * at, 0));
         } else {
             const bool in = k + 32 * g < K;
             r.w[s] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-                buffer(t.w, t.w_bytes), in ? t.w_at : kOutside, k / 2, 0));
+                buffer(t.w, t.w_bytes), in ? t.w_at : kOutside, at / 2, 0));
             r.sc[kFp4 && !kWide ? s : 0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-                buffer(t.sc, t.sc_bytes), in ? t.sc_at : kOutside, k / 16, 0);
+                buffer(t.sc, t.sc_bytes), in ? t.sc_at : kOutside, at / 16, 0);
         }
     }
 }
@@ -273,10 +275,11 @@ __device__ __forceinline__ void load_tokens(Tokens<kFp4, kDown, NT>& r, __amdgpu
 {
     using X = Tokens<kFp4, kDown, NT>;
     const bool in = k0 + 8 * (lane % X::kLanes) < K;
+    const int step = k0 < K ? k0 * (kDown ? 4 : 2) : 0;
     for (int i = 0; i < X::R; ++i)
         for (int w = 0; w < X::kWords / 4; ++w) {
             const uint4v u = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(
-                src, (in ? at[i] : kOutside) + 16 * w, k0 * (kDown ? 4 : 2), 0));
+                src, (in ? at[i] : kOutside) + 16 * w, step, 0));
             for (int j = 0; j < 4; ++j)
                 r.v[i][4 * w + j] = u[j];
         }

@@ -167,3 +167,35 @@ def test_block_tables_refuses_shared_memory(M):
     with pytest.raises(ValueError):
         M.kv_block_tables(lens, query, table, 4, 8, free_pages=free, seq_lens=lens)
     assert bool((host(buf) == 0).all())
+
+
+# ---- what a layer must not read ---------------------------------------------------------
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 20])
+@pytest.mark.parametrize("hidden,inter", [(32, 32), (96, 64), (256, 128), (288, 160), (512, 256), (544, 288), (768, 384)])
+def test_moe_unreached_experts_and_padding_may_hold_anything(M, kind, tokens, hidden, inter):
+    """NaN in all weights of the experts that no token reaches, right behind the
+    reached ones' last rows, and between the rows of a pitched x; summed axes of one
+    to three chunks, whole and ragged."""
+    c = S.moe_case(tokens + hidden, kind, tokens, hidden, inter, 4)
+    c["logits"][:, 1::2] = -5.0 - c["logits"][:, 1::2].abs()
+    c["logits"][:, 0::2] += 8.0
+    nan8, nan16 = 0x7f, math.nan
+    for n in ("w1", "w2"):
+        c[n][1::2] = 0xff if kind == "nvfp4" else nan16
+    if kind == "nvfp4":
+        for n in ("s1", "s2"):
+            c[n][1::2] = nan8
+        for n in ("gs1", "gs2"):
+            c[n][1::2] = math.nan
+    dev = device(c)
+    wide = torch.full((tokens, hidden + 24), math.nan, dtype=torch.bfloat16).cuda()
+    wide[:, :hidden] = dev["x"]
+    say("moe unread", kind, tokens, hidden, inter)
+    for top_k in (1, 2):
+        out, ids, _ = S.call_moe(M, c, dict(dev, x=wide[:, :hidden]), top_k)
+        ref, tol, want, _ = R.moe_layer(c["x"], c["logits"], c["w1d"], c["w2d"], top_k, True,
+                                        2.0 ** -17 if kind == "bf16" else 2.0 ** -11)
+        assert host(ids).tolist() == want.tolist()
+        d = (host(out).double() - ref).abs() - tol
+        assert bool((d <= 0).all()), d.max()
