@@ -61,6 +61,7 @@ _ptr = _b._ptr
 _pitch = _b._pitch
 Nvfp4Error = _b.Nvfp4Error
 _empty = torch.empty
+_I32_MAX, _I64_MAX = 2 ** 31 - 1, 2 ** 63 - 1
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
@@ -91,6 +92,19 @@ def _current(device, stream):
 def _check(status, what):
     if status != 0:
         raise Nvfp4Error(status, what)
+
+
+def _fits(v, name, bits):
+    """A size that the C call takes as a signed integer of `bits` bits; ctypes
+    would cut a larger one short."""
+    if not -(1 << (bits - 1)) <= v < 1 << (bits - 1):
+        raise ValueError("%s does not fit %d bits" % (name, bits))
+    return v
+
+
+def _at_most(v, name):
+    """A size of which every value past 64 bits means the same as the largest."""
+    return _I64_MAX if v > _I64_MAX else _fits(v, name, 64)
 
 
 def _cuda(t, name):
@@ -186,6 +200,7 @@ def kv_block_tables(context_lens: torch.Tensor | None, query_lens: torch.Tensor,
     begin = _scalar(free_begin, "free_begin", _I32, device)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
+    _fits(page_size, "page_size", 32)
 
     def launch(st, slots, query_offsets, seq_lens, free_end):
         if slots is None:
@@ -273,6 +288,11 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
     vg = _scalar(v_gs, "v_gs", _F32, device)
     if max_seq_len is None:
         max_seq_len = max_pages * page_size
+    if not (0 <= page_size <= _I32_MAX and 0 <= max_query_len <= _I64_MAX and 0 <= max_seq_len <= _I64_MAX
+            and 0 <= window <= _I64_MAX):
+        _fits(page_size, "page_size", 32)
+        max_query_len, window = _at_most(max_query_len, "max_query_len"), _at_most(window, "window")
+        max_seq_len = _at_most(max_seq_len, "max_seq_len")
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
     L = _lib()
@@ -310,6 +330,7 @@ def _moe(fn, what, x, logits, top_k, inter, weights, renormalize, out, topk_ids,
     device = x.device
     tokens, hidden = x.shape
     experts = logits.shape[1]
+    _fits(top_k, "top_k", 32)
     need = _moe_workspace(tokens, hidden, inter, experts, top_k)
 
     def launch(st, out, topk_ids, topk_weights):

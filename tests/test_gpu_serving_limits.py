@@ -199,3 +199,33 @@ def test_moe_unreached_experts_and_padding_may_hold_anything(M, kind, tokens, hi
         assert host(ids).tolist() == want.tolist()
         d = (host(out).double() - ref).abs() - tol
         assert bool((d <= 0).all()), d.max()
+
+
+# ---- Python integers past the C types ---------------------------------------------------
+def test_integers_past_the_c_types(M):
+    """Sizes that would wrap are refused; hints and windows past 64 bits mean the
+    same as the largest that fit."""
+    c = attn_case(41, 8, 2, 64, 16, [90, 33], [1, 3])
+    dev = device(c)
+    lens = torch.tensor([5, 6], dtype=torch.int32).cuda()
+    table = torch.zeros(2, 4, dtype=torch.int32).cuda()
+    say("integers past the C types")
+    for page in (2 ** 32 + 16, 2 ** 31, -2 ** 32 + 16, 2 ** 64 + 16):
+        with pytest.raises(ValueError):
+            M.kv_block_tables(None, lens, table, page, 11)
+        with pytest.raises(ValueError):
+            call_attention(M, dict(c, page=page), dev)
+    want = call_attention(M, c, dev, max_query_len=2 ** 63 - 1, max_seq_len=2 ** 63 - 1, window=2 ** 63 - 1)
+    for big in (2 ** 63, 2 ** 64 + 5, 2 ** 70):
+        got = call_attention(M, c, dev, max_query_len=big, max_seq_len=big, window=big)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), big
+        for name in ("max_query_len", "max_seq_len", "window"):
+            with pytest.raises(ValueError):
+                call_attention(M, c, dev, **{name: -big - 1})
+    with pytest.raises(M.Nvfp4Error):
+        call_attention(M, c, dev, window=-1)
+    for tokens in (0, 2):
+        w = S.moe_case(42, "bf16", tokens, 64, 32, 4)
+        for top_k in (2 ** 32 + 1, -2 ** 32 + 1):
+            with pytest.raises(ValueError):
+                S.call_moe(M, w, device(w), top_k)
