@@ -229,3 +229,111 @@ def test_integers_past_the_c_types(M):
         for top_k in (2 ** 32 + 1, -2 ** 32 + 1):
             with pytest.raises(ValueError):
                 S.call_moe(M, w, device(w), top_k)
+
+
+# ---- every form of the prompt kernel ------------------------------------------------------
+@pytest.mark.parametrize("heads,kv_heads,dim,page,totals,news", [
+    (4, 1, 256, 24, [300, 65], [130, 65]), (8, 2, 256, 1, [150, 40], [60, 40]), (4, 2, 256, 7, [700], [200]),
+    (2, 2, 256, 100, [260, 1, 90], [257, 1, 33]), (3, 1, 64, 40, [600], [300])])
+def test_attention_prompts_with_other_pages(M, heads, kv_heads, dim, page, totals, news):
+    c = attn_case(dim + heads + page, heads, kv_heads, dim, page, totals, news, pad=2)
+    say("attention prompts, other pages", heads, kv_heads, dim, page, totals, news)
+    check_attention(M, c, gs=(0.9, 1.1))
+    check_attention(M, c, window=50)
+    check_attention(M, c, causal=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 24, 1])
+def test_attention_split_prompts(M, dim, page):
+    """Ranges of several thousand tokens for few requests: the prompt kernel's
+    splits and their join, with windows that empty the first splits."""
+    c = attn_case(dim + page, 8, 2, dim, page, [4097, 1500, 60], [70, 40, 33])
+    say("attention split prompts", dim, page)
+    need = M.serving.raw().nvfp4_paged_attention_workspace(143, 8, 2, dim, 3, 70, 4097, 0)
+    assert need > 0
+    check_attention(M, c)
+    check_attention(M, c, window=1200)
+    check_attention(M, c, window=3000, causal=False)
+
+
+# ---- small values beside large ones -------------------------------------------------------
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [1, 40, 200])
+@pytest.mark.parametrize("power", [20, 31, 35])
+def test_attention_small_components_of_a_query(M, dim, news, power):
+    """One component of q meets keys of 0 and is 2^power times the others, which alone
+    make the scores. Down to 2^-31 of the largest they are exact in FP16; below they are
+    off by at most 2^-39 of it."""
+    c = attn_case(51, 4, 2, dim, 16, [230], [news], scale=0.05 * 2.0 ** power)
+    g = torch.Generator().manual_seed(power + dim)
+    q = (1 + torch.randint(0, 128, c["q"].shape, generator=g) / 128) * torch.where(torch.rand(c["q"].shape, generator=g) < 0.5, -1.0, 1.0)
+    q *= 2.0 ** -power
+    q[:, :, 3] = 1.0
+    c["q"] = q.to(torch.bfloat16)
+    assert torch.equal(c["q"].float(), q)
+    kp = c["kp"].view(-1, 2, dim // 2)
+    kp[:, :, 1] &= 0x0f                                # element 3 of each head's keys: 0
+    c["ks"] = (c["ks"].int() & 7 | 0x38).to(torch.uint8)         # scales of 1 to 2
+    say("attention small components", dim, news, power)
+    out, lse = call_attention(M, c, device(c))
+    ref, ref_lse, tol, lse_tol = R.paged_attention(*[c[k] for k in ("q", "kp", "ks", "vp", "vs", "table", "lens", "offsets")], 2,
+                                                   16, c["scale"])
+    d = 0.0 if power <= 31 else 2.0 ** -39 * dim * 12 * c["scale"]      # keys are at most 6 x 1.875
+    v = R.nvfp4_values(c["vp"], c["vs"]).abs().max()
+    assert bool(((host(lse).double() - ref_lse).abs() <= lse_tol + d).all())
+    assert bool(((host(out).double() - ref).abs() <= tol + 2 * d * v).all())
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+@pytest.mark.parametrize("tokens", [1, 18])
+@pytest.mark.parametrize("inter", [96, 512])
+@pytest.mark.parametrize("power", [10, 18, 22])
+def test_moe_small_activations_beside_a_large_one(M, kind, tokens, inter, power):
+    """h[0] is about 2^(power + 11) times the others and meets weights of 0, so the others
+    alone make the result: h is rounded by 2^-11 relative or, where that is more, by 2^-39
+    of the largest of its run of 256 (NVFP4 weights), by 2^-17 relative (BF16 weights)."""
+    hidden, experts = 64, 2
+    g = torch.Generator().manual_seed(power)
+    c = S.moe_case(52, kind, tokens, hidden, inter, experts)
+    x = torch.zeros(tokens, hidden)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, 2.0 ** -power, 1.0
+    c["x"] = x.to(torch.bfloat16)
+    j = torch.arange(inter)
+    gate, up = 16 * (j // 8) + j % 8, 16 * (j // 8) + 8 + j % 8
+    w1 = torch.zeros(experts, 2 * inter, hidden, dtype=torch.float64)
+    w1[:, gate, 0] = 4.0                                                 # gates: 4
+    w1[:, up, 1] = torch.randint(1, 5, (experts, inter), generator=g).double() / 2      # ups: 2^-power times 0.5 to 2
+    w1[:, 8, 1], w1[:, 8, 2] = 0.0, 6.0                                  # the first up: 6, times 256 by its block's scale
+    w1[:, 8] *= 256
+    w2 = torch.randint(1, 5, (experts, hidden, inter), generator=g).double() / 2
+    w2[:, :, 0] = 0.0
+    if kind == "bf16":
+        c["w1"], c["w2"] = w1.to(torch.bfloat16), w2.to(torch.bfloat16)
+        assert torch.equal(c["w1"].double(), w1)
+    else:
+        for name, w in (("1", w1), ("2", w2)):
+            scale = torch.ones(w.shape[0], w.shape[1], w.shape[2] // 16, dtype=torch.float64)
+            if name == "1":
+                scale[:, 8] = 256.0
+            code = (torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]).double() ==
+                    (w / scale.repeat_interleave(16, -1))[..., None]).double().argmax(-1).to(torch.uint8)
+            c["w" + name] = code[..., 0::2] | code[..., 1::2] << 4
+            c["s" + name] = torch.where(scale == 256.0, 0x78, 0x38).to(torch.uint8)
+            c["gs" + name] = torch.ones(experts)
+            assert torch.equal(R.nvfp4_values(c["w" + name], c["s" + name]), w)
+    say("moe small activations", kind, tokens, inter, power)
+    out, ids, weights = S.call_moe(M, c, device(c), 1)
+    ids = host(ids)[:, 0].long()
+    acc = torch.matmul(w1, c["x"][0].double())                           # every token is the same
+    h = acc[:, gate] * torch.sigmoid(acc[:, gate]) * acc[:, up]
+    want = torch.matmul(w2, h[:, :, None])[:, :, 0][ids]
+    if kind == "bf16":
+        dh = 2.0 ** -17 * h.abs()
+    else:
+        run = torch.nn.functional.pad(h.abs(), (0, -inter % 256)).view(experts, -1, 256).amax(2).repeat_interleave(256, 1)[:, :inter]
+        dh = torch.maximum(2.0 ** -11 * h.abs(), 2.0 ** -39 * run)
+    dh = dh + 2.0 ** -19 * h.abs()
+    tol = torch.matmul(w2, dh[:, :, None])[:, :, 0][ids] + want.abs() * (2.0 ** -8 + (inter + 16) * 2.0 ** -24 + 2.0 ** -20)
+    worst = ((host(out).double() - want).abs() / tol).max()
+    assert worst <= 1, worst
