@@ -144,6 +144,15 @@ __device__ __forceinline__ half8v scaled_half8(uint4v w, int e, bool negative)
     return r;
 }
 
+// What a product with such a row is multiplied by to give its score in base 2:
+// positive, so that the largest product gives the largest score, and not 0, which
+// would turn a hidden token's -inf into NaN. A NaN stays one.
+__device__ __forceinline__ float score_factor(float k_scale, int e)
+{
+    const float f = ldexpf(fabsf(k_scale), -e);
+    return f < 0x1p-126f ? 0x1p-126f : f;
+}
+
 __device__ __forceinline__ uint32_t largest_bits(uint4v w, uint32_t top)
 {
     for (int i = 0; i < 4; ++i)
@@ -409,9 +418,7 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
             const int e = fp16_exponent(top);
             for (int f = 0; f < KF; ++f)
                 q[rt][f] = scaled_half8(w[rt][f], e, k_scale < 0);
-            // positive, so that the largest product gives the largest score, and
-            // not 0, which would turn a hidden token's -inf into NaN
-            factor[rt] = fmaxf(ldexpf(fabsf(k_scale), -e), 0x1p-126f);
+            factor[rt] = score_factor(k_scale, e);
         }
 
         float4v o[RT][C][VM];
@@ -541,7 +548,7 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
             const int64_t token = s.first + r / group;
             const int head = h * group + r % group;
             const bool whole_row = a.splits == 1;
-            const float norm = whole_row ? (total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
+            const float norm = whole_row ? (total != 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
             for (int d = (tid & 15) * 4; d < D; d += 64) {
                 float4v v = {0, 0, 0, 0};
                 for (int w = 0; w < 4; ++w)
@@ -556,7 +563,7 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
                 if (!whole_row) {
                     write_split(a, s, D, split, token * a.heads + head, top, total);
                 } else if (a.lse) {
-                    a.lse[token * a.heads + head] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+                    a.lse[token * a.heads + head] = total != 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
                 }
             }
         }
@@ -790,9 +797,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
 #pragma unroll
             for (int f = 0; f < KF; ++f)
                 q[f] = scaled_half8(w[f], e, k_scale < 0);
-            // positive, so that the largest product gives the largest score, and
-            // not 0, which would turn a hidden token's -inf into NaN
-            factor = fmaxf(ldexpf(fabsf(k_scale), -e), 0x1p-126f);
+            factor = score_factor(k_scale, e);
         }
         // the tokens that some, and that all, rows of this wave see
         Span mine = s;
@@ -918,7 +923,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
             const int64_t token = s.first + r / group;
             const int head = h * group + r % group;
             const bool whole_row = a.splits == 1;
-            const float norm = whole_row ? (total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
+            const float norm = whole_row ? (total != 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -934,7 +939,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                 if (!whole_row) {
                     write_split(a, s, D, split, token * a.heads + head, m, total);
                 } else if (a.lse) {
-                    a.lse[token * a.heads + head] = total > 0 ? (m + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+                    a.lse[token * a.heads + head] = total != 0 ? (m + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
                 }
             }
         }
@@ -1014,10 +1019,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a)
             o += o_lds[wave / kWaves * kWaves + w][x];
     }
     if (shown && wave % kWaves == 0 && lane < kLanes) {
-        o *= total > 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f;
+        o *= total != 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f;
         *(uint2v*)(a.out + token * a.ld_out + head * D + 4 * x) = uint2v{bf16x2(o[0], o[1]), bf16x2(o[2], o[3])};
         if (x == 0 && a.lse)
-            a.lse[row] = total > 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+            a.lse[row] = total != 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
     }
 }
 

@@ -337,3 +337,51 @@ def test_moe_small_activations_beside_a_large_one(M, kind, tokens, inter, power)
     tol = torch.matmul(w2, dh[:, :, None])[:, :, 0][ids] + want.abs() * (2.0 ** -8 + (inter + 16) * 2.0 ** -24 + 2.0 ** -20)
     worst = ((host(out).double() - want).abs() / tol).max()
     assert worst <= 1, worst
+
+
+# ---- NaN -------------------------------------------------------------------------------
+@pytest.mark.parametrize("dim,news,hint", [(64, 1, 100), (128, 1, 4000), (256, 2, 100), (128, 40, 100), (64, 200, 4000),
+                                           (256, 100, 100)])
+def test_attention_nan_is_not_hidden(M, dim, news, hint):
+    """A global scale of keys that is NaN, and a query with a NaN: the results of the rows
+    it reaches are NaN, no number; the other rows' stay in their bounds."""
+    c = attn_case(61, 8, 2, dim, 16, [3000, 500], [news, 1], scale=0.02)
+    dev = device(c)
+    say("attention nan", dim, news, hint)
+    nan = torch.tensor([math.nan]).cuda()
+    for more in (dict(k_gs=nan), dict(k_gs=nan, window=600)):
+        out, lse = call_attention(M, c, dev, max_seq_len=hint, **more)
+        assert bool(torch.isnan(host(out)).all()) and bool(torch.isnan(host(lse)).all())
+    c["q"][0, 2, 5] = math.nan
+    out, lse = call_attention(M, c, device(c), max_seq_len=hint)
+    out, lse = host(out), host(lse)
+    assert bool(torch.isnan(out[0, 2]).all()) and bool(torch.isnan(lse[0, 2]))
+    c["q"][0, 2, 5] = 0
+    ref, ref_lse, tol, lse_tol = R.paged_attention(*[c[k] for k in ("q", "kp", "ks", "vp", "vs", "table", "lens", "offsets")], 2,
+                                                   16, c["scale"])
+    rest = torch.ones(news + 1, 8, dtype=torch.bool)
+    rest[0, 2] = False
+    assert bool(((out.double() - ref).abs() <= tol)[rest].all()) and bool(((lse.double() - ref_lse).abs() <= lse_tol)[rest].all())
+
+
+# ---- a cache past 4 GiB -----------------------------------------------------------------
+@pytest.mark.parametrize("page", [16, 24])
+@pytest.mark.parametrize("news", [1, 70])
+def test_attention_far_in_a_large_cache(M, page, news):
+    """Codes of 4.6 GB each for keys and values: pages behind 4 GiB give what the same
+    pages in a small cache give."""
+    c = attn_case(71, 16, 8, 256, page, [400, 90], [news, 1])
+    dev = device(c)
+    say("attention large cache", page, news)
+    want = call_attention(M, c, dev)
+    used = c["kp"].shape[0]
+    slots = 4500000 // page * page
+    first = slots // page - used // page
+    big = dict(dev)
+    for k in ("kp", "ks", "vp", "vs"):
+        big[k] = torch.zeros(slots, c[k].shape[1], dtype=torch.uint8, device="cuda")
+        big[k][slots - used:] = dev[k]
+    assert big["kp"].numel() > 2 ** 32
+    big["table"] = torch.where(dev["table"] >= 0, dev["table"] + first, dev["table"])
+    got = call_attention(M, c, big)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
