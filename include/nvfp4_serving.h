@@ -97,7 +97,9 @@ nvfp4_status_t kv_block_tables(const int32_t *context_lens, const int32_t *query
  *           values.
  *   max_query_len, max_seq_len: the largest n and L that the caller expects.
  *           They choose the kernel and the split of the work, not the result:
- *           longer requests are computed too, only slower.
+ *           longer requests are computed too, only slower. A max_seq_len far
+ *           above the real lengths costs workgroups without work, time in
+ *           the join and workspace, which grow with it up to 256 splits.
  *   workspace: nvfp4_paged_attention_workspace(...) bytes (may be 0, then
  *           workspace may be NULL), 16-byte aligned.
  * Products are exact products of the BF16 q and the NVFP4 values, summed in
@@ -159,9 +161,11 @@ int64_t nvfp4_paged_attention_workspace(int64_t tokens, int32_t heads, int32_t k
  *   expert (gs1, gs2 [E], NULL: 1.0), cols along the summed axis.
  * Every product is exact and sums are FP32. The activations of both products
  * (x, then h in FP32) are brought to the matrix instructions' types:
- *   NVFP4 weights: each token's values in a run of the summed axis (256 or 512)
- *   are scaled by a power of two into FP16's range; x keeps every bit down to
- *   2^-28 of the largest value of its run, h is rounded (2^-11 relative);
+ *   NVFP4 weights: each token's values in a run of the summed axis (256 or 512
+ *   for x, 256 for h) are scaled by a power of two into FP16's range; x keeps
+ *   every bit down to 2^-31 of the largest value of its run, smaller values are
+ *   off by at most 2^-39 of that; h is rounded, by 2^-11 relative or by 2^-39 of
+ *   the largest value of its run where that is more;
  *   BF16 weights: x as it is, h as the sum of two BF16 numbers (2^-17 relative).
  * x must be finite, and h inside the BF16 range: a token's row of out is infinite
  * or NaN otherwise; other tokens' rows are not touched by it.

@@ -7,7 +7,9 @@
 // memory, the expert's tokens in the right one, from LDS. The third adds up a
 // token's top_k rows of y with the routing weights. The first finds the
 // routing itself: each workgroup counts, for the tokens, how many logits stand
-// before its expert's.
+// before its expert's. (In every workgroup, which with many experts costs more
+// than the weights: 4096 x 1024, top 8, 32 tokens, 60 reached of 64 experts 114 us,
+// 178 reached of 512 627 us.)
 #include "fp4_operand.hpp"
 #include "serving_common.hpp"
 
@@ -628,7 +630,9 @@ nvfp4_status_t run(Moe a, int64_t hidden, int64_t inter, int64_t workspace_bytes
     // the reached experts are few: one workgroup column per pair, where pairs
     // with an expert that an earlier token has leave at once; else per expert
     a.by_pair = tokens * a.top_k <= a.experts;
-    // columns of 16 tokens for twice an expert's share: more take another pass
+    // columns of 16 tokens for twice an expert's share: more take another pass, which
+    // reads the weights again (4096 x 1024, 64 tokens on one of 64 experts: four
+    // passes, 91 us, against 79 for the one pass of a layer with one expert)
     const int64_t share = a.experts == 1 ? tokens : 2 * tokens * a.top_k / a.experts;
     const int64_t cols = share < tokens ? share : tokens;
     const int nt = cols <= 16 ? 1 : cols <= 32 ? 2 : 4;

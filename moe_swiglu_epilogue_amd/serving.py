@@ -266,7 +266,8 @@ def nvfp4_paged_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
     scales [num_slots, kv_heads * head_dim / 16]) through block_table int32
     [B, max_pages]; request b owns rows query_offsets[b]..query_offsets[b+1]
     of q, at the end of its seq_lens[b] tokens. max_query_len and max_seq_len
-    (default: the table's width) steer the speed only. scale defaults to
+    (default: the table's width) steer the speed only; a max_seq_len far above
+    the real lengths costs time and workspace. scale defaults to
     head_dim ** -0.5; window > 0 keeps the last `window` positions. Returns out
     (BF16, like q) and, with ``lse`` True or a tensor, also lse FP32
     [tokens, heads]. Rows of no request are left as they were (``out`` and
