@@ -200,7 +200,8 @@ def kv_block_tables(context_lens: torch.Tensor | None, query_lens: torch.Tensor,
     begin = _scalar(free_begin, "free_begin", _I32, device)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    _fits(page_size, "page_size", 32)
+    if not 0 <= page_size <= _I32_MAX:
+        _fits(page_size, "page_size", 32)
 
     def launch(st, slots, query_offsets, seq_lens, free_end):
         if slots is None:
@@ -331,7 +332,8 @@ def _moe(fn, what, x, logits, top_k, inter, weights, renormalize, out, topk_ids,
     device = x.device
     tokens, hidden = x.shape
     experts = logits.shape[1]
-    _fits(top_k, "top_k", 32)
+    if not 0 <= top_k <= _I32_MAX:
+        _fits(top_k, "top_k", 32)
     need = _moe_workspace(tokens, hidden, inter, experts, top_k)
 
     def launch(st, out, topk_ids, topk_weights):

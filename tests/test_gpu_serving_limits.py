@@ -385,3 +385,116 @@ def test_attention_far_in_a_large_cache(M, page, news):
     big["table"] = torch.where(dev["table"] >= 0, dev["table"] + first, dev["table"])
     got = call_attention(M, c, big)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---- rows far apart, the largest layers ---------------------------------------------------
+def spread(t, pitch, fill):
+    """A view with t's values and rows `pitch` elements apart, and its buffer."""
+    buf = torch.full(((t.shape[0] - 1) * pitch + t[0].numel(),), fill, dtype=t.dtype, device="cuda")
+    view = buf.as_strided(t.shape, (pitch,) + t.stride()[1:])
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("news,page", [([1, 2, 1], 16), ([70, 3, 1], 16), ([1, 40, 2], 24)])
+def test_attention_rows_and_tables_far_apart(M, news, page):
+    """Rows of q, out and the block table whose byte offsets pass 32 bits."""
+    c = attn_case(81, 8, 2, 64, page, [2500, 90, 40], news)
+    dev = device(c)
+    say("attention far rows", news, page)
+    want, want_lse = call_attention(M, c, dev)
+    rows = c["q"].shape[0]
+    pitch = (5 << 30) // 2 // (rows - 1) // 8 * 8
+    far = dict(dev, q=spread(dev["q"], pitch, 3.0), table=spread(dev["table"], (5 << 30) // 8, -1))
+    out = spread(torch.zeros_like(dev["q"]), pitch, 5.0)
+    _, lse = call_attention(M, c, far, out=out)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    del far, out
+
+
+def test_block_tables_rows_far_apart(M):
+    context, query, table, free = S.table_case(82, 3, 300, 16, "prompts")
+    total, width = sum(max(q, 0) for q in query), len(table[0])
+    far = spread(torch.tensor(table, dtype=torch.int32).cuda(), (5 << 30) // 8, -9)
+    say("block tables far rows")
+    got = M.kv_block_tables(S.ints(context), S.ints(query), far, 16, total, free_pages=S.ints(free))
+    want = R.kv_block_tables(context, query, table, 16, total, free)
+    for a, b in zip(got, want):
+        assert host(a).tolist() == (b if isinstance(b, list) else [b])
+    assert host(far).tolist() == table
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+def test_moe_rows_far_apart(M, kind):
+    """x over the most bytes that a call takes, out over more than 4 GiB."""
+    c = S.moe_case(83, kind, 64, 64, 32, 6)
+    dev = device(c)
+    say("moe far rows", kind)
+    want = S.call_moe(M, c, dev, 2)
+    pitch = (2 ** 31 - 4096 - 1) // 2 - 64
+    x = spread(dev["x"], pitch // 63 // 8 * 8, math.nan)
+    out = spread(torch.zeros_like(dev["x"]), (5 << 30) // 2 // 63 // 8 * 8, 5.0)
+    got = S.call_moe(M, c, dict(dev, x=x), 2, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(M.Nvfp4Error):
+        S.call_moe(M, c, dict(dev, x=spread(dev["x"], 2 ** 30 // 63 // 8 * 8 + 8, 0.0)), 2)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+@pytest.mark.parametrize("hidden,inter", [(2 ** 20, 32), (32, 2 ** 20)])
+def test_moe_largest_layers(M, kind, hidden, inter):
+    c = S.moe_case(84, kind, 2, hidden, inter, 2)
+    say("moe largest", kind, hidden, inter)
+    S.check_moe(M, c, 1, True)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+def test_moe_most_workspace(M, kind):
+    """64 tokens whose values of h fill nearly 2^31 bytes: the last tokens' results are
+    those of a call with these tokens alone."""
+    hidden, inter, experts, top_k = 32, 2 ** 20, 8, 7
+    g = torch.Generator(device="cuda").manual_seed(85)
+    x = torch.randn(64, hidden, generator=g, device="cuda").to(torch.bfloat16)
+    dev = dict(x=x, logits=torch.randn(64, experts, generator=g, device="cuda"))
+    shapes = (("1", (experts, 2 * inter, hidden)), ("2", (experts, hidden, inter)))
+    for n, (e, rows, cols) in shapes:
+        if kind == "bf16":
+            dev["w" + n] = torch.empty(e, rows, cols, dtype=torch.bfloat16, device="cuda").normal_(0, cols ** -0.5, generator=g)
+        else:
+            dev["w" + n] = torch.randint(0, 256, (e, rows, cols // 2), generator=g, device="cuda", dtype=torch.uint8)
+            dev["s" + n] = torch.randint(0x20, 0x41, (e, rows, cols // 16), generator=g, device="cuda", dtype=torch.uint8)
+            dev["gs" + n] = torch.full((e,), (8 * cols) ** -0.5, device="cuda")
+    c = dict(kind=kind)
+    say("moe most workspace", kind)
+    out, ids, weights = S.call_moe(M, c, dev, top_k)
+    for first in (0, 30, 61):
+        few, few_ids, few_weights = S.call_moe(M, c, dict(dev, x=x[first:first + 3].contiguous(), logits=dev["logits"][first:first + 3]), top_k)
+        assert torch.equal(ids[first:first + 3], few_ids) and torch.equal(weights[first:first + 3], few_weights)
+        # the same FP32 sums, cut into other runs: two BF16 roundings, and some 2^10 roundings
+        # of random sign (2^20 terms) of 2^-24 of the largest sums
+        a, b = out[first:first + 3].double(), few.double()
+        assert bool(((a - b).abs() <= 2.0 ** -7 * b.abs() + 2.0 ** -10 * b.abs().amax()).all())
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "bf16"])
+@pytest.mark.parametrize("tokens", [2, 16, 40])
+def test_moe_rows_of_a_padded_batch_leave_the_others_alone(M, kind, tokens):
+    """Rows of x with NaN and infinities, and of logits with NaN, as a padded batch may
+    hold: the other rows' results keep every byte."""
+    c = S.moe_case(91, kind, tokens, 288, 96, 6)
+    dev = device(c)
+    say("moe padded rows", kind, tokens)
+    for top_k in (1, 3):
+        want = S.call_moe(M, c, dev, top_k)
+        for bad, logits in ((math.nan, False), (math.inf, False), (math.nan, True)):
+            rest = torch.arange(tokens) % 5 != 1
+            x, z = c["x"].clone(), c["logits"].clone()
+            x[~rest] = bad
+            x[~rest, ::3] = -bad
+            if logits:
+                z[~rest] = math.nan
+            got = S.call_moe(M, c, dict(dev, x=x.cuda(), logits=z.cuda()), top_k)
+            for a, b in zip(got, want):
+                assert torch.equal(host(a)[rest], host(b)[rest]), (top_k, bad, logits)
+            out = host(got[0])[~rest]
+            assert bool((out == 0).all() if logits else (~torch.isfinite(out)).any())
