@@ -104,20 +104,21 @@ nvfp4_status_t kv_block_tables(const int32_t *context_lens, const int32_t *query
  *           workspace may be NULL), 16-byte aligned.
  * Products are exact products of the BF16 q and the NVFP4 values, summed in
  * FP32; a query row is scaled by a power of two into FP16's range, where its
- * values are exact down to 2^-31 of the row's largest and smaller ones are off
- * by at most 2^-39 of that. Probabilities are
- * rounded to FP16 for the product with v: off by at most 2^-11 relative, or by
- * 2^-36 of the row's largest probability where that is more (so a tail of n
- * tokens is off by at most n 2^-36 of that). Sums are FP32. q, the global scales
- * and the scales of a request's L tokens must be finite (nvfp4_quantize_paged
- * writes no others from finite values); a NaN in k_gs or in a row of q makes out
- * and lse NaN in the rows that it reaches. Slots that no row can see (behind L, of hidden
- * pages, of no request) may hold anything. head_dim is 64, 128 or 256; heads a multiple of kv_heads, at most
- * 1024; ld_q, ld_out multiples of 8; q, out, packed caches 16-byte aligned,
- * scale caches 4-byte (8 for head_dim 128, 16 for 256); num_slots < 2^31,
- * tokens * heads <= 2^30, num_seqs <= 65535, num_seqs * kv_heads <= 2^22,
- * max_pages * page_size <= 2^30; window >= 2^31 hides nothing. One kernel,
- * or two where a long context is split over workgroups.
+ * values are exact down to 2^-31 of the row's largest and smaller ones are
+ * off by at most 2^-39 of that. Probabilities are rounded to FP16 for the
+ * product with v: off by at most 2^-11 relative, or by 2^-36 of the row's
+ * largest probability where that is more (so a tail of n tokens is off by at
+ * most n 2^-36 of that). Sums are FP32. q, the global scales and the scales
+ * of a request's L tokens must be finite (nvfp4_quantize_paged writes no
+ * others from finite values); a NaN in k_gs or in a row of q makes out and
+ * lse NaN in the rows that it reaches. Slots that no row can see (behind L,
+ * of hidden pages, of no request) may hold anything. head_dim is 64, 128 or
+ * 256; heads a multiple of kv_heads, at most 1024; ld_q, ld_out multiples of
+ * 8; q, out, packed caches 16-byte aligned, scale caches 4-byte (8 for
+ * head_dim 128, 16 for 256); num_slots < 2^31, tokens * heads <= 2^30,
+ * num_seqs <= 65535, num_seqs * kv_heads <= 2^22, max_pages * page_size <=
+ * 2^30; window >= 2^31 hides nothing. One kernel, or two where a long
+ * context is split over workgroups.
  */
 nvfp4_status_t nvfp4_paged_attention(const uint16_t *q, int64_t tokens, int64_t ld_q,
                                      int32_t heads, int32_t kv_heads, int32_t head_dim,
