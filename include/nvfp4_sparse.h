@@ -139,7 +139,8 @@ nvfp4_status_t nvfp4_select_pages(const uint16_t *q, int64_t tokens, int64_t ld_
  * token's own show nothing; a page listed twice counts twice. out and lse are those
  * of nvfp4_paged_attention, as are the types, layouts, roundings and limits; a row
  * that sees no token gets out = 0 and lse = -inf, rows of no request keep their
- * values. list_len is 0 to 2048, list_len * page_size <= 2^30.
+ * values. list_len is 0 to 2048, list_len * page_size <= 2^30, tokens * heads <=
+ * 2^23.
  * workspace: nvfp4_sparse_attention_workspace(...) bytes (may be 0, then
  * workspace may be NULL), 16-byte aligned. One kernel, or two where a row's list
  * is split over workgroups.
@@ -160,7 +161,8 @@ nvfp4_status_t nvfp4_sparse_attention(const uint16_t *q, int64_t tokens, int64_t
 /* Bytes of workspace that nvfp4_sparse_attention needs for these sizes (the same
  * arguments as the call's), or -1 where the call refuses them. Needs no GPU. */
 int64_t nvfp4_sparse_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_heads,
-                                         int32_t head_dim, int32_t page_size, int64_t list_len);
+                                         int32_t head_dim, int32_t page_size,
+                                         int64_t num_seqs, int64_t list_len);
 
 #ifdef __cplusplus
 }

@@ -334,12 +334,11 @@ __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, Table table
 }
 
 // One tile for a wave's query rows: scores, their exponentials and the sums. Row
-// rt's tokens are those of [lo[rt], hi[rt]) that the tile shows; all rows see
-// [all_begin, all_end).
-template <int D, int RT>
-__device__ __forceinline__ void attend(const Tile<D>& t, int t0, int lane, const half8v (&q)[RT][D / 32],
-                                       const float (&factor)[RT], const int (&lo)[RT], const int (&hi)[RT],
-                                       int all_begin, int all_end, float (&m)[RT], float (&l)[RT],
+// rt sees those of its 32 tokens whose bit is set in seen(rt), as far as the tile
+// shows them; `whole`: every row sees all.
+template <int D, int RT, class Seen>
+__device__ __forceinline__ void attend(const Tile<D>& t, int lane, const half8v (&q)[RT][D / 32], const float (&factor)[RT],
+                                       bool whole, Seen seen_by, float (&m)[RT], float (&l)[RT],
                                        float4v (&o)[RT][Tile<D>::C][Tile<D>::VM])
 {
     using T = Tile<D>;
@@ -367,7 +366,7 @@ __device__ __forceinline__ void attend(const Tile<D>& t, int t0, int lane, const
 
     // exponentials: base 2, against the row's reference
     const uint32_t hid = ~(uint32_t)__ballot(t.shown);     // bit j: token j does not count
-    const bool whole = hid == 0 && t0 >= all_begin && t0 + 32 <= all_end;
+    whole = whole && hid == 0;
     half8v p[RT];
     for (int rt = 0; rt < RT; ++rt) {
         float x[8];
@@ -375,7 +374,7 @@ __device__ __forceinline__ void attend(const Tile<D>& t, int t0, int lane, const
             x[i] = sc[rt][i >> 2][i & 3];
         float top = largest(x);
         if (!whole) {
-            const uint32_t seen = ~hid & bits_between(lo[rt] - t0, hi[rt] - t0);
+            const uint32_t seen = ~hid & seen_by(rt);
             for (int i = 0; i < 8; ++i) {
                 const int in = 16 * (i >> 2) + 4 * g + (i & 3);
                 x[i] = seen >> in & 1 ? x[i] : -INFINITY;
@@ -425,18 +424,18 @@ __device__ __forceinline__ void attend(const Tile<D>& t, int t0, int lane, const
     }
 }
 
-// LDS of a workgroup's four waves for joining their rows.
-template <int D>
+// LDS of a workgroup's W waves for joining their rows.
+template <int D, int W = 4>
 struct Joined {
-    float o[4][16][D + 4];
-    float m[4][16], l[4][16];
+    float o[W][16][D + 4];
+    float m[W][16], l[W][16];
 };
 
-// Joins the four waves, a row tile at a time, and writes the rows row0 ... of the
+// Joins the W waves, a row tile at a time, and writes the rows row0 ... of the
 // `rows` that begin at token `first`, or their part of the workspace where the
 // tokens are split; `used`: how many splits have work.
-template <int D, int RT>
-__device__ __forceinline__ void join_waves(const Attn& a, Joined<D>& lds, int split, int used, int first, int rows,
+template <int D, int RT, int W = 4>
+__device__ __forceinline__ void join_waves(const Attn& a, Joined<D, W>& lds, int split, int used, int first, int rows,
                                            int row0, int h, const float (&m)[RT], const float (&l)[RT],
                                            const float4v (&o)[RT][Tile<D>::C][Tile<D>::VM])
 {
@@ -458,12 +457,12 @@ __device__ __forceinline__ void join_waves(const Attn& a, Joined<D>& lds, int sp
         }
         __syncthreads();
         const int row = tid >> 4, r = row0 + 16 * rt + row;
-        if (r >= rows)
+        if (r >= rows || (W > 4 && row >= 16))
             continue;
-        float top = -INFINITY, total = 0, f[4];
-        for (int w = 0; w < 4; ++w)
+        float top = -INFINITY, total = 0, f[W];
+        for (int w = 0; w < W; ++w)
             top = fmaxf(top, lds.m[w][row]);
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < W; ++w) {
             f[w] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lds.m[w][row] - top);
             total += f[w] * lds.l[w][row];
         }
@@ -473,7 +472,7 @@ __device__ __forceinline__ void join_waves(const Attn& a, Joined<D>& lds, int sp
         const float norm = whole_row ? (total != 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
         for (int d = (tid & 15) * 4; d < D; d += 64) {
             float4v v = {0, 0, 0, 0};
-            for (int w = 0; w < 4; ++w)
+            for (int w = 0; w < W; ++w)
                 v += f[w] * *(float4v*)&lds.o[w][row][d];
             v *= norm;
             if (whole_row)

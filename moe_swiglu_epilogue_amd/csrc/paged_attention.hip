@@ -113,7 +113,8 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
         }
 
         auto compute = [&](const Tile<D>& t, int t0) {
-            attend<D, RT>(t, t0, lane, q, factor, lo, hi, s.all_begin, s.all_end, m, l, o);
+            attend<D, RT>(t, lane, q, factor, t0 >= s.all_begin && t0 + 32 <= s.all_end,
+                          [&](int rt) { return bits_between(lo[rt] - t0, hi[rt] - t0); }, m, l, o);
         };
         for (; t0 < last; t0 += 256) {
             compute(even, t0);

@@ -1,11 +1,13 @@
 // Attention over listed pages of the paged NVFP4 cache (include/nvfp4_sparse.h).
 //
-// A token's listed pages, one behind the other, are a range of list_len *
-// page_size tokens, which a workgroup walks in tiles of 32 as the rows kernel of
-// paged_attention.hip does with a request's tokens (attention_rows.hpp): the same
-// arithmetic, one (token, key/value head) a workgroup, whose query rows are the
-// heads that share the key/value head. The workgroup first looks the list up: for
-// each entry the page in the cache and how many of its tokens the query sees.
+// A workgroup takes some tokens that follow each other and a key/value head; its
+// query rows are the heads that share the key/value head, of all its tokens. It
+// first looks the tokens' lists up and joins them into one list of pages, with a
+// bit for each token that has listed the page. The pages, one behind the other,
+// are a range of tokens that its waves walk in tiles of 32 as the rows kernel of
+// paged_attention.hip does with a request's tokens (attention_rows.hpp); what a
+// row sees of a tile is a word of bits made from the page's bits and the row's
+// position. A page that several tokens list is loaded and converted once.
 #include "attention_rows.hpp"
 #include "nvfp4_sparse.h"
 
@@ -17,6 +19,7 @@ struct Sparse {
     Attn a;
     const int32_t* pages;
     int list_len;
+    int together;      // tokens that a workgroup takes
 };
 
 // The request of token t, -1 if it is none's: the last b with offsets[b] <= t.
@@ -30,25 +33,116 @@ __device__ __forceinline__ int request_of(const Attn& a, int t, int lane)
     return b >= a.num_seqs ? -1 : b;
 }
 
-// The listed pages of a workgroup's range: the page in the cache, -1 where the
-// query sees nothing of it, and the number of its tokens that it sees.
+// The listed pages that some token sees: the page in the cache, the position of its
+// first token in the request, and a bit for each token that listed it. While the
+// list is made: `first` is the page's number in the request, -1 for an entry that
+// shows nothing.
 struct Listed {
-    int page[kMostListed], seen[kMostListed];
+    int page[kMostListed], first[kMostListed];
+    uint16_t by[kMostListed];
 };
 
-template <int D>
+template <int D, int W>
 union Shared {
-    Joined<D> joined;
+    Joined<D, W> joined;
     Listed list;
 };
 
-template <int D, int RT, bool kPaged16>
-__global__ __launch_bounds__(256, (D * RT <= 256 ? 2 : 1)) void sparse_rows_kernel(Sparse s)
+template <int W>
+struct Counts {
+    int n[W];
+    int repeated;
+};
+
+// Looks up the lists of the tokens t, ..., t + run - 1 of request b, the first of them
+// at position pos0, and joins them. Returns the number of pages; `run` becomes 1
+// where a token has listed a page twice, which then counts twice.
+template <int W>
+__device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W>& counts, int b, int t, int h, int pos0,
+                                         int& run)
+{
+    const Attn& a = s.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int pitch = (s.list_len + 3) & ~3;
+    int entries = run * pitch;
+    if (tid == 0)
+        counts.repeated = 0;
+    for (int e = tid; e < entries; e += 64 * W) {
+        const int token = run == 1 ? 0 : e / pitch, i = e - token * pitch;
+        const int p = i < s.list_len ? s.pages[((int64_t)(t + token) * a.kv_heads + h) * s.list_len + i] : -1;
+        int page = -1;
+        if (p >= 0 && p < a.max_pages && (int64_t)p * a.page <= pos0 + token)
+            page = a.table[b * a.ld_table + p];
+        const bool in = page >= 0 && page < a.num_pages;
+        list.page[e] = page;
+        list.first[e] = in ? p : -1;
+        list.by[e] = in ? 1 : 0;
+    }
+    __syncthreads();
+    if (run > 1) {
+        // an entry stands for its page if no token before has listed it
+        for (int e = tid; e < entries; e += 64 * W) {
+            const int p = list.first[e], token = e / pitch;
+            if (p < 0)
+                continue;
+            int by = 0, own = 0;
+            for (int other = 0; other < run; ++other) {
+                int found = 0;
+                for (int i = 0; i < pitch; i += 4) {
+                    const int4 v = *(const int4*)&list.first[other * pitch + i];
+                    found += (v.x == p) + (v.y == p) + (v.z == p) + (v.w == p);
+                }
+                by |= found ? 1 << other : 0;
+                own = other == token ? found : own;
+            }
+            if (own > 1)
+                counts.repeated = 1;
+            list.by[e] = (uint16_t)(by & ((1 << token) - 1) ? 0 : by);
+        }
+        __syncthreads();
+        if (counts.repeated) {
+            run = 1;
+            entries = pitch;
+            for (int e = tid; e < entries; e += 64 * W)
+                list.by[e] = list.first[e] >= 0 ? 1 : 0;
+            __syncthreads();
+        }
+    }
+    // the entries that stand for a page, moved to the front
+    int total = 0;
+    for (int base = 0; base < entries; base += 64 * W) {
+        const int e = base + tid;
+        const int by = e < entries ? list.by[e] : 0;
+        const int page = by ? list.page[e] : 0, p = by ? list.first[e] : 0;
+        const uint64_t in = __ballot(by != 0);
+        if (lane == 0)
+            counts.n[wave] = __popcll(in);
+        __syncthreads();
+        int at = total + __popcll(in & ((1ull << lane) - 1));
+        for (int w = 0; w < W; ++w) {
+            at += w < wave ? counts.n[w] : 0;
+            total += counts.n[w];
+        }
+        if (by) {
+            list.page[at] = page;
+            list.first[at] = p * a.page;
+            list.by[at] = (uint16_t)by;
+        }
+        __syncthreads();
+    }
+    return total;
+}
+
+template <int D, int RT, bool kPaged16, int W>
+constexpr int kSparseWaves = W == 8 ? 1 : RT == 1 && D <= 128 && kPaged16 ? 3 : D * RT <= 256 ? 2 : 1;
+
+template <int D, int RT, bool kPaged16, int W>
+__global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sparse_rows_kernel(Sparse s)
 {
     using T = Tile<D>;
-    constexpr int C = T::C, KF = D / 32, VM = T::VM;
-    __shared__ Shared<D> lds;
-    __shared__ int ends[4];
+    constexpr int C = T::C, KF = D / 32, VM = T::VM, kStep = 32 * W;
+    __shared__ Shared<D, W> lds;
+    __shared__ Counts<W> counts;
     const Attn& a = s.a;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -56,86 +150,80 @@ __global__ __launch_bounds__(256, (D * RT <= 256 ? 2 : 1)) void sparse_rows_kern
     const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
 
     // As in the rows kernel: all key/value heads of a token go to one XCD
-    const int64_t per_split = (int64_t)a.tokens * a.row_blocks;
-    const int64_t units = (per_split * a.splits + 7) / 8 * 8 * a.kv_heads;
-    for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const int64_t j = unit >> 3, work = j / a.kv_heads * 8 + (unit & 7);
-        const int h = (int)(j % a.kv_heads);
-        if (work >= per_split * a.splits)
-            continue;
-        const int split = (int)(work / per_split);
-        const int64_t item = work % per_split;
-        const int token = (int)(item / a.row_blocks), row0 = (int)(item % a.row_blocks) * 16 * RT;
+    const uint32_t groups = (uint32_t)(a.tokens + s.together - 1) / s.together;
+    const uint32_t per_split = groups * a.row_blocks, works = per_split * a.splits;
+    const uint32_t j = blockIdx.x >> 3, work = j / a.kv_heads * 8 + (blockIdx.x & 7);
+    if (work >= works)
+        return;
+    const int h = (int)(j % a.kv_heads);
+    const int split = (int)(work / per_split);
+    const uint32_t item = work % per_split;
+    const int row0 = (int)(item % a.row_blocks) * 16 * RT;
+    int token = (int)(item / a.row_blocks) * s.together;
+    const int token_end = min(token + s.together, a.tokens);
+    // the tokens of one request at a time
+    for (int run = 1; token < token_end; token += run) {
+        run = 1;
         const int b = request_of(a, token, lane);
         if (b < 0)
             continue;
+        const int behind = a.offsets[b + 1];
+        run = min(token_end, behind) - token;
         const int len = a.num_pages > 0 ? min(max(a.lens[b], 0), a.max_pages * a.page) : 0;
-        const int position = min(len - a.offsets[b + 1] + token, len - 1);
-
-        // the list of this split
-        const int first = split * a.chunk;
-        const int most = min(first + a.chunk, s.list_len * a.page);
-        const int page0 = (int)page_of(a, first), pages = most > first ? (int)page_of(a, most - 1) - page0 + 1 : 0;
-        const int32_t* list = s.pages + ((int64_t)token * a.kv_heads + h) * s.list_len + page0;
-        int used = 0;
-        __syncthreads();                        // the LDS of the item before is read
-        for (int i = tid; i < pages; i += 256) {
-            const int p = list[i];
-            int entry = -1, seen = 0;
-            if (p >= 0 && p < a.max_pages) {
-                entry = a.table[b * a.ld_table + p];
-                // a page behind the token's own: nothing
-                seen = (int)min(max((int64_t)position + 1 - (int64_t)p * a.page, (int64_t)0), (int64_t)a.page);
-            }
-            const bool in = entry >= 0 && entry < a.num_pages && seen > 0;
-            lds.list.page[i] = in ? entry : -1;
-            lds.list.seen[i] = in ? seen : 0;
-            used = in ? i + 1 : used;
-        }
-        for (int d = 32; d; d >>= 1)
-            used = max(used, __shfl_xor(used, d));
-        if (lane == 0)
-            ends[wave] = used;
-        __syncthreads();
-        used = max(max(ends[0], ends[1]), max(ends[2], ends[3]));
-        const int last = __builtin_amdgcn_readfirstlane((int)min((int64_t)most, ((int64_t)page0 + used) * a.page));
+        const int pos0 = min(len - behind + token, len - 1);
+        __syncthreads();                        // the LDS of what came before is read
+        const int range = make_list<W>(s, lds.list, counts, b, token, h, pos0, run) * a.page;
+        // the splits take equal parts of what there is
+        const int chunk = a.splits == 1 ? range : ((range + a.splits - 1) / a.splits + 127) & ~127;
+        const int first = split * chunk, last = __builtin_amdgcn_readfirstlane(min(first + chunk, range));
 
         auto entries = [&](int t0) {
-            Entries r = {{-1, -1}};
-            if (kPaged16)
-                for (int hh = 0; hh < 2; ++hh)
-                    if (t0 + 16 * hh < last)
-                        r.e[hh] = __builtin_amdgcn_readfirstlane(lds.list.page[(int)page_of(a, t0 + 16 * hh) - page0]);
+            Entries r;
+            for (int hh = 0; hh < 2; ++hh) {
+                const int at = t0 + 16 * hh;
+                const bool in = kPaged16 && at < last;
+                r.e[hh] = in ? __builtin_amdgcn_readfirstlane(lds.list.page[page_of(a, at)]) : -1;
+            }
             return r;
         };
-        auto request = [&](Tile<D>& t, int t0) {
-            if (t0 >= last)
+        auto request = [&](Tile<D>& t, Entries e, int t0) {
+            if (!kPaged16 && t0 >= last)
                 return;
-            load_tile<D, kPaged16>(t, a, lds.list.page - page0, entries(t0), h, t0, first, last, lane);
-            const int at = min(t0 + (lane & 31), last - 1), p = (int)page_of(a, at);
-            t.shown = t.shown && at - p * a.page < lds.list.seen[p - page0];
-            __builtin_amdgcn_sched_barrier(0);
+            load_tile<D, kPaged16>(t, a, lds.list.page, e, h, t0, first, last, lane);
+            __builtin_amdgcn_sched_barrier(0);      // no use of the other tile moves up here
         };
+        int t0 = first + 32 * wave;
+        Entries e0 = entries(t0), e1 = entries(t0 + kStep);
+
+        uint4v w[RT][KF];
+        int bit[RT], pos[RT];
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = row0 + 16 * rt + n, rr = min(r, run * group - 1);
+            const int of = run == 1 ? 0 : rr / group;
+            bit[rt] = r < run * group ? of : 31;
+            pos[rt] = pos0 + of;
+            const uint16_t* src = a.q + (token + of) * a.ld_q + (h * group + rr - of * group) * D;
+            for (int f = 0; f < KF; ++f)
+                w[rt][f] = *(const uint4v*)(src + (D > 64 ? 128 * (f / 4) + 32 * g + 8 * (f % 4) : 16 * g + 8 * f));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        Tile<D> even, odd;
+        request(even, e0, t0);
+        request(odd, e1, t0 + kStep);
+        e0 = entries(t0 + 2 * kStep);
+        e1 = entries(t0 + 3 * kStep);
 
         half8v q[RT][KF];
         float factor[RT];
-        int lo[RT], hi[RT];
         for (int rt = 0; rt < RT; ++rt) {
-            const int r = row0 + 16 * rt + n;
-            lo[rt] = 0;
-            hi[rt] = r < group ? INT32_MAX : 0;
-            const uint16_t* src = a.q + token * a.ld_q + (h * group + min(r, group - 1)) * D;
-            uint4v w[KF];
             uint32_t top = 0;
-            for (int f = 0; f < KF; ++f) {
-                w[f] = *(const uint4v*)(src + (D > 64 ? 128 * (f / 4) + 32 * g + 8 * (f % 4) : 16 * g + 8 * f));
-                top = largest_bits(w[f], top);
-            }
+            for (int f = 0; f < KF; ++f)
+                top = largest_bits(w[rt][f], top);
             top = max(top, (uint32_t)__shfl_xor((int)top, 16));
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
             const int e = fp16_exponent(top);
             for (int f = 0; f < KF; ++f)
-                q[rt][f] = scaled_half8(w[f], e, k_scale < 0);
+                q[rt][f] = scaled_half8(w[rt][f], e, k_scale < 0);
             factor[rt] = score_factor(k_scale, e);
         }
 
@@ -148,31 +236,81 @@ __global__ __launch_bounds__(256, (D * RT <= 256 ? 2 : 1)) void sparse_rows_kern
                 for (int i = 0; i < VM; ++i)
                     o[rt][c][i] = float4v{0, 0, 0, 0};
         }
-        for (int t0 = first + 32 * wave; t0 < last; t0 += 128) {
-            Tile<D> tile;
-            request(tile, t0);
-            attend<D, RT>(tile, t0, lane, q, factor, lo, hi, 0, INT32_MAX, m, l, o);
+        const int everyone = (1 << run) - 1;
+        auto compute = [&](Tile<D>& t, int t0) {
+            bool whole = true;
+            uint32_t seen[RT];
+            if (kPaged16) {
+                int place[2], by[2];
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int at = min(t0 + 16 * hh, last - 16), i = (int)page_of(a, at);
+                    place[hh] = __builtin_amdgcn_readfirstlane(lds.list.first[i]) + (at - i * a.page);
+                    by[hh] = __builtin_amdgcn_readfirstlane(lds.list.by[i]);
+                    whole = whole && by[hh] == everyone && place[hh] + 15 <= pos0;
+                }
+                // what lies behind the request's tokens may be anything
+                t.shown = t.shown && ((lane & 16) ? place[1] : place[0]) + n < len;
+                for (int rt = 0; rt < RT; ++rt)
+                    seen[rt] = ~0u;
+                if (!whole)
+                    for (int rt = 0; rt < RT; ++rt) {
+                        seen[rt] = 0;
+                        for (int hh = 0; hh < 2; ++hh)
+                            seen[rt] |= by[hh] >> bit[rt] & 1 ? bits_between(0, min(pos[rt] - place[hh] + 1, 16)) << 16 * hh : 0;
+                    }
+            } else {
+                const int at = t0 + (lane & 31), i = (int)page_of(a, min(at, last - 1));
+                const int place = lds.list.first[i] + (at - i * a.page);
+                const int by = at < last ? lds.list.by[i] : 0;
+                t.shown = t.shown && place < len;
+                for (int rt = 0; rt < RT; ++rt)
+                    seen[rt] = 0;
+                for (int k = 0; k < run; ++k) {
+                    const uint32_t all = (uint32_t)__ballot((by >> k & 1) && place <= pos0 + k);
+                    whole = whole && all == ~0u;
+                    for (int rt = 0; rt < RT; ++rt)
+                        seen[rt] = bit[rt] == k ? all : seen[rt];
+                }
+            }
+            attend<D, RT>(t, lane, q, factor, whole, [&](int rt) { return seen[rt]; }, m, l, o);
+        };
+        for (; t0 < last; t0 += 2 * kStep) {
+            compute(even, t0);
+            request(even, e0, t0 + 2 * kStep);
+            e0 = entries(t0 + 4 * kStep);
+            if (t0 + kStep < last)
+                compute(odd, t0 + kStep);
+            request(odd, e1, t0 + 3 * kStep);
+            e1 = entries(t0 + 5 * kStep);
         }
         __syncthreads();                        // the list is read, its LDS goes to the join
-        join_waves<D, RT>(a, lds.joined, split, a.splits, token, group, row0, h, m, l, o);
+        join_waves<D, RT, W>(a, lds.joined, split, a.splits, token, run * group, row0, h, m, l, o);
     }
 }
 
-// How the work is cut: 16 RT query rows a workgroup, and splits of the listed
-// tokens where there are too few workgroups for the card.
+// How the work is cut: tokens that a workgroup takes together, its query rows, and
+// splits of the listed tokens where there are too few workgroups for the card.
 struct SparsePlan {
-    int block, row_blocks, splits, chunk;
+    int together, block, row_blocks, splits, waves;
 };
 
 SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t page_size,
-                       int64_t list_len)
+                       int64_t num_seqs, int64_t list_len)
 {
     using serving::ceil_div;
     SparsePlan p;
     const int group = heads / kv_heads;
-    p.block = head_dim > 128 ? 16 : group <= 64 ? ceil_div(group, 16) * 16 : 64;
-    p.row_blocks = ceil_div(group, p.block);
-    const int64_t range = list_len * page_size, items = tokens * kv_heads * p.row_blocks;
+    const int64_t pitch = ceil_div(list_len, (int64_t)4) * 4;
+    const int64_t average = tokens / (num_seqs < 1 ? 1 : num_seqs);
+    p.together = 1;
+    while (p.together < average && (p.together + 1) * group <= 16 && (p.together + 1) * pitch <= 1024 &&
+           (p.together + 1) * list_len * page_size <= (1 << 30))
+        ++p.together;
+    const int rows = p.together * group;
+    p.block = head_dim > 128 ? 16 : rows <= 64 ? ceil_div(rows, 16) * 16 : 64;
+    p.row_blocks = ceil_div(rows, p.block);
+    const int64_t range = list_len * page_size;
+    const int64_t items = ceil_div(tokens, (int64_t)p.together) * kv_heads * p.row_blocks;
     const int64_t slots = 512;
     int64_t splits = items < 1 ? 1 : slots / items;
     if (splits > ceil_div(range, (int64_t)128))
@@ -181,29 +319,29 @@ SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t 
         splits = 256;
     if (splits < 1 || tokens * heads > (1 << 22))
         splits = 1;
-    const int64_t chunk = ceil_div(ceil_div(range, splits), (int64_t)128) * 128;
-    p.chunk = (int)(chunk < 128 ? 128 : chunk);
-    p.splits = (int)ceil_div(range < 1 ? 1 : range, (int64_t)p.chunk);
+    p.splits = (int)splits;
+    p.waves = 4;
     return p;
 }
 
+// Pages of whole 16 tokens are read a half tile at a time, scales also where there is
+// nothing to see; so there must be a page.
 template <int D, int RT>
 void launch_rows(const Sparse& s, dim3 grid, hipStream_t stream)
 {
-    if (s.a.page % 16 == 0)
-        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, true>), grid, dim3(256), 0, stream, s);
+    if (s.a.page % 16 == 0 && s.a.num_pages > 0)
+        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, true, 4>), grid, dim3(256), 0, stream, s);
     else
-        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, false>), grid, dim3(256), 0, stream, s);
+        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, false, 4>), grid, dim3(256), 0, stream, s);
 }
 
 template <int D>
 void launch(const Sparse& s, int block, hipStream_t stream)
 {
     const Attn& a = s.a;
-    const int64_t work = (int64_t)a.tokens * a.row_blocks * a.splits;
-    const int64_t units = (work + 7) / 8 * 8 * a.kv_heads;
-    // a grid holds less than 2^32 threads; workgroups take several items beyond 2^22
-    const dim3 grid((unsigned)(units < (1 << 22) ? units : 1 << 22));
+    const int64_t groups = (a.tokens + (int64_t)s.together - 1) / s.together;
+    const int64_t units = (groups * a.row_blocks * a.splits + 7) / 8 * 8 * a.kv_heads;
+    const dim3 grid((unsigned)units);
     if (block == 16) {
         launch_rows<D, 1>(s, grid, stream);
     } else if constexpr (D <= 128) {
@@ -227,19 +365,20 @@ bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t page_size
 
 bool sizes_supported(int64_t tokens, int32_t heads, int32_t head_dim, int32_t page_size, int64_t list_len)
 {
-    return (head_dim == 64 || head_dim == 128 || head_dim == 256) && heads <= 1024 && tokens <= (1 << 30) / heads &&
+    return (head_dim == 64 || head_dim == 128 || head_dim == 256) && heads <= 1024 && tokens <= (1 << 23) / heads &&
            list_len <= kMostListed && list_len <= (1 << 30) / page_size;
 }
 
 }  // namespace
 
 extern "C" int64_t nvfp4_sparse_attention_workspace(int64_t tokens, int32_t heads, int32_t kv_heads,
-                                                    int32_t head_dim, int32_t page_size, int64_t list_len)
+                                                    int32_t head_dim, int32_t page_size, int64_t num_seqs,
+                                                    int64_t list_len)
 {
-    if (!sizes_ok(tokens, heads, kv_heads, page_size, list_len) ||
+    if (num_seqs < 0 || !sizes_ok(tokens, heads, kv_heads, page_size, list_len) ||
         !sizes_supported(tokens, heads, head_dim, page_size, list_len))
         return -1;
-    const SparsePlan p = sparse_plan(tokens, heads, kv_heads, head_dim, page_size, list_len);
+    const SparsePlan p = sparse_plan(tokens, heads, kv_heads, head_dim, page_size, num_seqs, list_len);
     return p.splits > 1 ? tokens * heads * 4 * ((head_dim + 2) * p.splits + 1) : 0;
 }
 
@@ -273,10 +412,11 @@ extern "C" nvfp4_status_t nvfp4_sparse_attention(
         !aligned(seq_lens, 4) || !aligned(query_offsets, 4) || !aligned(pages, 4) || !aligned(k_gs, 4) ||
         !aligned(v_gs, 4) || !aligned(lse, 4) || !aligned(workspace, 16))
         return NVFP4_ERROR_MISALIGNED;
-    const int64_t need = nvfp4_sparse_attention_workspace(tokens, heads, kv_heads, head_dim, page_size, list_len);
+    const int64_t need = nvfp4_sparse_attention_workspace(tokens, heads, kv_heads, head_dim, page_size, num_seqs,
+                                                          list_len);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return NVFP4_ERROR_INVALID_VALUE;
-    const SparsePlan p = sparse_plan(tokens, heads, kv_heads, head_dim, page_size, list_len);
+    const SparsePlan p = sparse_plan(tokens, heads, kv_heads, head_dim, page_size, num_seqs, list_len);
     Sparse s = {};
     Attn& a = s.a;
     a.q = q;
@@ -310,8 +450,8 @@ extern "C" nvfp4_status_t nvfp4_sparse_attention(
     a.page_shift = 31 + shift;
     a.page_magic = (uint32_t)((((uint64_t)1 << a.page_shift) + page_size - 1) / page_size);
     a.splits = p.splits;
-    a.chunk = p.chunk;
     a.row_blocks = p.row_blocks;
+    s.together = p.together;
     s.pages = pages;
     s.list_len = (int)list_len;
     if (head_dim == 64)

@@ -36,7 +36,7 @@ def _lib():
                                          _i64, _i32, _i32, _i32, _vp, _vp]
         L.nvfp4_sparse_attention.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _i64,
                                              _vp, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
-        L.nvfp4_sparse_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64]
+        L.nvfp4_sparse_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64, _i64]
         for fn in (L.nvfp4_rope_append, L.nvfp4_page_keys, L.nvfp4_select_pages, L.nvfp4_sparse_attention):
             fn.restype = C.c_int
         L.nvfp4_sparse_attention_workspace.restype = _i64
@@ -265,7 +265,7 @@ def nvfp4_sparse_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: to
     vg = _scalar(v_gs, "v_gs", _F32, device)
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
-    need = _sparse_workspace(tokens, heads, kv, dim, page_size, listed)
+    need = _sparse_workspace(tokens, heads, kv, dim, page_size, n, listed)
 
     def launch(st):
         o, z, zp = out, None, None

@@ -390,6 +390,27 @@ def test_sparse_attention_split(M, heads, kv, dim, page, n):
     check_sparse(M, c, lists(c, kv, n, 5))
 
 
+@pytest.mark.parametrize("heads,kv,dim,page", [(8, 2, 128, 16), (4, 4, 64, 32), (8, 8, 128, 6), (16, 2, 128, 32), (15, 3, 256, 16),
+                                               (5, 5, 256, 7), (12, 1, 64, 64), (3, 1, 64, 1)])
+@pytest.mark.parametrize("n", [3, 20])
+def test_sparse_attention_tokens_that_share_pages(M, heads, kv, dim, page, n):
+    """Chunks of tokens, whose lists are joined: pages that some, all or one of them
+    list, in any order; requests that end inside a group of tokens; lists with a
+    page listed twice among the others; entries that show nothing."""
+    totals, news = [40 * page, 9 * page + 3, 5, 25 * page + 1], [37, 6, 5, 21]
+    c = request_case(heads + dim + page, kv, dim, page, totals, news, heads=heads, pad=3)
+    g = torch.Generator().manual_seed(n)
+    tokens, width = c["q"].shape[0], c["table"].shape[1]
+    common = torch.rand(1, kv, width, generator=g)
+    p = (common + 0.5 * torch.rand(tokens, kv, width, generator=g)).argsort(-1)[..., :n].int().contiguous()
+    p[torch.rand(p.shape, generator=g) < 0.1] = -1
+    say("sparse chunks", heads, kv, dim, page, n)
+    check_sparse(M, c, p, gs=(0.7, 1.9))
+    p[9, :, 1], p[20, 0, 2], p[50, -1, 0] = p[9, :, 0], p[20, 0, 0], p[50, -1, 1]
+    p[30:33] = lists(c, kv, n, 4, wild=True)[30:33]
+    check_sparse(M, c, p)
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_sparse_attention_rows_that_see_nothing(M, dim):
     """Empty contexts, queries before the context, hidden pages, empty lists, lists of

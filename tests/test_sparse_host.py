@@ -148,16 +148,17 @@ def test_sparse_workspace(lib):
     """None for many tokens; for few an output row, a reference and a sum a split, and
     a count a row."""
     size = lib.nvfp4_sparse_attention_workspace
-    assert size(4096, 32, 8, 128, 64, 32) == 0 and size(0, 32, 8, 128, 64, 32) >= 0 and size(1, 8, 8, 128, 16, 0) == 0
-    n = size(1, 32, 8, 128, 64, 32)
+    assert size(4096, 32, 8, 128, 64, 1, 32) == 0 and size(0, 32, 8, 128, 64, 2, 32) >= 0 and size(1, 8, 8, 128, 16, 1, 0) == 0
+    n = size(1, 32, 8, 128, 64, 1, 1000)
     assert n > 0 and (n // 4 // 32 - 1) % 130 == 0
-    for bad in ((-1, 8, 8, 128, 16, 4), (1, 8, 3, 128, 16, 4), (1, 8, 8, 96, 16, 4), (1, 8, 8, 128, 0, 4), (1, 8, 8, 128, 16, 2049),
-                (1, 8, 8, 128, 2 ** 20, 1025), (2 ** 28, 8, 8, 128, 16, 4)):
+    for bad in ((-1, 8, 8, 128, 16, 1, 4), (1, 8, 3, 128, 16, 1, 4), (1, 8, 8, 96, 16, 1, 4), (1, 8, 8, 128, 0, 1, 4),
+                (1, 8, 8, 128, 16, 1, 2049), (1, 8, 8, 128, 2 ** 20, 1, 1025), (2 ** 28, 8, 8, 128, 16, 1, 4),
+                (1, 8, 8, 128, 16, -1, 4)):
         assert size(*bad) == -1, bad
-    # a split's range never passes 32 bits
     for page, listed in ((2 ** 30, 1), (2 ** 19, 2048), (1, 2048), (524287, 2048)):
         for tokens in (1, 3, 100):
-            assert size(tokens, 8, 1, 64, page, listed) >= 0
+            for seqs in (0, 1, 50):
+                assert size(tokens, 8, 1, 64, page, seqs, listed) >= 0
 
 
 # ---- the definitions -------------------------------------------------------------
