@@ -118,8 +118,8 @@ nvfp4_status_t nvfp4_page_keys(const uint8_t *k_packed, const uint8_t *k_scales,
  * specified; its list is valid). head_dim is 64, 128 or 256; heads a multiple of
  * kv_heads, at most 1024; top_k, first >= 0, local >= 1, first + top_k + local <=
  * 2048; max_pages <= 32768 and max_pages * page_size <= 2^30; num_seqs <= 65535,
- * num_slots < 2^31, tokens * heads <= 2^30; exponents 0 to 64; ld_q a multiple of 8; q and
- * keys 16-byte aligned. One kernel.
+ * num_slots < 2^31, tokens * heads <= 2^23; exponents are taken to be 0 to 64; ld_q a
+ * multiple of 8; q and keys 16-byte aligned. One kernel.
  */
 nvfp4_status_t nvfp4_select_pages(const uint16_t *q, int64_t tokens, int64_t ld_q, int32_t heads,
                                   int32_t kv_heads, int32_t head_dim, const int8_t *keys,

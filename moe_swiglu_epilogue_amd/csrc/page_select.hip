@@ -113,9 +113,12 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 }
 
 // ---- selection -----------------------------------------------------------------
-// A workgroup takes a token and a key/value head: scores of all pages in front of
-// the token's own ones as ordered whole numbers in LDS, the top_k-th of them
-// by counting their leading bytes, then the listed pages in order.
+// A workgroup takes a token, or some that follow each other in one request, and a
+// key/value head. Scores are products of whole numbers on the matrix cores
+// (v_mfma_i32_16x16x64_i8): a page a row, a query row a column, so the largest of a
+// token's rows is found within 16 lanes. They go to LDS as FP32, exactly. Then the
+// top_k-th largest is searched, by all waves for a single token and by a wave each
+// for several, and the listed pages are written in order.
 struct Select {
     const uint16_t* q;
     const int8_t *keys, *exponents;
@@ -123,7 +126,14 @@ struct Select {
     Requests r;
     int64_t ld_q;
     int tokens, heads, kv_heads, top, first, local;
+    int together;      // tokens that a workgroup takes
+    int pitch;         // scores of a token in LDS
 };
+
+constexpr int kMostRows = 64;      // query rows that are compared at once
+constexpr int kBins = 256;
+
+typedef int int4v __attribute__((ext_vector_type(4)));
 
 // The request of token t, -1 if it is none's: the last b with offsets[b] <= t.
 __device__ __forceinline__ int request_of(const Requests& r, int t)
@@ -137,187 +147,400 @@ __device__ __forceinline__ int request_of(const Requests& r, int t)
     return b >= r.num_seqs ? -1 : b;
 }
 
-// FP32 as whole numbers in the same order; finite ones are above 0 and below 2^32 - 1.
+// FP32 as whole numbers in the same order.
 __device__ __forceinline__ uint32_t ordered(float v)
 {
     const uint32_t b = __float_as_uint(v);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads) void select_pages_kernel(Select a)
+template <int kCtrl>
+__device__ __forceinline__ int other_lane(int v)
 {
-    extern __shared__ uint32_t score[];                   // of each page; 0: not to be chosen
-    __shared__ uint32_t q8[64][D / 4];
-    __shared__ uint32_t count[256];
-    __shared__ uint32_t tops[kThreads / 64], chosen[2];
-    __shared__ uint32_t taken[kThreads / 64], ties[kThreads / 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int group = a.heads / a.kv_heads, width = a.first + a.top + a.local;
-    for (int64_t item = blockIdx.x; item < (int64_t)a.tokens * a.kv_heads; item += gridDim.x) {
-        __syncthreads();                                  // the LDS of the item before is read
-        const int64_t t = item / a.kv_heads;
-        const int h = (int)(item % a.kv_heads);
-        const int b = request_of(a.r, (int)t);
-        if (b < 0)
-            continue;
-        int32_t* out = a.pages + (t * a.kv_heads + h) * width;
-        const int len = length_of(a.r, b);
-        const int64_t p = min((int64_t)len - a.r.offsets[b + 1] + t, (int64_t)len - 1);
-        if (p < 0) {
-            for (int i = tid; i < width; i += kThreads)
-                out[i] = -1;
-            continue;
-        }
-        const int own = (int)(p / a.r.page), before = max(own - a.local + 1, 0);    // [first, before): by score
-        const int32_t* table = a.r.table + b * a.r.ld_table;
+    return __builtin_amdgcn_mov_dpp(v, kCtrl, 0xf, 0xf, true);
+}
 
-        // the queries in 8 bits
-        const uint16_t* q = a.q + t * a.ld_q + h * group * D;
-        uint32_t top = 0;
-        for (int i = tid; i < group * D / 8; i += kThreads) {
-            const uint4v w = *(const uint4v*)(q + 8 * i);
-            for (int k = 0; k < 4; ++k)
-                top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
-        }
-        for (int d = 32; d; d >>= 1)
-            top = max(top, (uint32_t)__shfl_xor((int)top, d));
-        if (lane == 0)
-            tops[wave] = top;
-        __syncthreads();
-        for (int w = 0; w < kThreads / 64; ++w)
-            top = max(top, tops[w]);
-        const int e = top == 0 || top >= 0x7f800000u ? 0 : ilogbf(__uint_as_float(top)) - 6;
+// Largest of `width` neighbouring lanes (1, 2, 4, 8 or 16), in all of them.
+__device__ __forceinline__ int max_of(int v, int width)
+{
+    if (width > 1)
+        v = max(v, other_lane<0xb1>(v));        // lane ^ 1
+    if (width > 2)
+        v = max(v, other_lane<0x4e>(v));        // lane ^ 2
+    if (width > 4)
+        v = max(v, other_lane<0x141>(v));       // 7 - lane of eight
+    if (width > 8)
+        v = max(v, other_lane<0x140>(v));       // 15 - lane of sixteen
+    return v;
+}
 
-        for (int j = tid; j < own + 1; j += kThreads)
-            score[j] = 0;
-        for (int h0 = 0; h0 < group; h0 += 64) {
-            const int rows = min(group - h0, 64);
-            __syncthreads();
-            for (int i = tid; i < rows * D / 4; i += kThreads) {
-                uint32_t w = 0;
-                for (int k = 0; k < 4; ++k) {
-                    const float x = ldexpf(__uint_as_float((uint32_t)q[h0 * D + 4 * i + k] << 16), -e);
-                    w |= (uint32_t)((int)rintf(fminf(fmaxf(x, -127.0f), 127.0f)) & 255) << (8 * k);
-                }
-                q8[i / (D / 4)][i % (D / 4)] = w;
-            }
-            __syncthreads();
-            for (int j = a.first + tid; j < before; j += kThreads) {
-                const int entry = table[j];
-                if (entry < 0 || entry >= a.r.num_pages)
-                    continue;
-                const int64_t at = (int64_t)entry * a.kv_heads + h;
-                uint32_t key[D / 4];
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint4v w = *(const uint4v*)(a.keys + at * D + 16 * i);
-                    for (int k = 0; k < 4; ++k)
-                        key[4 * i + k] = w[k];
-                }
-                int best = INT32_MIN;
-                for (int r = 0; r < rows; ++r) {
-                    int sum = 0;
-                    for (int i = 0; i < D / 4; ++i)
-                        sum = __builtin_amdgcn_sdot4((int)key[i], (int)q8[r][i], sum, false);
-                    best = max(best, sum);
-                }
-                score[j] = max(score[j], ordered(ldexpf((float)best, a.exponents[at])));
-            }
-        }
-        __syncthreads();
+// What is chosen by score: scores above `limit` and the first `ties` that equal it.
+struct Limit {
+    float limit;
+    uint32_t ties;
+};
 
-        // The top_k-th largest score, a byte at a time: `above` have larger leading
-        // bytes than `prefix`, and the one wanted is the `want`-th of those that share it.
-        uint32_t prefix = 0, want = a.top;
-        bool all = a.top == 0;          // whether nothing (top 0) or everything is chosen
-        for (int shift = 24; shift >= 0 && !all; shift -= 8) {
-            count[tid] = 0;
-            __syncthreads();
-            for (int j = a.first + tid; j < before; j += kThreads) {
-                const uint32_t v = score[j];
-                if (v != 0 && (shift == 24 || v >> (shift + 8) == prefix >> (shift + 8)))
-                    atomicAdd(&count[v >> shift & 255], 1u);
-            }
-            __syncthreads();
-            // thread tid: how many have a byte above tid
-            const uint32_t mine = count[tid];
-            uint32_t sum = mine;
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t up = __shfl_down(sum, d);
-                if (lane + d < 64)
-                    sum += up;
-            }
-            if (lane == 0)
-                tops[wave] = sum;
-            if (tid == 0)
-                chosen[0] = 256;
-            __syncthreads();
-            for (int w = wave + 1; w < kThreads / 64; ++w)
-                sum += tops[w];
-            if (sum >= want && sum - mine < want) {
-                chosen[0] = tid;
-                chosen[1] = want - (sum - mine);
-            }
-            __syncthreads();
-            if (chosen[0] == 256) {
-                all = true;             // fewer than top_k (only in the first round)
-            } else {
-                prefix |= chosen[0] << shift;
-                want = chosen[1];
-            }
-            __syncthreads();
-        }
-        // chosen: scores above prefix, and the first `want` that equal it
-        const uint32_t limit = a.top == 0 ? ~0u : all ? 0 : prefix;
-        const uint32_t equals = a.top == 0 || all ? 0 : want;
-
-        // Each wave takes a run of the pages; first it counts, then it writes.
-        const int run = (own / (kThreads / 64) / 64 + 1) * 64;
-        const int from = wave * run, to = min(from + run, own + 1);
-        auto judge = [&](int j, bool& sure, bool& tie) {
-            const bool inside = j < to, scored = inside && j >= a.first && j < before;
-            const uint32_t v = scored ? score[j] : 0;
-            sure = inside && (scored ? v > limit : true);
-            tie = scored && v == limit && v != 0;
-        };
-        uint32_t n = 0, m = 0;
+// The pages in [from, to) by one wave: how many are listed for sure and how many
+// tie, or their numbers written to out from `at` on.
+struct Walk {
+    const float* score;
+    int first, before;       // pages in [first, before) are chosen by score
+    Limit l;
+    __device__ __forceinline__ void judge(int j, int to, bool& sure, bool& tie) const
+    {
+        const bool inside = j < to, scored = inside && j >= first && j < before;
+        const float v = scored ? score[j] : -INFINITY;
+        sure = inside && (scored ? v > l.limit : true);
+        tie = scored && v == l.limit && v != -INFINITY;
+    }
+    __device__ __forceinline__ void count(int from, int to, uint32_t& sure, uint32_t& tied) const
+    {
+        const int lane = threadIdx.x & 63;
         for (int j0 = from; j0 < to; j0 += 64) {
-            bool sure, tie;
-            judge(j0 + lane, sure, tie);
-            n += __popcll(__ballot(sure));
-            m += __popcll(__ballot(tie));
+            bool s, t;
+            judge(j0 + lane, to, s, t);
+            sure += __popcll(__ballot(s));
+            tied += __popcll(__ballot(t));
         }
-        if (lane == 0) {
-            taken[wave] = n;
-            ties[wave] = m;
-        }
-        __syncthreads();
-        uint32_t at = 0, seen = 0, total = 0, all_ties = 0;
-        for (int w = 0; w < kThreads / 64; ++w) {
-            if (w == wave) {
-                at = total;
-                seen = all_ties;
-            }
-            total += taken[w];
-            all_ties += ties[w];
-        }
-        at += min(seen, equals);
-        total += min(all_ties, equals);
+    }
+    __device__ __forceinline__ uint32_t write(int from, int to, uint32_t at, uint32_t seen, int32_t* out) const
+    {
+        const int lane = threadIdx.x & 63;
+        const uint64_t below = (1ull << lane) - 1;
         for (int j0 = from; j0 < to; j0 += 64) {
-            bool sure, tie;
-            judge(j0 + lane, sure, tie);
-            const uint64_t below = (1ull << lane) - 1;
-            const uint64_t tied = __ballot(tie);
-            const bool in = sure || (tie && seen + __popcll(tied & below) < equals);
+            bool s, t;
+            judge(j0 + lane, to, s, t);
+            const uint64_t tied = __ballot(t);
+            const bool in = s || (t && seen + __popcll(tied & below) < l.ties);
             const uint64_t listed = __ballot(in);
             if (in)
                 out[at + __popcll(listed & below)] = j0 + lane;
             at += __popcll(listed);
             seen += __popcll(tied);
         }
-        for (uint32_t i = total + tid; i < (uint32_t)width; i += kThreads)
-            out[i] = -1;
+        return at;
     }
+};
+
+// The top-th largest of score[first .. before) by one wave: bisection of the ordered
+// numbers, with the count of those above by ballots, until the count is right.
+__device__ __forceinline__ Limit wave_limit(const float* score, int first, int before, int top)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t lo = ~0u, hi = 0, n = 0;
+    const uint32_t none = ordered(-INFINITY);
+    for (int j0 = first; j0 < before; j0 += 64) {
+        const uint32_t v = j0 + lane < before ? ordered(score[j0 + lane]) : none;
+        n += __popcll(__ballot(v != none));
+        lo = min(lo, v == none ? ~0u : v);
+        hi = max(hi, v);
+    }
+    if (top == 0)
+        return {INFINITY, 0};
+    if ((int)n <= top)
+        return {-INFINITY, 0};
+    for (int d = 32; d; d >>= 1) {
+        lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
+        hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
+    }
+    // at least `top` are >= lo, fewer are > hi
+    uint32_t above = 0;         // how many are > hi
+    bool exact = false;         // exactly `top` are >= lo
+    while (lo < hi && !exact) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        uint32_t c = 0;
+        for (int j0 = first; j0 < before; j0 += 64)
+            c += __popcll(__ballot(j0 + lane < before && ordered(score[j0 + lane]) >= mid));
+        if ((int)c >= top) {
+            lo = mid;
+            exact = (int)c == top;
+        } else {
+            hi = mid - 1;
+            above = c;
+        }
+    }
+    const float limit = __uint_as_float(lo & 0x80000000u ? lo & 0x7fffffffu : ~lo);
+    return {limit, exact ? ~0u : top - above};
+}
+
+template <int W>
+struct SelectShared {
+    uint32_t bins[kBins];
+    float lo[W], hi[W];
+    uint32_t n[W], ties[W];
+    int chosen, want, exponent[16];
+};
+
+// The same by all waves: the scores between two bounds are counted in 256 equal
+// parts; the smallest and largest score of the part that holds the top-th are the
+// new bounds, until it holds one value or as many as are wanted. Every round leaves
+// at least a score out, as the bounds themselves fall into different parts.
+template <int W>
+__device__ __forceinline__ Limit group_limit(SelectShared<W>& lds, const float* score, int first, int before, int top)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (top == 0)
+        return {INFINITY, 0};
+    float lo = -3e38f, hi = INFINITY, base = 0, scale = 0;      // scores in [lo, hi], in part `chosen` of them
+    int chosen = 0;
+    uint32_t want = top;
+    // a larger score never goes to a lower part
+    auto part = [&](float v) { return min((int)((v - base) * scale), kBins - 1); };
+    for (bool all = true;; all = false) {
+        float low = INFINITY, high = -INFINITY;
+        uint32_t n = 0;
+        for (int j = first + tid; j < before; j += 64 * W) {
+            const float v = score[j];
+            if (v >= lo && v <= hi && part(v) == chosen) {
+                ++n;
+                low = fminf(low, v);
+                high = fmaxf(high, v);
+            }
+        }
+        for (int d = 32; d; d >>= 1) {
+            low = fminf(low, __shfl_xor(low, d));
+            high = fmaxf(high, __shfl_xor(high, d));
+            n += __shfl_xor(n, d);
+        }
+        if (lane == 0) {
+            lds.lo[wave] = low;
+            lds.hi[wave] = high;
+            lds.n[wave] = n;
+        }
+        for (int i = tid; i < kBins; i += 64 * W)
+            lds.bins[i] = 0;
+        __syncthreads();
+        n = 0;
+        for (int w = 0; w < W; ++w) {
+            low = fminf(low, lds.lo[w]);
+            high = fmaxf(high, lds.hi[w]);
+            n += lds.n[w];
+        }
+        if (n <= want)
+            return all ? Limit{-INFINITY, 0} : Limit{low, n};
+        lo = base = low;
+        hi = high;
+        if (lo == hi)
+            return {lo, want};
+        scale = (float)kBins / (hi - lo);
+        for (int j = first + tid; j < before; j += 64 * W) {
+            const float v = score[j];
+            if (v >= lo && v <= hi)
+                atomicAdd(&lds.bins[part(v)], 1u);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            uint32_t mine[4], sum = 0;
+            for (int i = 0; i < 4; ++i)
+                sum += mine[i] = lds.bins[4 * lane + i];
+            uint32_t up = sum;          // with those of the lanes above
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t v = __shfl_down(up, d);
+                up += lane + d < 64 ? v : 0;
+            }
+            uint32_t above = up - sum;
+            for (int i = 3; i >= 0; --i) {
+                if (above < want && above + mine[i] >= want) {
+                    lds.chosen = 4 * lane + i;
+                    lds.want = (int)(want - above);
+                }
+                above += mine[i];
+            }
+        }
+        __syncthreads();
+        chosen = lds.chosen;
+        want = lds.want;
+    }
+}
+
+// Sixteen pages for a wave: their keys as the left operand of the products (lane % 16
+// the page, 16 (lane / 16) + 64 k .. the dimensions), their exponents.
+template <int D>
+struct PageTile {
+    int4v key[D / 64];
+    int exponent;        // -1: not a page to be chosen
+};
+
+template <int D, int W>
+__global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
+{
+    constexpr int K = D / 64, kPitch = D + 16, kAhead = D > 128 ? 2 : 4;
+    extern __shared__ __align__(16) float score[];        // [tokens][pitch]; -inf: not to be chosen
+    __shared__ __align__(16) uint8_t q8[kMostRows][kPitch];
+    __shared__ SelectShared<W> lds;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = a.heads / a.kv_heads, listed = a.first + a.top + a.local;
+    int width = 1;                                        // columns of a token: a power of two
+    while (width < 16 && width < group)
+        width *= 2;
+    const int h = blockIdx.x % a.kv_heads;
+    int token = blockIdx.x / a.kv_heads * a.together;
+    const int token_end = min(token + a.together, a.tokens);
+
+    // the tokens of one request at a time
+    for (int run = 1; token < token_end; token += run) {
+        run = 1;
+        const int b = request_of(a.r, token);
+        if (b < 0)
+            continue;
+        const int behind = a.r.offsets[b + 1], len = length_of(a.r, b);
+        run = min(token_end, behind) - token;
+        const int pos0 = min(len - behind + token, len - 1), pos1 = min(pos0 + run, len) - 1;
+        const int32_t* table = a.r.table + b * a.r.ld_table;
+        // the pages that some token may choose by score
+        const int before = pos1 < 0 ? 0 : max(pos1 / a.r.page - a.local + 1, 0);
+
+        // Pages in tiles of 16, kAhead of a wave's in flight.
+        auto load = [&](PageTile<D>& t, int j0) {
+            const int j = j0 + n;
+            const int entry = j < before ? table[j] : -1;
+            const bool in = entry >= 0 && entry < a.r.num_pages;
+            const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
+            t.exponent = in ? min(max((int)a.exponents[at], 0), 64) : -1;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                t.key[k] = in ? *(const int4v*)(a.keys + at * D + 64 * k + 16 * g) : int4v{0, 0, 0, 0};
+        };
+        PageTile<D> tile[kAhead];
+        int j0 = a.first + 16 * wave;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (j0 + 16 * W * u < before)
+                load(tile[u], j0 + 16 * W * u);
+
+        // the tokens' common exponents
+        const uint16_t* q = a.q + token * a.ld_q + h * group * D;
+        for (int i = wave; i < run; i += W) {
+            uint32_t top = 0;
+            for (int x = lane; x < group * D / 8; x += 64) {
+                const uint4v w = *(const uint4v*)(q + i * a.ld_q + 8 * x);
+                for (int k = 0; k < 4; ++k)
+                    top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
+            }
+            for (int d = 32; d; d >>= 1)
+                top = max(top, (uint32_t)__shfl_xor((int)top, d));
+            if (lane == 0)
+                lds.exponent[i] = top == 0 || top >= 0x7f800000u ? 0 : ilogbf(__uint_as_float(top)) - 6;
+        }
+        __syncthreads();
+
+        // scores, of 64 query rows at a time: run * group rows, or the heads of a token
+        for (int h0 = 0; h0 < group; h0 += kMostRows) {
+            const int heads = min(group - h0, kMostRows), rows = run * heads;
+            if (h0)
+                __syncthreads();
+            for (int i = tid; i < rows * (D / 8); i += 64 * W) {
+                const int row = i / (D / 8), x = i % (D / 8) * 8, of = run == 1 ? 0 : row / group;
+                const uint4v w = *(const uint4v*)(q + of * a.ld_q + (h0 + row - of * group) * D + x);
+                const int e = -lds.exponent[of];
+                uint32_t v[2] = {0, 0};
+                for (int k = 0; k < 8; ++k) {
+                    const float y = ldexpf(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), e);
+                    v[k >> 2] |= (uint32_t)((int)rintf(fminf(fmaxf(y, -127.0f), 127.0f)) & 255) << (8 * (k & 3));
+                }
+                *(uint2*)&q8[row][x] = make_uint2(v[0], v[1]);
+            }
+            __syncthreads();
+            // column tiles: several tokens each, or several for a token
+            const int tokens = 16 / width, parts = (heads + 15) / 16;
+            auto compare = [&](const PageTile<D>& t, int j0) {
+                int e[4];
+                for (int i = 0; i < 4; ++i)
+                    e[i] = __builtin_amdgcn_ds_bpermute((4 * g + i) * 4, t.exponent);
+                for (int t0 = 0; t0 < run; t0 += tokens) {
+                    const int of = min(t0 + n / width, run - 1);
+                    int best[4] = {INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN};
+                    for (int p = 0; p < parts; ++p) {
+                        const int row = of * heads + min(16 * p + n % width, heads - 1);
+                        int4v sum = {0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.key[k], *(const int4v*)&q8[row][64 * k + 16 * g],
+                                                                        sum, 0, 0, 0);
+                        for (int i = 0; i < 4; ++i)
+                            best[i] = max(best[i], sum[i]);
+                    }
+                    for (int i = 0; i < 4; ++i)
+                        best[i] = max_of(best[i], width);
+                    if (n % width == 0 && t0 + n / width < run)
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = j0 + 4 * g + i;
+                            float* at = score + (t0 + n / width) * a.pitch + j;
+                            float v = e[i] < 0 ? -INFINITY : ldexpf((float)best[i], e[i]);
+                            if (j < before)
+                                *at = h0 ? fmaxf(*at, v) : v;
+                        }
+                }
+            };
+            if (h0) {
+                j0 = a.first + 16 * wave;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (j0 + 16 * W * u < before)
+                        load(tile[u], j0 + 16 * W * u);
+            }
+            while (j0 < before) {
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    if (j0 + 16 * W * u < before)
+                        compare(tile[u], j0 + 16 * W * u);
+                    if (j0 + 16 * W * (u + kAhead) < before)
+                        load(tile[u], j0 + 16 * W * (u + kAhead));
+                }
+                j0 += 16 * W * kAhead;
+            }
+        }
+        __syncthreads();
+
+        if (run == 1) {
+            int32_t* out = a.pages + ((int64_t)token * a.kv_heads + h) * listed;
+            const int pages = pos0 < 0 ? 0 : pos0 / a.r.page + 1;
+            Walk w = {score, a.first, before, group_limit<W>(lds, score, a.first, before, a.top)};
+            // each wave counts in a run of the pages, then writes
+            const int each = (pages + W * 64 - 1) / (W * 64) * 64, from = min(wave * each, pages), to = min(from + each, pages);
+            uint32_t sure = 0, tied = 0;
+            w.count(from, to, sure, tied);
+            __syncthreads();
+            if (lane == 0) {
+                lds.n[wave] = sure;
+                lds.ties[wave] = tied;
+            }
+            __syncthreads();
+            uint32_t at = 0, seen = 0, total = 0, all = 0;
+            for (int i = 0; i < W; ++i) {
+                at = i == wave ? total : at;
+                seen = i == wave ? all : seen;
+                total += lds.n[i];
+                all += lds.ties[i];
+            }
+            w.write(from, to, at + min(seen, w.l.ties), seen, out);
+            for (int i = (int)(total + min(all, w.l.ties)) + tid; i < listed; i += 64 * W)
+                out[i] = -1;
+        } else {
+            for (int i = wave; i < run; i += W) {
+                int32_t* out = a.pages + ((int64_t)(token + i) * a.kv_heads + h) * listed;
+                const int p = min(pos0 + i, len - 1), pages = p < 0 ? 0 : p / a.r.page + 1;
+                const int end = max(pages - a.local, 0);
+                const float* mine = score + i * a.pitch;
+                const Walk w = {mine, a.first, end, wave_limit(mine, a.first, end, a.top)};
+                const int total = (int)w.write(0, pages, 0, 0, out);
+                for (int x = total + lane; x < listed; x += 64)
+                    out[x] = -1;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int D>
+void launch_select(const Select& a, dim3 grid, unsigned lds, hipStream_t stream)
+{
+    // a grid holds less than 2^32 threads
+    if (a.together > 1 || a.r.max_pages <= 512 || grid.x > (1 << 20))
+        hipLaunchKernelGGL((select_pages_kernel<D, 4>), grid, dim3(256), lds, stream, a);
+    else
+        hipLaunchKernelGGL((select_pages_kernel<D, 16>), grid, dim3(1024), lds, stream, a);
 }
 
 bool requests_ok(int64_t num_slots, int32_t page_size, int64_t ld_table, int64_t max_pages, int64_t num_seqs)
@@ -380,7 +603,7 @@ extern "C" nvfp4_status_t nvfp4_select_pages(const uint16_t* q, int64_t tokens, 
         ld_q < 0 || !requests_ok(num_slots, page_size, ld_table, max_pages, num_seqs))
         return NVFP4_ERROR_INVALID_VALUE;
     if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || heads > 1024 || num_seqs > 65535 ||
-        num_slots > INT32_MAX || tokens > (1 << 30) / heads || max_pages > kMostPages ||
+        num_slots > INT32_MAX || tokens > (1 << 23) / heads || max_pages > kMostPages ||
         max_pages > (1 << 30) / page_size || top_k > kMostListed || first > kMostListed || local > kMostListed ||
         first + top_k + local > kMostListed)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
@@ -397,16 +620,21 @@ extern "C" nvfp4_status_t nvfp4_select_pages(const uint16_t* q, int64_t tokens, 
     Select a = {q, keys, exponents, pages,
                 {block_table, seq_lens, query_offsets, ld_table, (int)(num_slots / page_size), (int)max_pages,
                  page_size, (int)num_seqs},
-                ld_q, (int)tokens, heads, kv_heads, top_k, first, local};
-    // a grid holds less than 2^32 threads: beyond 2^22 workgroups each takes several tokens
-    const int64_t items = tokens * kv_heads;
-    const dim3 grid((unsigned)(items < (1 << 22) ? items : 1 << 22));
-    const unsigned lds = (unsigned)max_pages * 4;
+                ld_q, (int)tokens, heads, kv_heads, top_k, first, local, 1, ((int)max_pages + 3) & ~3};
+    // Tokens of long chunks go to a workgroup together, as many as 64 query rows and
+    // 64 KB of scores hold, at most 16.
+    const int group = heads / kv_heads;
+    while (a.together < 16 && a.together < tokens / num_seqs && (a.together + 1) * group <= kMostRows &&
+           (a.together + 1) * a.pitch * 4 <= 65536)
+        ++a.together;
+    const int64_t items = ceil_div(tokens, (int64_t)a.together) * kv_heads;
+    const dim3 grid((unsigned)items);
+    const unsigned lds = (unsigned)(a.together * a.pitch * 4);
     if (head_dim == 64)
-        hipLaunchKernelGGL((select_pages_kernel<64>), grid, dim3(kThreads), lds, stream, a);
+        launch_select<64>(a, grid, lds, stream);
     else if (head_dim == 128)
-        hipLaunchKernelGGL((select_pages_kernel<128>), grid, dim3(kThreads), lds, stream, a);
+        launch_select<128>(a, grid, lds, stream);
     else
-        hipLaunchKernelGGL((select_pages_kernel<256>), grid, dim3(kThreads), lds, stream, a);
+        launch_select<256>(a, grid, lds, stream);
     return launched();
 }

@@ -149,13 +149,26 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
     const int group = a.heads / a.kv_heads;
     const float k_scale = a.scale * (a.k_gs ? a.k_gs[0] : 1.0f) * kLog2e;
 
-    // As in the rows kernel: all key/value heads of a token go to one XCD
+    // Workgroups go to the 8 XCDs in turn. Tokens of many requests: all key/value
+    // heads of a token go to one XCD one after the other, as in the rows kernel.
+    // Tokens that share pages: an XCD takes a run of the tokens for one head after
+    // the other, so that its L2 holds little but what they share.
     const uint32_t groups = (uint32_t)(a.tokens + s.together - 1) / s.together;
     const uint32_t per_split = groups * a.row_blocks, works = per_split * a.splits;
-    const uint32_t j = blockIdx.x >> 3, work = j / a.kv_heads * 8 + (blockIdx.x & 7);
-    if (work >= works)
-        return;
-    const int h = (int)(j % a.kv_heads);
+    const uint32_t xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+    uint32_t work, h;
+    if (s.together > 1) {
+        const uint32_t run = (works * a.kv_heads + 7) / 8, at = xcd * run + j;
+        h = at / works;
+        work = at % works;
+        if (j >= run || h >= (uint32_t)a.kv_heads)
+            return;
+    } else {
+        work = j / a.kv_heads * 8 + xcd;
+        h = j % a.kv_heads;
+        if (work >= works)
+            return;
+    }
     const int split = (int)(work / per_split);
     const uint32_t item = work % per_split;
     const int row0 = (int)(item % a.row_blocks) * 16 * RT;

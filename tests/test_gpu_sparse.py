@@ -275,9 +275,34 @@ def test_select(M, heads, kv, dim, page):
         check_select(M, c, top, first, local)
 
 
+@pytest.mark.parametrize("heads,kv,dim,page", [(8, 2, 128, 16), (3, 3, 64, 4), (12, 1, 256, 8), (14, 2, 64, 1), (40, 1, 128, 2),
+                                               (20, 4, 256, 3), (64, 1, 64, 5), (200, 1, 128, 4)])
+def test_select_tokens_of_a_chunk(M, heads, kv, dim, page):
+    """Chunks of tokens, which a workgroup takes some of at a time; requests that end
+    inside them."""
+    totals, news = [200 * page, 9 * page + 3, 5, 70 * page + 1], [37, 6, 5, 21]
+    c = request_case(heads + dim, kv, dim, page, totals, news, heads=heads, pad=3)
+    for top, first, local in ((4, 1, 2), (0, 0, 1), (30, 2, 3), (300, 0, 1)):
+        say("select chunk", heads, kv, dim, page, top, first, local)
+        check_select(M, c, top, first, local)
+
+
+@pytest.mark.parametrize("news", [1, 9])
+@pytest.mark.parametrize("octaves", [0, 30, 64])
+def test_select_scores_of_any_spread(M, news, octaves):
+    """Exponents up to the largest, one score far above the others, long lists."""
+    c = request_case(11, 2, 64, 2, [1400, 900], [news, news], heads=4)
+    c["exponents"] = torch.randint(0, octaves + 1, c["exponents"].shape, dtype=torch.int8, generator=torch.Generator().manual_seed(1))
+    c["keys"][5:9], c["exponents"][5:9] = 127, 64
+    for top in (1, 7, 120, 600):
+        say("select spread", news, octaves, top)
+        check_select(M, c, top, 1, 2)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [2, 1], [9, 11]])
 @pytest.mark.parametrize("spread", ["one value", "few values", "zero queries"])
-def test_select_ties_go_to_the_lower_page(M, spread):
-    c = request_case(7, 2, 64, 4, [1200, 900], [2, 1], heads=4)
+def test_select_ties_go_to_the_lower_page(M, spread, news):
+    c = request_case(7, 2, 64, 4, [1200, 900], news, heads=4)
     g = torch.Generator().manual_seed(1)
     if spread == "one value":
         c["keys"][:], c["exponents"][:] = 3, 1
