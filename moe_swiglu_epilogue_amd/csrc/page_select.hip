@@ -131,7 +131,6 @@ struct Select {
 };
 
 constexpr int kMostRows = 64;      // query rows that are compared at once
-constexpr int kBins = 256;
 
 typedef int int4v __attribute__((ext_vector_type(4)));
 
@@ -154,24 +153,28 @@ __device__ __forceinline__ uint32_t ordered(float v)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ float number(uint32_t v)
+{
+    return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
+}
+
 template <int kCtrl>
 __device__ __forceinline__ int other_lane(int v)
 {
     return __builtin_amdgcn_mov_dpp(v, kCtrl, 0xf, 0xf, true);
 }
 
-// Largest of `width` neighbouring lanes (1, 2, 4, 8 or 16), in all of them.
-__device__ __forceinline__ int max_of(int v, int width)
+// Largest of 2^bits neighbouring lanes, at most 16, in all of them.
+__device__ __forceinline__ int max_of(int v, int bits)
 {
-    if (width > 1)
-        v = max(v, other_lane<0xb1>(v));        // lane ^ 1
-    if (width > 2)
-        v = max(v, other_lane<0x4e>(v));        // lane ^ 2
-    if (width > 4)
-        v = max(v, other_lane<0x141>(v));       // 7 - lane of eight
-    if (width > 8)
-        v = max(v, other_lane<0x140>(v));       // 15 - lane of sixteen
-    return v;
+    const int two = max(v, other_lane<0xb1>(v));            // lane ^ 1
+    v = bits > 0 ? two : v;
+    const int four = max(v, other_lane<0x4e>(v));           // lane ^ 2
+    v = bits > 1 ? four : v;
+    const int eight = max(v, other_lane<0x141>(v));         // 7 - lane of eight
+    v = bits > 2 ? eight : v;
+    const int sixteen = max(v, other_lane<0x140>(v));       // 15 - lane of sixteen
+    return bits > 3 ? sixteen : v;
 }
 
 // What is chosen by score: scores above `limit` and the first `ties` that equal it.
@@ -180,176 +183,93 @@ struct Limit {
     uint32_t ties;
 };
 
-// The pages in [from, to) by one wave: how many are listed for sure and how many
-// tie, or their numbers written to out from `at` on.
-struct Walk {
-    const float* score;
-    int first, before;       // pages in [first, before) are chosen by score
-    Limit l;
-    __device__ __forceinline__ void judge(int j, int to, bool& sure, bool& tie) const
-    {
-        const bool inside = j < to, scored = inside && j >= first && j < before;
-        const float v = scored ? score[j] : -INFINITY;
-        sure = inside && (scored ? v > l.limit : true);
-        tie = scored && v == l.limit && v != -INFINITY;
-    }
-    __device__ __forceinline__ void count(int from, int to, uint32_t& sure, uint32_t& tied) const
-    {
-        const int lane = threadIdx.x & 63;
-        for (int j0 = from; j0 < to; j0 += 64) {
-            bool s, t;
-            judge(j0 + lane, to, s, t);
-            sure += __popcll(__ballot(s));
-            tied += __popcll(__ballot(t));
-        }
-    }
-    __device__ __forceinline__ uint32_t write(int from, int to, uint32_t at, uint32_t seen, int32_t* out) const
-    {
-        const int lane = threadIdx.x & 63;
-        const uint64_t below = (1ull << lane) - 1;
-        for (int j0 = from; j0 < to; j0 += 64) {
-            bool s, t;
-            judge(j0 + lane, to, s, t);
-            const uint64_t tied = __ballot(t);
-            const bool in = s || (t && seen + __popcll(tied & below) < l.ties);
-            const uint64_t listed = __ballot(in);
-            if (in)
-                out[at + __popcll(listed & below)] = j0 + lane;
-            at += __popcll(listed);
-            seen += __popcll(tied);
-        }
-        return at;
-    }
-};
-
-// The top-th largest of score[first .. before) by one wave: bisection of the ordered
-// numbers, with the count of those above by ballots, until the count is right.
-__device__ __forceinline__ Limit wave_limit(const float* score, int first, int before, int top)
-{
-    const int lane = threadIdx.x & 63;
-    uint32_t lo = ~0u, hi = 0, n = 0;
-    const uint32_t none = ordered(-INFINITY);
-    for (int j0 = first; j0 < before; j0 += 64) {
-        const uint32_t v = j0 + lane < before ? ordered(score[j0 + lane]) : none;
-        n += __popcll(__ballot(v != none));
-        lo = min(lo, v == none ? ~0u : v);
-        hi = max(hi, v);
-    }
-    if (top == 0)
-        return {INFINITY, 0};
-    if ((int)n <= top)
-        return {-INFINITY, 0};
-    for (int d = 32; d; d >>= 1) {
-        lo = min(lo, (uint32_t)__shfl_xor((int)lo, d));
-        hi = max(hi, (uint32_t)__shfl_xor((int)hi, d));
-    }
-    // at least `top` are >= lo, fewer are > hi
-    uint32_t above = 0;         // how many are > hi
-    bool exact = false;         // exactly `top` are >= lo
-    while (lo < hi && !exact) {
-        const uint32_t mid = lo + (hi - lo + 1) / 2;
-        uint32_t c = 0;
-        for (int j0 = first; j0 < before; j0 += 64)
-            c += __popcll(__ballot(j0 + lane < before && ordered(score[j0 + lane]) >= mid));
-        if ((int)c >= top) {
-            lo = mid;
-            exact = (int)c == top;
-        } else {
-            hi = mid - 1;
-            above = c;
-        }
-    }
-    const float limit = __uint_as_float(lo & 0x80000000u ? lo & 0x7fffffffu : ~lo);
-    return {limit, exact ? ~0u : top - above};
-}
-
 template <int W>
 struct SelectShared {
-    uint32_t bins[kBins];
-    float lo[W], hi[W];
-    uint32_t n[W], ties[W];
-    int chosen, want, exponent[16];
+    float lo, hi;                      // of all waves' scores, as ordered numbers
+    uint32_t n[3], sure[W], ties[W];
 };
 
-// The same by all waves: the scores between two bounds are counted in 256 equal
-// parts; the smallest and largest score of the part that holds the top-th are the
-// new bounds, until it holds one value or as many as are wanted. Every round leaves
-// at least a score out, as the bounds themselves fall into different parts.
-template <int W>
-__device__ __forceinline__ Limit group_limit(SelectShared<W>& lds, const float* score, int first, int before, int top)
+// The top-th largest of score[first .. before): bisection of the values between the
+// smallest and the largest, counting by ballots those not below the middle, until
+// the count is right or one value is left. By one wave (W = 1) or by all of a
+// workgroup's, which add their counts up in LDS. The first 8 scores of a lane stay
+// in registers, which is all up to 512 pages a wave.
+template <int W, class Shared>
+__device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int first, int before, int top)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (top == 0)
+    constexpr int kHeld = 8;
+    const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6;
+    if (top == 0 || before <= first)
         return {INFINITY, 0};
-    float lo = -3e38f, hi = INFINITY, base = 0, scale = 0;      // scores in [lo, hi], in part `chosen` of them
-    int chosen = 0;
-    uint32_t want = top;
-    // a larger score never goes to a lower part
-    auto part = [&](float v) { return min((int)((v - base) * scale), kBins - 1); };
-    for (bool all = true;; all = false) {
-        float low = INFINITY, high = -INFINITY;
-        uint32_t n = 0;
-        for (int j = first + tid; j < before; j += 64 * W) {
-            const float v = score[j];
-            if (v >= lo && v <= hi && part(v) == chosen) {
-                ++n;
-                low = fminf(low, v);
-                high = fmaxf(high, v);
-            }
-        }
-        for (int d = 32; d; d >>= 1) {
-            low = fminf(low, __shfl_xor(low, d));
-            high = fmaxf(high, __shfl_xor(high, d));
-            n += __shfl_xor(n, d);
-        }
+    const int from = first + 64 * wave + lane;
+    const int rest = first + 64 * W * kHeld;           // pages from here on are read again each time
+    float held[kHeld], lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int j = from + 64 * W * i;
+        held[i] = j < before ? score[j] : -INFINITY;
+        lo = held[i] == -INFINITY ? lo : fminf(lo, held[i]);
+        hi = fmaxf(hi, held[i]);
+    }
+#pragma unroll 1
+    for (int j = rest + 64 * wave + lane; j < before; j += 64 * W) {
+        const float v = score[j];
+        lo = v == -INFINITY ? lo : fminf(lo, v);
+        hi = fmaxf(hi, v);
+    }
+#pragma unroll 1
+    for (int d = 32; d; d >>= 1) {
+        lo = fminf(lo, __shfl_xor(lo, d));
+        hi = fmaxf(hi, __shfl_xor(hi, d));
+    }
+    if (W > 1) {
         if (lane == 0) {
-            lds.lo[wave] = low;
-            lds.hi[wave] = high;
-            lds.n[wave] = n;
-        }
-        for (int i = tid; i < kBins; i += 64 * W)
-            lds.bins[i] = 0;
-        __syncthreads();
-        n = 0;
-        for (int w = 0; w < W; ++w) {
-            low = fminf(low, lds.lo[w]);
-            high = fmaxf(high, lds.hi[w]);
-            n += lds.n[w];
-        }
-        if (n <= want)
-            return all ? Limit{-INFINITY, 0} : Limit{low, n};
-        lo = base = low;
-        hi = high;
-        if (lo == hi)
-            return {lo, want};
-        scale = (float)kBins / (hi - lo);
-        for (int j = first + tid; j < before; j += 64 * W) {
-            const float v = score[j];
-            if (v >= lo && v <= hi)
-                atomicAdd(&lds.bins[part(v)], 1u);
+            atomicMin((int*)&lds.lo, (int)(ordered(lo) ^ 0x80000000u));
+            atomicMax((int*)&lds.hi, (int)(ordered(hi) ^ 0x80000000u));
         }
         __syncthreads();
-        if (wave == 0) {
-            uint32_t mine[4], sum = 0;
-            for (int i = 0; i < 4; ++i)
-                sum += mine[i] = lds.bins[4 * lane + i];
-            uint32_t up = sum;          // with those of the lanes above
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t v = __shfl_down(up, d);
-                up += lane + d < 64 ? v : 0;
-            }
-            uint32_t above = up - sum;
-            for (int i = 3; i >= 0; --i) {
-                if (above < want && above + mine[i] >= want) {
-                    lds.chosen = 4 * lane + i;
-                    lds.want = (int)(want - above);
-                }
-                above += mine[i];
-            }
+        lo = number(__float_as_uint(lds.lo) ^ 0x80000000u);
+        hi = number(__float_as_uint(lds.hi) ^ 0x80000000u);
+    }
+    if (lo > hi)
+        return {INFINITY, 0};
+    // the top-th largest is in [lo, hi]; `above` are larger than hi
+    int above = 0, turn = 0;
+    float mid = lo;
+    for (;;) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            c += __popcll(__ballot(held[i] >= mid));
+#pragma unroll 1
+        for (int j0 = rest + 64 * wave; j0 < before; j0 += 64 * W)
+            c += __popcll(__ballot(j0 + lane < before && score[j0 + lane] >= mid));
+        if (W > 1) {
+            // the next turn's sum is cleared in front of this turn's barrier; it was last
+            // read in front of the barrier before
+            if (lane == 0)
+                atomicAdd(&lds.n[turn], (uint32_t)c);
+            const int next = turn == 2 ? 0 : turn + 1;
+            if (threadIdx.x == 0)
+                lds.n[next] = 0;
+            __syncthreads();
+            c = lds.n[turn];
+            turn = next;
         }
-        __syncthreads();
-        chosen = lds.chosen;
-        want = lds.want;
+        if (c >= top) {
+            lo = mid;
+            if (c == top)
+                return {lo, ~0u};
+        } else {
+            if (mid == lo)                  // all of them, and fewer than top
+                return {-INFINITY, 0};
+            above = c;
+            hi = number(ordered(mid) - 1);  // the next smaller number: not below lo
+        }
+        if (lo >= hi)
+            return {lo, (uint32_t)(top - above)};
+        mid = lo + 0.5f * (hi - lo);
+        mid = mid > lo ? mid : hi;
     }
 }
 
@@ -364,16 +284,16 @@ struct PageTile {
 template <int D, int W>
 __global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
 {
-    constexpr int K = D / 64, kPitch = D + 16, kAhead = D > 128 ? 2 : 4;
+    constexpr int K = D / 64, kPitch = D + 16;
     extern __shared__ __align__(16) float score[];        // [tokens][pitch]; -inf: not to be chosen
     __shared__ __align__(16) uint8_t q8[kMostRows][kPitch];
     __shared__ SelectShared<W> lds;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = a.heads / a.kv_heads, listed = a.first + a.top + a.local;
-    int width = 1;                                        // columns of a token: a power of two
-    while (width < 16 && width < group)
-        width *= 2;
+    int bits = 0;                                         // 2^bits columns for a token, at most 16
+    while (bits < 4 && 1 << bits < group)
+        ++bits;
     const int h = blockIdx.x % a.kv_heads;
     int token = blockIdx.x / a.kv_heads * a.together;
     const int token_end = min(token + a.together, a.tokens);
@@ -388,148 +308,165 @@ __global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
         run = min(token_end, behind) - token;
         const int pos0 = min(len - behind + token, len - 1), pos1 = min(pos0 + run, len) - 1;
         const int32_t* table = a.r.table + b * a.r.ld_table;
+        const uint16_t* q = a.q + token * a.ld_q + h * group * D;
         // the pages that some token may choose by score
         const int before = pos1 < 0 ? 0 : max(pos1 / a.r.page - a.local + 1, 0);
-
-        // Pages in tiles of 16, kAhead of a wave's in flight.
-        auto load = [&](PageTile<D>& t, int j0) {
-            const int j = j0 + n;
-            const int entry = j < before ? table[j] : -1;
-            const bool in = entry >= 0 && entry < a.r.num_pages;
-            const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
-            t.exponent = in ? min(max((int)a.exponents[at], 0), 64) : -1;
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                t.key[k] = in ? *(const int4v*)(a.keys + at * D + 64 * k + 16 * g) : int4v{0, 0, 0, 0};
-        };
-        PageTile<D> tile[kAhead];
-        int j0 = a.first + 16 * wave;
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (j0 + 16 * W * u < before)
-                load(tile[u], j0 + 16 * W * u);
-
-        // the tokens' common exponents
-        const uint16_t* q = a.q + token * a.ld_q + h * group * D;
-        for (int i = wave; i < run; i += W) {
-            uint32_t top = 0;
-            for (int x = lane; x < group * D / 8; x += 64) {
-                const uint4v w = *(const uint4v*)(q + i * a.ld_q + 8 * x);
-                for (int k = 0; k < 4; ++k)
-                    top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
-            }
-            for (int d = 32; d; d >>= 1)
-                top = max(top, (uint32_t)__shfl_xor((int)top, d));
-            if (lane == 0)
-                lds.exponent[i] = top == 0 || top >= 0x7f800000u ? 0 : ilogbf(__uint_as_float(top)) - 6;
+        __syncthreads();                                  // the LDS of what came before is read
+        if (tid == 0) {
+            lds.lo = __int_as_float(INT32_MAX);
+            lds.hi = __int_as_float(INT32_MIN);
+            lds.n[0] = 0;
         }
-        __syncthreads();
 
         // scores, of 64 query rows at a time: run * group rows, or the heads of a token
+#pragma unroll 1
         for (int h0 = 0; h0 < group; h0 += kMostRows) {
-            const int heads = min(group - h0, kMostRows), rows = run * heads;
+            const int heads = min(group - h0, kMostRows);
             if (h0)
                 __syncthreads();
-            for (int i = tid; i < rows * (D / 8); i += 64 * W) {
-                const int row = i / (D / 8), x = i % (D / 8) * 8, of = run == 1 ? 0 : row / group;
-                const uint4v w = *(const uint4v*)(q + of * a.ld_q + (h0 + row - of * group) * D + x);
-                const int e = -lds.exponent[of];
-                uint32_t v[2] = {0, 0};
-                for (int k = 0; k < 8; ++k) {
-                    const float y = ldexpf(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), e);
-                    v[k >> 2] |= (uint32_t)((int)rintf(fminf(fmaxf(y, -127.0f), 127.0f)) & 255) << (8 * (k & 3));
+            else
+                // places in the cache, -1 where hidden, wait in LDS where the scores go
+#pragma unroll 1
+                for (int j = a.first + tid; j < before; j += 64 * W) {
+                    const int entry = table[j];
+                    score[j] = __int_as_float(entry >= 0 && entry < a.r.num_pages ? entry : -1);
                 }
-                *(uint2*)&q8[row][x] = make_uint2(v[0], v[1]);
+            // queries in 8 bits, a token a wave or a single token by all waves
+#pragma unroll 1
+            for (int i = run == 1 ? 0 : wave; i < run; i += W) {
+                const uint16_t* qi = q + i * a.ld_q;
+                uint32_t top = 0;
+#pragma unroll 1
+                for (int x = lane; x < group * D / 8; x += 64) {
+                    const uint4v w = *(const uint4v*)(qi + 8 * x);
+                    for (int k = 0; k < 4; ++k)
+                        top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
+                }
+#pragma unroll 1
+                for (int d = 32; d; d >>= 1)
+                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
+                const int e = top == 0 || top >= 0x7f800000u ? 0 : 6 - ilogbf(__uint_as_float(top));
+#pragma unroll 1
+                for (int x = (run == 1 ? 64 * wave : 0) + lane; x < heads * D / 8; x += run == 1 ? 64 * W : 64) {
+                    const uint4v w = *(const uint4v*)(qi + h0 * D + 8 * x);
+                    uint32_t v[2] = {0, 0};
+                    for (int k = 0; k < 8; ++k) {
+                        const float y = ldexpf(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), e);
+                        v[k >> 2] |= (uint32_t)((int)rintf(__builtin_amdgcn_fmed3f(y, -127.0f, 127.0f)) & 255) << (8 * (k & 3));
+                    }
+                    *(uint2*)&q8[i * heads + x / (D / 8)][x % (D / 8) * 8] = make_uint2(v[0], v[1]);
+                }
             }
             __syncthreads();
+
+            auto load = [&](PageTile<D>& t, int j0) {
+                const int j = j0 + n;
+                int entry = -1;
+                if (j < before)
+                    entry = h0 ? table[j] : __float_as_int(score[j]);
+                const bool in = entry >= 0 && entry < a.r.num_pages;
+                const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
+                t.exponent = -1;
+                if (in) {
+                    t.exponent = min(max((int)a.exponents[at], 0), 64);
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        t.key[k] = *(const int4v*)(a.keys + at * D + 64 * k + 16 * g);
+                }
+            };
             // column tiles: several tokens each, or several for a token
-            const int tokens = 16 / width, parts = (heads + 15) / 16;
+            const int parts = (heads + 15) / 16;
             auto compare = [&](const PageTile<D>& t, int j0) {
                 int e[4];
                 for (int i = 0; i < 4; ++i)
                     e[i] = __builtin_amdgcn_ds_bpermute((4 * g + i) * 4, t.exponent);
-                for (int t0 = 0; t0 < run; t0 += tokens) {
-                    const int of = min(t0 + n / width, run - 1);
+#pragma unroll 1
+                for (int t0 = 0; t0 < run; t0 += 16 >> bits) {
+                    const int of = t0 + (n >> bits), row0 = min(of, run - 1) * heads, col = n & ((1 << bits) - 1);
                     int best[4] = {INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN};
+#pragma unroll 1
                     for (int p = 0; p < parts; ++p) {
-                        const int row = of * heads + min(16 * p + n % width, heads - 1);
+                        const uint8_t* row = q8[row0 + min(16 * p + col, heads - 1)] + 16 * g;
                         int4v sum = {0, 0, 0, 0};
 #pragma unroll
                         for (int k = 0; k < K; ++k)
-                            sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.key[k], *(const int4v*)&q8[row][64 * k + 16 * g],
-                                                                        sum, 0, 0, 0);
+                            sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.key[k], *(const int4v*)(row + 64 * k), sum, 0, 0, 0);
                         for (int i = 0; i < 4; ++i)
                             best[i] = max(best[i], sum[i]);
                     }
                     for (int i = 0; i < 4; ++i)
-                        best[i] = max_of(best[i], width);
-                    if (n % width == 0 && t0 + n / width < run)
+                        best[i] = max_of(best[i], bits);
+                    if (col == 0 && of < run) {
+                        float* at = score + of * a.pitch + j0 + 4 * g;
                         for (int i = 0; i < 4; ++i) {
-                            const int j = j0 + 4 * g + i;
-                            float* at = score + (t0 + n / width) * a.pitch + j;
-                            float v = e[i] < 0 ? -INFINITY : ldexpf((float)best[i], e[i]);
-                            if (j < before)
-                                *at = h0 ? fmaxf(*at, v) : v;
+                            const float v = e[i] < 0 ? -INFINITY : ldexpf((float)best[i], e[i]);
+                            if (j0 + 4 * g + i < before)
+                                at[i] = h0 ? fmaxf(at[i], v) : v;
                         }
+                    }
                 }
             };
-            if (h0) {
-                j0 = a.first + 16 * wave;
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u)
-                    if (j0 + 16 * W * u < before)
-                        load(tile[u], j0 + 16 * W * u);
-            }
-            while (j0 < before) {
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    if (j0 + 16 * W * u < before)
-                        compare(tile[u], j0 + 16 * W * u);
-                    if (j0 + 16 * W * (u + kAhead) < before)
-                        load(tile[u], j0 + 16 * W * (u + kAhead));
-                }
-                j0 += 16 * W * kAhead;
+            PageTile<D> next;
+            load(next, a.first + 16 * wave);
+#pragma unroll 1
+            for (int j0 = a.first + 16 * wave; j0 < before; j0 += 16 * W) {
+                const PageTile<D> tile = next;
+                load(next, j0 + 16 * W);
+                compare(tile, j0);
             }
         }
         __syncthreads();
 
-        if (run == 1) {
-            int32_t* out = a.pages + ((int64_t)token * a.kv_heads + h) * listed;
-            const int pages = pos0 < 0 ? 0 : pos0 / a.r.page + 1;
-            Walk w = {score, a.first, before, group_limit<W>(lds, score, a.first, before, a.top)};
-            // each wave counts in a run of the pages, then writes
-            const int each = (pages + W * 64 - 1) / (W * 64) * 64, from = min(wave * each, pages), to = min(from + each, pages);
-            uint32_t sure = 0, tied = 0;
-            w.count(from, to, sure, tied);
-            __syncthreads();
-            if (lane == 0) {
-                lds.n[wave] = sure;
-                lds.ties[wave] = tied;
-            }
-            __syncthreads();
-            uint32_t at = 0, seen = 0, total = 0, all = 0;
-            for (int i = 0; i < W; ++i) {
-                at = i == wave ? total : at;
-                seen = i == wave ? all : seen;
-                total += lds.n[i];
-                all += lds.ties[i];
-            }
-            w.write(from, to, at + min(seen, w.l.ties), seen, out);
-            for (int i = (int)(total + min(all, w.l.ties)) + tid; i < listed; i += 64 * W)
-                out[i] = -1;
-        } else {
-            for (int i = wave; i < run; i += W) {
-                int32_t* out = a.pages + ((int64_t)(token + i) * a.kv_heads + h) * listed;
-                const int p = min(pos0 + i, len - 1), pages = p < 0 ? 0 : p / a.r.page + 1;
-                const int end = max(pages - a.local, 0);
-                const float* mine = score + i * a.pitch;
-                const Walk w = {mine, a.first, end, wave_limit(mine, a.first, end, a.top)};
-                const int total = (int)w.write(0, pages, 0, 0, out);
-                for (int x = total + lane; x < listed; x += 64)
-                    out[x] = -1;
+        // The listed pages in order: a wave takes a token, or a run of a single token's
+        // pages, which it counts first and then writes.
+        const int shares = run == 1 ? W : 1;
+#pragma unroll 1
+        for (int i = run == 1 ? 0 : wave; i < run; i += W) {
+            const float* mine = score + i * a.pitch;
+            int32_t* out = a.pages + ((int64_t)(token + i) * a.kv_heads + h) * listed;
+            const int p = min(pos0 + i, len - 1), pages = p < 0 ? 0 : p / a.r.page + 1, end = max(pages - a.local, 0);
+            const Limit l = run == 1 ? find_limit<W>(lds, mine, a.first, end, a.top) : find_limit<1>(lds, mine, a.first, end, a.top);
+            const int each = (pages + shares * 64 - 1) / (shares * 64) * 64;
+            const int from = run == 1 ? min(wave * each, pages) : 0, to = min(from + each, pages);
+            uint32_t at = 0, seen = 0;
+#pragma unroll 1
+            for (int pass = shares == 1; pass < 2; ++pass) {
+                uint32_t sure = 0, tied = seen;
+                const uint64_t below = (1ull << lane) - 1;
+#pragma unroll 1
+                for (int j0 = from; j0 < to; j0 += 64) {
+                    const int j = j0 + lane;
+                    const bool scored = j >= a.first && j < end;
+                    const float v = scored ? mine[j] : 0.0f;
+                    const bool tie = scored && v == l.limit && j < to && v != -INFINITY;
+                    const uint64_t equal = __ballot(tie);
+                    const bool in = j < to && (scored ? v > l.limit || (pass && tie && tied + __popcll(equal & below) < l.ties) : true);
+                    const uint64_t taken = __ballot(in);
+                    if (pass && in)
+                        out[at + sure + __popcll(taken & below)] = j;
+                    sure += __popcll(taken);
+                    tied += __popcll(equal);
+                }
+                if (pass == 0) {
+                    if (lane == 0) {
+                        lds.sure[wave] = sure;
+                        lds.ties[wave] = tied;
+                    }
+                    __syncthreads();
+#pragma unroll 1
+                    for (int w = 0; w < wave; ++w) {
+                        at += lds.sure[w];
+                        seen += lds.ties[w];
+                    }
+                    at += min(seen, l.ties);
+                } else if (to == pages && (from < to || run > 1 || wave == 0)) {
+                    // the last pages' wave fills the rest of the list
+#pragma unroll 1
+                    for (int x = (int)(at + sure) + lane; x < listed; x += 64)
+                        out[x] = -1;
+                }
             }
         }
-        __syncthreads();
     }
 }
 
