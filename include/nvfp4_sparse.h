@@ -119,7 +119,9 @@ nvfp4_status_t nvfp4_page_keys(const uint8_t *k_packed, const uint8_t *k_scales,
  * kv_heads, at most 1024; top_k, first >= 0, local >= 1, first + top_k + local <=
  * 2048; max_pages <= 32768 and max_pages * page_size <= 2^30; num_seqs <= 65535,
  * num_slots < 2^31, tokens * heads <= 2^23; exponents are taken to be 0 to 64; ld_q a
- * multiple of 8; q and keys 16-byte aligned. One kernel.
+ * multiple of 8; q and keys 16-byte aligned. workspace:
+ * nvfp4_select_pages_workspace(...) bytes (may be 0, then workspace may be NULL),
+ * 16-byte aligned. One kernel, or two for few tokens.
  */
 nvfp4_status_t nvfp4_select_pages(const uint16_t *q, int64_t tokens, int64_t ld_q, int32_t heads,
                                   int32_t kv_heads, int32_t head_dim, const int8_t *keys,
@@ -127,8 +129,13 @@ nvfp4_status_t nvfp4_select_pages(const uint16_t *q, int64_t tokens, int64_t ld_
                                   const int32_t *block_table, int64_t ld_table,
                                   int64_t max_pages, const int32_t *seq_lens,
                                   const int32_t *query_offsets, int64_t num_seqs, int32_t top_k,
-                                  int32_t first, int32_t local, int32_t *pages,
-                                  hipStream_t stream);
+                                  int32_t first, int32_t local, int32_t *pages, void *workspace,
+                                  int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that nvfp4_select_pages needs for these sizes (the same
+ * arguments as the call's), or -1 where the call refuses them. Needs no GPU. */
+int64_t nvfp4_select_pages_workspace(int64_t tokens, int32_t heads, int32_t kv_heads,
+                                     int64_t num_seqs, int64_t max_pages);
 
 /*
  * Attention of each token over the tokens of its listed pages, as

@@ -113,21 +113,28 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 }
 
 // ---- selection -----------------------------------------------------------------
-// A workgroup takes a token, or some that follow each other in one request, and a
-// key/value head. Scores are products of whole numbers on the matrix cores
-// (v_mfma_i32_16x16x64_i8): a page a row, a query row a column, so the largest of a
-// token's rows is found within 16 lanes. They go to LDS as FP32, exactly. Then the
-// top_k-th largest is searched, by all waves for a single token and by a wave each
-// for several, and the listed pages are written in order.
+// Scores are products of whole numbers on the matrix cores
+// (v_mfma_i32_16x16x64_i8): a query row a row, a page a column, so a lane holds four
+// rows of one page, and the largest of a token's rows is found in its registers
+// and, from 8 rows on, by one or two exchanges. As FP32 they are exact. Then the
+// top_k-th largest is searched and the listed pages are written in order.
+//   Many tokens: a workgroup takes some that follow each other in one request and a
+// key/value head, keeps their scores in LDS, and a wave each selects; a single
+// token's is selected by all waves (select_chunk_kernel).
+//   Few tokens: a compute unit alone reads keys at some 25 GB/s, so their pages go to a
+// workgroup for each 256 (score_pages_kernel), and by way of the workspace to a
+// workgroup for each list (list_pages_kernel).
 struct Select {
     const uint16_t* q;
     const int8_t *keys, *exponents;
     int32_t* pages;
+    float* scores;     // workspace
     Requests r;
     int64_t ld_q;
     int tokens, heads, kv_heads, top, first, local;
     int together;      // tokens that a workgroup takes
-    int pitch;         // scores of a token in LDS
+    int pitch;         // scores of a token
+    int chunks;        // workgroups over a token's pages
 };
 
 constexpr int kMostRows = 64;      // query rows that are compared at once
@@ -158,23 +165,34 @@ __device__ __forceinline__ float number(uint32_t v)
     return __uint_as_float(v & 0x80000000u ? v & 0x7fffffffu : ~v);
 }
 
-template <int kCtrl>
-__device__ __forceinline__ int other_lane(int v)
+// op over the lanes up to each; `none` is what op leaves alone. Row shifts and
+// broadcasts: an exchange through LDS takes some ten times as long.
+template <class Op>
+__device__ __forceinline__ uint32_t up_to_lane(uint32_t v, uint32_t none, Op op)
 {
-    return __builtin_amdgcn_mov_dpp(v, kCtrl, 0xf, 0xf, true);
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x111, 0xf, 0xf, false));    // row_shr:1
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x112, 0xf, 0xf, false));
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x114, 0xf, 0xf, false));
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x118, 0xf, 0xf, false));
+    v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x142, 0xa, 0xf, false));    // row_bcast:15
+    return op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, 0x143, 0xc, 0xf, false)); // row_bcast:31
 }
 
-// Largest of 2^bits neighbouring lanes, at most 16, in all of them.
-__device__ __forceinline__ int max_of(int v, int bits)
+__device__ __forceinline__ uint32_t sums_up_to_lane(uint32_t v)
 {
-    const int two = max(v, other_lane<0xb1>(v));            // lane ^ 1
-    v = bits > 0 ? two : v;
-    const int four = max(v, other_lane<0x4e>(v));           // lane ^ 2
-    v = bits > 1 ? four : v;
-    const int eight = max(v, other_lane<0x141>(v));         // 7 - lane of eight
-    v = bits > 2 ? eight : v;
-    const int sixteen = max(v, other_lane<0x140>(v));       // 15 - lane of sixteen
-    return bits > 3 ? sixteen : v;
+    return up_to_lane(v, 0, [](uint32_t x, uint32_t y) { return x + y; });
+}
+
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 63); }
+
+__device__ __forceinline__ uint32_t largest_of(uint32_t v)
+{
+    return last_lane(up_to_lane(v, 0, [](uint32_t x, uint32_t y) { return max(x, y); }));
+}
+
+__device__ __forceinline__ uint32_t smallest_of(uint32_t v)
+{
+    return last_lane(up_to_lane(v, ~0u, [](uint32_t x, uint32_t y) { return min(x, y); }));
 }
 
 // What is chosen by score: scores above `limit` and the first `ties` that equal it.
@@ -183,97 +201,195 @@ struct Limit {
     uint32_t ties;
 };
 
+constexpr int kBins = 256;
+
 template <int W>
 struct SelectShared {
-    float lo, hi;                      // of all waves' scores, as ordered numbers
-    uint32_t n[3], sure[W], ties[W];
+    uint32_t bins[W][kBins];           // a wave's own, or two of the workgroup's in turn
+    uint32_t lo[2], hi[2], found;      // of all waves' scores, as ordered numbers
+    uint32_t counts[W];
 };
 
-// The top-th largest of score[first .. before): bisection of the values between the
-// smallest and the largest, counting by ballots those not below the middle, until
-// the count is right or one value is left. By one wave (W = 1) or by all of a
-// workgroup's, which add their counts up in LDS. The first 8 scores of a lane stay
-// in registers, which is all up to 512 pages a wave.
+// The top-th largest of score[first .. before): the scores between the smallest and
+// the largest are counted in 256 equal parts, and the search goes on in the part that
+// holds the top-th, until all of it is wanted or it holds one value. By one wave
+// (W = 1) in bins of its own, or by all of a workgroup's. The parts that hold the
+// smallest and the largest score differ, so every round leaves a score out; two
+// rounds are usual. (A wave alone takes 8 clocks an instruction: halving the range by
+// counts took a dozen rounds of 0.6 us.) The first 8 scores of a lane stay in
+// registers, which is all up to 512 pages a wave.
 template <int W, class Shared>
 __device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int first, int before, int top)
 {
     constexpr int kHeld = 8;
-    const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (top == 0 || before <= first)
         return {INFINITY, 0};
-    const int from = first + 64 * wave + lane;
-    const int rest = first + 64 * W * kHeld;           // pages from here on are read again each time
-    float held[kHeld], lo = INFINITY, hi = -INFINITY;
+    const int from = first + (W == 1 ? 0 : 64 * wave) + lane;
+    const int rest = from + 64 * W * kHeld;            // pages from here on are read again each time
+    float held[kHeld];
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int j = from + 64 * W * i;
-        held[i] = j < before ? score[j] : -INFINITY;
-        lo = held[i] == -INFINITY ? lo : fminf(lo, held[i]);
-        hi = fmaxf(hi, held[i]);
+        held[i] = first + 64 * W * i < before && j < before ? score[j] : -INFINITY;
     }
-#pragma unroll 1
-    for (int j = rest + 64 * wave + lane; j < before; j += 64 * W) {
-        const float v = score[j];
-        lo = v == -INFINITY ? lo : fminf(lo, v);
-        hi = fmaxf(hi, v);
-    }
-#pragma unroll 1
-    for (int d = 32; d; d >>= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d));
-        hi = fmaxf(hi, __shfl_xor(hi, d));
-    }
-    if (W > 1) {
-        if (lane == 0) {
-            atomicMin((int*)&lds.lo, (int)(ordered(lo) ^ 0x80000000u));
-            atomicMax((int*)&lds.hi, (int)(ordered(hi) ^ 0x80000000u));
-        }
-        __syncthreads();
-        lo = number(__float_as_uint(lds.lo) ^ 0x80000000u);
-        hi = number(__float_as_uint(lds.hi) ^ 0x80000000u);
-    }
-    if (lo > hi)
-        return {INFINITY, 0};
-    // the top-th largest is in [lo, hi]; `above` are larger than hi
-    int above = 0, turn = 0;
-    float mid = lo;
-    for (;;) {
-        int c = 0;
+    auto each = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            c += __popcll(__ballot(held[i] >= mid));
+            if (first + 64 * W * i < before)
+                f(held[i]);
 #pragma unroll 1
-        for (int j0 = rest + 64 * wave; j0 < before; j0 += 64 * W)
-            c += __popcll(__ballot(j0 + lane < before && score[j0 + lane] >= mid));
+        for (int j = rest; j < before; j += 64 * W)
+            f(score[j]);
+    };
+    uint32_t low = ~0u, high = 0, n = 0;
+    each([&](float v) {
+        const bool in = v != -INFINITY;
+        low = min(low, in ? ordered(v) : ~0u);
+        high = max(high, in ? ordered(v) : 0);
+        n += in;
+    });
+    low = smallest_of(low);
+    high = largest_of(high);
+    n = last_lane(sums_up_to_lane(n));
+    if (W > 1) {
+        if (lane == 0) {
+            atomicMin(&lds.lo[0], low);
+            atomicMax(&lds.hi[0], high);
+            atomicAdd(&lds.found, n);
+        }
+        __syncthreads();
+        low = lds.lo[0];
+        high = lds.hi[0];
+        n = lds.found;
+    }
+    if ((int)n <= top)
+        return {-INFINITY, 0};
+    // the limit is the want-th largest of the n scores in [lo, hi]
+    float lo = number(low), hi = number(high);
+    uint32_t want = top;
+    for (int turn = 0; lo < hi; turn ^= 1) {
+        uint32_t* bins = lds.bins[W == 1 ? wave : turn];
+        const float scale = (float)kBins / (hi - lo);
+        // a larger score never goes to a lower part
+        auto part = [&](float v) { return min((int)((v - lo) * scale), kBins - 1); };
+        if (W == 1) {
+            *(uint4v*)&bins[4 * lane] = uint4v{0, 0, 0, 0};
+            asm volatile("" ::: "memory");              // a wave's accesses to LDS keep their order
+        }
+        each([&](float v) {
+            if (v >= lo && v <= hi)
+                atomicAdd(&bins[part(v)], 1u);
+        });
         if (W > 1) {
-            // the next turn's sum is cleared in front of this turn's barrier; it was last
-            // read in front of the barrier before
-            if (lane == 0)
-                atomicAdd(&lds.n[turn], (uint32_t)c);
-            const int next = turn == 2 ? 0 : turn + 1;
-            if (threadIdx.x == 0)
-                lds.n[next] = 0;
+            // what the next round adds to was last read in front of the barrier before
+            if (wave == 0)
+                *(uint4v*)&lds.bins[turn ^ 1][4 * lane] = uint4v{0, 0, 0, 0};
+            if (threadIdx.x == 0) {
+                lds.lo[turn ^ 1] = ~0u;
+                lds.hi[turn ^ 1] = 0;
+            }
             __syncthreads();
-            c = lds.n[turn];
-            turn = next;
         }
-        if (c >= top) {
-            lo = mid;
-            if (c == top)
-                return {lo, ~0u};
-        } else {
-            if (mid == lo)                  // all of them, and fewer than top
-                return {-INFINITY, 0};
-            above = c;
-            hi = number(ordered(mid) - 1);  // the next smaller number: not below lo
+        asm volatile("" ::: "memory");
+        const uint4v mine = *(const uint4v*)&bins[4 * lane];
+        const uint32_t sum = mine[0] + mine[1] + mine[2] + mine[3];
+        uint32_t above = n - sums_up_to_lane(sum);      // in the lanes above
+        uint32_t chosen = 0, more = 0, left = 0;
+        bool here = false;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const bool it = above < want && above + mine[i] >= want;
+            chosen = it ? 4 * lane + i : chosen;
+            more = it ? above : more;
+            left = it ? mine[i] : left;
+            here = here || it;
+            above += mine[i];
         }
-        if (lo >= hi)
-            return {lo, (uint32_t)(top - above)};
-        mid = lo + 0.5f * (hi - lo);
-        mid = mid > lo ? mid : hi;
+        const int at = __ffsll((long long)__ballot(here)) - 1;
+        chosen = (uint32_t)__builtin_amdgcn_readlane((int)chosen, at);
+        want -= (uint32_t)__builtin_amdgcn_readlane((int)more, at);
+        n = (uint32_t)__builtin_amdgcn_readlane((int)left, at);
+        low = ~0u;
+        high = 0;
+        each([&](float v) {
+            const bool in = v >= lo && v <= hi && part(v) == (int)chosen;
+            low = min(low, in ? ordered(v) : ~0u);
+            high = max(high, in ? ordered(v) : 0);
+        });
+        low = smallest_of(low);
+        high = largest_of(high);
+        if (W > 1) {
+            if (lane == 0) {
+                atomicMin(&lds.lo[turn ^ 1], low);
+                atomicMax(&lds.hi[turn ^ 1], high);
+            }
+            __syncthreads();
+            low = lds.lo[turn ^ 1];
+            high = lds.hi[turn ^ 1];
+        }
+        lo = number(low);
+        hi = number(high);
+        if (n == want)
+            return {lo, ~0u};
+    }
+    return {lo, want};
+}
+
+// Where a request's tokens stand: its table, the new tokens' end, its length.
+struct Place {
+    const int32_t* table;
+    int behind, len;
+};
+
+__device__ __forceinline__ Place place_of(const Requests& r, int b)
+{
+    return {r.table + b * r.ld_table, r.offsets[b + 1], length_of(r, b)};
+}
+
+// The pages in front of which the one at position p, in a page of its own, chooses
+// by score.
+__device__ __forceinline__ int scored_before(const Select& a, int p)
+{
+    return p < 0 ? 0 : max(p / a.r.page - a.local + 1, 0);
+}
+
+template <int D>
+using Queries = uint8_t[kMostRows][D + 16];
+
+// Rows h0, ... of the `run` tokens' queries (at most 64 rows) in 8 bits: a token a
+// wave, or a single token by all W waves.
+template <int D, int W>
+__device__ __forceinline__ void quantize_queries(Queries<D>& q8, const uint16_t* q, int64_t ld_q, int group, int h0,
+                                                 int heads, int run)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll 1
+    for (int i = run == 1 ? 0 : wave; i < run; i += W) {
+        const uint16_t* qi = q + i * ld_q;
+        uint32_t top = 0;
+#pragma unroll 1
+        for (int x = lane; x < group * D / 8; x += 64) {
+            const uint4v w = *(const uint4v*)(qi + 8 * x);
+            for (int k = 0; k < 4; ++k)
+                top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
+        }
+        top = largest_of(top);
+        const int e = top == 0 || top >= 0x7f800000u ? 0 : 6 - ilogbf(__uint_as_float(top));
+#pragma unroll 1
+        for (int x = (run == 1 ? 64 * wave : 0) + lane; x < heads * D / 8; x += run == 1 ? 64 * W : 64) {
+            const uint4v w = *(const uint4v*)(qi + h0 * D + 8 * x);
+            uint32_t v[2] = {0, 0};
+            for (int k = 0; k < 8; ++k) {
+                const float y = ldexpf(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), e);
+                v[k >> 2] |= (uint32_t)((int)rintf(__builtin_amdgcn_fmed3f(y, -127.0f, 127.0f)) & 255) << (8 * (k & 3));
+            }
+            *(uint2*)&q8[i * heads + x / (D / 8)][x % (D / 8) * 8] = make_uint2(v[0], v[1]);
+        }
     }
 }
 
-// Sixteen pages for a wave: their keys as the left operand of the products (lane % 16
+// Sixteen pages for a wave: their keys as the right operand of the products (lane % 16
 // the page, 16 (lane / 16) + 64 k .. the dimensions), their exponents.
 template <int D>
 struct PageTile {
@@ -281,19 +397,155 @@ struct PageTile {
     int exponent;        // -1: not a page to be chosen
 };
 
-template <int D, int W>
-__global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
+// entry: this lane's page in the cache, any other number for none.
+template <int D>
+__device__ __forceinline__ void load_pages(PageTile<D>& t, const Select& a, int entry, int h)
 {
-    constexpr int K = D / 64, kPitch = D + 16;
-    extern __shared__ __align__(16) float score[];        // [tokens][pitch]; -inf: not to be chosen
-    __shared__ __align__(16) uint8_t q8[kMostRows][kPitch];
-    __shared__ SelectShared<W> lds;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int group = a.heads / a.kv_heads, listed = a.first + a.top + a.local;
-    int bits = 0;                                         // 2^bits columns for a token, at most 16
+    const int g = (threadIdx.x & 63) >> 4;
+    const bool in = entry >= 0 && entry < a.r.num_pages;
+    const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
+    t.exponent = -1;
+    if (in) {
+        t.exponent = min(max((int)a.exponents[at], 0), 64);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+            t.key[k] = *(const int4v*)(a.keys + at * D + 64 * k + 16 * g);
+    }
+}
+
+// The scores of a tile's pages: put(token, score) for this lane's page (lane % 16) and
+// the tokens below `run` that the lane ends up with.
+template <int D, class Put>
+__device__ __forceinline__ void compare(const PageTile<D>& t, const Queries<D>& q8, int heads, int bits, int run, Put put)
+{
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int parts = (heads + 15) / 16;
+    auto score = [&](int of, int v) {
+        if (of < run)
+            put(of, t.exponent < 0 ? -INFINITY : ldexpf((float)v, t.exponent));
+    };
+    // row tiles: several tokens each, or several for a token
+#pragma unroll 1
+    for (int t0 = 0; t0 < run; t0 += 16 >> bits) {
+        const int row0 = min(t0 + (n >> bits), run - 1) * heads, part = n & ((1 << bits) - 1);
+        int4v best = {INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN};
+#pragma unroll 1
+        for (int p = 0; p < parts; ++p) {
+            const uint8_t* row = q8[row0 + min(16 * p + part, heads - 1)] + 16 * g;
+            int4v sum = {0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+                sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const int4v*)(row + 64 * k), t.key[k], sum, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                best[i] = max(best[i], sum[i]);
+        }
+        // row 4 g + i of the tile: the token t0 + (4 g + i >> bits)
+        if (bits >= 2) {
+            int v = max(max(best[0], best[1]), max(best[2], best[3]));
+            if (bits >= 3)
+                v = max(v, __shfl_xor(v, 16));
+            if (bits >= 4)
+                v = max(v, __shfl_xor(v, 32));
+            if ((4 * g & ((1 << bits) - 1)) == 0)
+                score(t0 + (4 * g >> bits), v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (bits == 0)
+                    score(t0 + 4 * g + i, best[i]);
+                else if (i % 2 == 0)
+                    score(t0 + 2 * g + i / 2, max(best[i], best[i + 1]));
+        }
+    }
+}
+
+// 2^bits rows for a token of `group` heads, at most 16.
+__device__ __forceinline__ int bits_of(int group)
+{
+    int bits = 0;
     while (bits < 4 && 1 << bits < group)
         ++bits;
+    return bits;
+}
+
+// Writes the list of the token at position p: by one wave (W = 1), or by all of a
+// workgroup's. A lane takes pages in a row, an odd number of them (LDS banks): it
+// counts, the counts in front of it are summed, then it writes.
+template <int W, class Shared>
+__device__ __forceinline__ void write_list(Shared& lds, const Select& a, const float* score, int p, int32_t* out)
+{
+    const int lane = threadIdx.x & 63, wave = W == 1 ? 0 : threadIdx.x >> 6, listed = a.first + a.top + a.local;
+    const int pages = p < 0 ? 0 : p / a.r.page + 1, end = max(pages - a.local, 0);
+    // up to 512 pages every wave searches for itself, without a barrier
+    const Limit l = W == 1 || end - a.first <= 512 ? find_limit<1>(lds, score, a.first, end, a.top)
+                                                   : find_limit<W>(lds, score, a.first, end, a.top);
+    const int each = (pages + 64 * W - 1) / (64 * W) | 1;
+    const int from = min((64 * wave + lane) * each, pages), to = min(from + each, pages);
+    auto judge = [&](int j, bool& sure, bool& tie) {
+        const bool scored = j >= a.first && j < end;
+        const float v = scored ? score[j] : INFINITY;
+        sure = !scored || v > l.limit;
+        tie = scored && v == l.limit && v != -INFINITY;
+    };
+    // sure ones, and ties in the upper half: there are at most 32768 pages
+    uint32_t count = 0;
+#pragma unroll 1
+    for (int j = from; j < to; ++j) {
+        bool sure, tie;
+        judge(j, sure, tie);
+        count += sure ? 1 : tie ? 1 << 16 : 0;
+    }
+    const uint32_t sums = sums_up_to_lane(count);
+    uint32_t before = sums - count, all = last_lane(sums);
+    if (W > 1) {
+        if (lane == 0)
+            lds.counts[wave] = all;
+        __syncthreads();
+        all = 0;
+#pragma unroll 1
+        for (int w = 0; w < W; ++w) {
+            before += w < wave ? lds.counts[w] : 0;
+            all += lds.counts[w];
+        }
+    }
+    uint32_t seen = before >> 16, at = (before & 0xffff) + min(seen, l.ties);
+#pragma unroll 1
+    for (int j = from; j < to; ++j) {
+        bool sure, tie;
+        judge(j, sure, tie);
+        if (sure || (tie && seen < l.ties))
+            out[at++] = j;
+        seen += !sure && tie;
+    }
+    const int total = (int)((all & 0xffff) + min(all >> 16, l.ties));
+#pragma unroll 1
+    for (int i = total + (W == 1 ? lane : threadIdx.x); i < listed; i += 64 * W)
+        out[i] = -1;
+}
+
+template <int W>
+__device__ __forceinline__ void clear(SelectShared<W>& lds)
+{
+    if (threadIdx.x < 64)
+        *(uint4v*)&lds.bins[0][4 * threadIdx.x] = uint4v{0, 0, 0, 0};
+    if (threadIdx.x == 0) {
+        lds.lo[0] = ~0u;
+        lds.hi[0] = 0;
+        lds.found = 0;
+    }
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void select_chunk_kernel(Select a)
+{
+    constexpr int W = 4, kAhead = D > 128 ? 2 : 4;
+    extern __shared__ __align__(16) float score[];        // [tokens][pitch]; -inf: not to be chosen
+    __shared__ __align__(16) Queries<D> q8;
+    __shared__ __align__(16) SelectShared<W> lds;
+    const int tid = threadIdx.x, lane = tid & 63, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = a.heads / a.kv_heads, listed = a.first + a.top + a.local, bits = bits_of(group);
     const int h = blockIdx.x % a.kv_heads;
     int token = blockIdx.x / a.kv_heads * a.together;
     const int token_end = min(token + a.together, a.tokens);
@@ -304,19 +556,13 @@ __global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
         const int b = request_of(a.r, token);
         if (b < 0)
             continue;
-        const int behind = a.r.offsets[b + 1], len = length_of(a.r, b);
-        run = min(token_end, behind) - token;
-        const int pos0 = min(len - behind + token, len - 1), pos1 = min(pos0 + run, len) - 1;
-        const int32_t* table = a.r.table + b * a.r.ld_table;
+        const Place r = place_of(a.r, b);
+        run = min(token_end, r.behind) - token;
+        const int pos0 = min(r.len - r.behind + token, r.len - 1), pos1 = min(pos0 + run, r.len) - 1;
         const uint16_t* q = a.q + token * a.ld_q + h * group * D;
-        // the pages that some token may choose by score
-        const int before = pos1 < 0 ? 0 : max(pos1 / a.r.page - a.local + 1, 0);
+        const int before = scored_before(a, pos1);        // for the last of the tokens
         __syncthreads();                                  // the LDS of what came before is read
-        if (tid == 0) {
-            lds.lo = __int_as_float(INT32_MAX);
-            lds.hi = __int_as_float(INT32_MIN);
-            lds.n[0] = 0;
-        }
+        clear(lds);
 
         // scores, of 64 query rows at a time: run * group rows, or the heads of a token
 #pragma unroll 1
@@ -325,165 +571,169 @@ __global__ __launch_bounds__(64 * W) void select_pages_kernel(Select a)
             if (h0)
                 __syncthreads();
             else
-                // places in the cache, -1 where hidden, wait in LDS where the scores go
+                // places in the cache wait in LDS where the scores go
 #pragma unroll 1
-                for (int j = a.first + tid; j < before; j += 64 * W) {
-                    const int entry = table[j];
-                    score[j] = __int_as_float(entry >= 0 && entry < a.r.num_pages ? entry : -1);
-                }
-            // queries in 8 bits, a token a wave or a single token by all waves
-#pragma unroll 1
-            for (int i = run == 1 ? 0 : wave; i < run; i += W) {
-                const uint16_t* qi = q + i * a.ld_q;
-                uint32_t top = 0;
-#pragma unroll 1
-                for (int x = lane; x < group * D / 8; x += 64) {
-                    const uint4v w = *(const uint4v*)(qi + 8 * x);
-                    for (int k = 0; k < 4; ++k)
-                        top = max(top, max(w[k] << 16 & 0x7fff0000u, w[k] & 0x7fff0000u));
-                }
-#pragma unroll 1
-                for (int d = 32; d; d >>= 1)
-                    top = max(top, (uint32_t)__shfl_xor((int)top, d));
-                const int e = top == 0 || top >= 0x7f800000u ? 0 : 6 - ilogbf(__uint_as_float(top));
-#pragma unroll 1
-                for (int x = (run == 1 ? 64 * wave : 0) + lane; x < heads * D / 8; x += run == 1 ? 64 * W : 64) {
-                    const uint4v w = *(const uint4v*)(qi + h0 * D + 8 * x);
-                    uint32_t v[2] = {0, 0};
-                    for (int k = 0; k < 8; ++k) {
-                        const float y = ldexpf(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16), e);
-                        v[k >> 2] |= (uint32_t)((int)rintf(__builtin_amdgcn_fmed3f(y, -127.0f, 127.0f)) & 255) << (8 * (k & 3));
-                    }
-                    *(uint2*)&q8[i * heads + x / (D / 8)][x % (D / 8) * 8] = make_uint2(v[0], v[1]);
-                }
-            }
+                for (int j = a.first + tid; j < before; j += 64 * W)
+                    score[j] = __int_as_float(r.table[j]);
+            quantize_queries<D, W>(q8, q, a.ld_q, group, h0, heads, run);
             __syncthreads();
-
-            auto load = [&](PageTile<D>& t, int j0) {
-                const int j = j0 + n;
-                int entry = -1;
-                if (j < before)
-                    entry = h0 ? table[j] : __float_as_int(score[j]);
-                const bool in = entry >= 0 && entry < a.r.num_pages;
-                const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
-                t.exponent = -1;
-                if (in) {
-                    t.exponent = min(max((int)a.exponents[at], 0), 64);
+            // kAhead tiles of a wave's at a time
+#pragma unroll 1
+            for (int j0 = a.first + 16 * wave; j0 < before; j0 += 16 * W * kAhead) {
+                PageTile<D> tile[kAhead];
 #pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        t.key[k] = *(const int4v*)(a.keys + at * D + 64 * k + 16 * g);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = j0 + 16 * W * u + n;
+                    load_pages(tile[u], a, j >= before ? -1 : h0 ? r.table[j] : __float_as_int(score[j]), h);
                 }
-            };
-            // column tiles: several tokens each, or several for a token
-            const int parts = (heads + 15) / 16;
-            auto compare = [&](const PageTile<D>& t, int j0) {
-                int e[4];
-                for (int i = 0; i < 4; ++i)
-                    e[i] = __builtin_amdgcn_ds_bpermute((4 * g + i) * 4, t.exponent);
-#pragma unroll 1
-                for (int t0 = 0; t0 < run; t0 += 16 >> bits) {
-                    const int of = t0 + (n >> bits), row0 = min(of, run - 1) * heads, col = n & ((1 << bits) - 1);
-                    int best[4] = {INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN};
-#pragma unroll 1
-                    for (int p = 0; p < parts; ++p) {
-                        const uint8_t* row = q8[row0 + min(16 * p + col, heads - 1)] + 16 * g;
-                        int4v sum = {0, 0, 0, 0};
 #pragma unroll
-                        for (int k = 0; k < K; ++k)
-                            sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(t.key[k], *(const int4v*)(row + 64 * k), sum, 0, 0, 0);
-                        for (int i = 0; i < 4; ++i)
-                            best[i] = max(best[i], sum[i]);
-                    }
-                    for (int i = 0; i < 4; ++i)
-                        best[i] = max_of(best[i], bits);
-                    if (col == 0 && of < run) {
-                        float* at = score + of * a.pitch + j0 + 4 * g;
-                        for (int i = 0; i < 4; ++i) {
-                            const float v = e[i] < 0 ? -INFINITY : ldexpf((float)best[i], e[i]);
-                            if (j0 + 4 * g + i < before)
-                                at[i] = h0 ? fmaxf(at[i], v) : v;
-                        }
-                    }
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = j0 + 16 * W * u + n;
+                    if (j - n < before)
+                        compare<D>(tile[u], q8, heads, bits, run, [&](int of, float v) {
+                            float* at = score + of * a.pitch + j;
+                            if (j < before)
+                                *at = h0 ? fmaxf(*at, v) : v;
+                        });
                 }
-            };
-            PageTile<D> next;
-            load(next, a.first + 16 * wave);
-#pragma unroll 1
-            for (int j0 = a.first + 16 * wave; j0 < before; j0 += 16 * W) {
-                const PageTile<D> tile = next;
-                load(next, j0 + 16 * W);
-                compare(tile, j0);
             }
         }
         __syncthreads();
+        int32_t* out = a.pages + ((int64_t)token * a.kv_heads + h) * listed;
+        if (run == 1)
+            write_list<W>(lds, a, score, pos0, out);
+        else
+#pragma unroll 1
+            for (int i = wave; i < run; i += W)
+                write_list<1>(lds, a, score + i * a.pitch, min(pos0 + i, r.len - 1), out + (int64_t)i * a.kv_heads * listed);
+    }
+}
 
-        // The listed pages in order: a wave takes a token, or a run of a single token's
-        // pages, which it counts first and then writes.
-        const int shares = run == 1 ? W : 1;
+constexpr int kPagesOfScores = 256;      // of a workgroup of score_pages_kernel
+
+template <int D>
+__global__ __launch_bounds__(256) void score_pages_kernel(Select a)
+{
+    constexpr int W = 4, kTiles = kPagesOfScores / 16 / W;
+    __shared__ __align__(16) Queries<D> q8;
+    const int n = threadIdx.x & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.heads / a.kv_heads, bits = bits_of(group);
+    const int h = blockIdx.x % a.kv_heads, chunk = blockIdx.x / a.kv_heads % a.chunks;
+    const int first = a.first + chunk * kPagesOfScores + 16 * wave;
+    int token = blockIdx.x / a.kv_heads / a.chunks * a.together;
+    const int token_end = min(token + a.together, a.tokens);
 #pragma unroll 1
-        for (int i = run == 1 ? 0 : wave; i < run; i += W) {
-            const float* mine = score + i * a.pitch;
-            int32_t* out = a.pages + ((int64_t)(token + i) * a.kv_heads + h) * listed;
-            const int p = min(pos0 + i, len - 1), pages = p < 0 ? 0 : p / a.r.page + 1, end = max(pages - a.local, 0);
-            const Limit l = run == 1 ? find_limit<W>(lds, mine, a.first, end, a.top) : find_limit<1>(lds, mine, a.first, end, a.top);
-            const int each = (pages + shares * 64 - 1) / (shares * 64) * 64;
-            const int from = run == 1 ? min(wave * each, pages) : 0, to = min(from + each, pages);
-            uint32_t at = 0, seen = 0;
+    for (int run = 1; token < token_end; token += run) {
+        run = 1;
+        const int b = request_of(a.r, token);
+        if (b < 0)
+            continue;
+        const Place r = place_of(a.r, b);
+        run = min(token_end, r.behind) - token;
+        const int before = scored_before(a, min(r.len - r.behind + token + run, r.len) - 1);
+        if (first - 16 * wave >= before)
+            continue;
+        PageTile<D> tile[kTiles];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+            load_pages(tile[u], a, first + 16 * W * u + n < before ? r.table[first + 16 * W * u + n] : -1, h);
+        const uint16_t* q = a.q + token * a.ld_q + h * group * D;
+        float* score = a.scores + ((int64_t)token * a.kv_heads + h) * a.pitch;
 #pragma unroll 1
-            for (int pass = shares == 1; pass < 2; ++pass) {
-                uint32_t sure = 0, tied = seen;
-                const uint64_t below = (1ull << lane) - 1;
-#pragma unroll 1
-                for (int j0 = from; j0 < to; j0 += 64) {
-                    const int j = j0 + lane;
-                    const bool scored = j >= a.first && j < end;
-                    const float v = scored ? mine[j] : 0.0f;
-                    const bool tie = scored && v == l.limit && j < to && v != -INFINITY;
-                    const uint64_t equal = __ballot(tie);
-                    const bool in = j < to && (scored ? v > l.limit || (pass && tie && tied + __popcll(equal & below) < l.ties) : true);
-                    const uint64_t taken = __ballot(in);
-                    if (pass && in)
-                        out[at + sure + __popcll(taken & below)] = j;
-                    sure += __popcll(taken);
-                    tied += __popcll(equal);
-                }
-                if (pass == 0) {
-                    if (lane == 0) {
-                        lds.sure[wave] = sure;
-                        lds.ties[wave] = tied;
-                    }
-                    __syncthreads();
-#pragma unroll 1
-                    for (int w = 0; w < wave; ++w) {
-                        at += lds.sure[w];
-                        seen += lds.ties[w];
-                    }
-                    at += min(seen, l.ties);
-                } else if (to == pages && (from < to || run > 1 || wave == 0)) {
-                    // the last pages' wave fills the rest of the list
-#pragma unroll 1
-                    for (int x = (int)(at + sure) + lane; x < listed; x += 64)
-                        out[x] = -1;
-                }
+        for (int h0 = 0; h0 < group; h0 += kMostRows) {
+            const int heads = min(group - h0, kMostRows);
+            __syncthreads();                              // the queries of before are read
+            quantize_queries<D, W>(q8, q, a.ld_q, group, h0, heads, run);
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) {
+                const int j = first + 16 * W * u + n;
+                if (j - n < before)
+                    compare<D>(tile[u], q8, heads, bits, run, [&](int of, float v) {
+                        float* at = score + (int64_t)of * a.kv_heads * a.pitch + j;
+                        if (j < before)
+                            *at = h0 ? fmaxf(*at, v) : v;
+                    });
             }
         }
     }
 }
 
-template <int D>
-void launch_select(const Select& a, dim3 grid, unsigned lds, hipStream_t stream)
+template <int W>
+__global__ __launch_bounds__(64 * W) void list_pages_kernel(Select a)
 {
-    // a grid holds less than 2^32 threads
-    if (a.together > 1 || a.r.max_pages <= 512 || grid.x > (1 << 20))
-        hipLaunchKernelGGL((select_pages_kernel<D, 4>), grid, dim3(256), lds, stream, a);
+    extern __shared__ __align__(16) float score[];
+    __shared__ __align__(16) SelectShared<W> lds;
+    const int token = blockIdx.x / a.kv_heads;
+    const int b = request_of(a.r, token);
+    if (b < 0)
+        return;
+    const Place r = place_of(a.r, b);
+    const int p = min(r.len - r.behind + token, r.len - 1), before = scored_before(a, p);
+    const float* from = a.scores + (int64_t)blockIdx.x * a.pitch;
+    for (int j = a.first + threadIdx.x; j < before; j += 64 * W)
+        score[j] = from[j];
+    clear(lds);
+    __syncthreads();
+    write_list<W>(lds, a, score, p, a.pages + (int64_t)blockIdx.x * (a.first + a.top + a.local));
+}
+
+// How the work is cut.
+struct SelectPlan {
+    int together;          // tokens of a workgroup that keeps their scores in LDS
+    int chunks;            // workgroups over a token's pages, 0: no such workgroups
+    int pitch;
+    int64_t workspace;
+};
+
+SelectPlan select_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t num_seqs, int64_t max_pages)
+{
+    SelectPlan p = {1, 0, ((int)max_pages + 3) & ~3, 0};
+    // Tokens of long chunks go to a workgroup together, as many as 64 query rows and
+    // 64 KB of scores hold, at most 16.
+    const int group = heads / kv_heads;
+    while (p.together < 16 && p.together < tokens / (num_seqs < 1 ? 1 : num_seqs) &&
+           (p.together + 1) * group <= kMostRows && (int64_t)(p.together + 1) * p.pitch * 4 <= 65536)
+        ++p.together;
+    const int64_t bytes = tokens * kv_heads * p.pitch * 4;
+    if (serving::ceil_div(tokens, (int64_t)p.together) * kv_heads <= 768 && bytes <= 1 << 28) {
+        p.chunks = serving::ceil_div(p.pitch, kPagesOfScores);
+        p.workspace = bytes;
+    }
+    return p;
+}
+
+template <int D>
+void launch_select(const Select& a, hipStream_t stream)
+{
+    const unsigned items = (unsigned)((a.tokens + (int64_t)a.together - 1) / a.together * a.kv_heads);
+    const unsigned lds = (unsigned)(a.together * a.pitch * 4);
+    if (a.chunks == 0) {
+        hipLaunchKernelGGL((select_chunk_kernel<D>), dim3(items), dim3(256), lds, stream, a);
+        return;
+    }
+    const unsigned lists = (unsigned)(a.tokens * a.kv_heads);
+    hipLaunchKernelGGL((score_pages_kernel<D>), dim3(items * a.chunks), dim3(256), 0, stream, a);
+    if (a.pitch <= 2048)
+        hipLaunchKernelGGL((list_pages_kernel<4>), dim3(lists), dim3(256), a.pitch * 4, stream, a);
     else
-        hipLaunchKernelGGL((select_pages_kernel<D, 16>), grid, dim3(1024), lds, stream, a);
+        hipLaunchKernelGGL((list_pages_kernel<16>), dim3(lists), dim3(1024), a.pitch * 4, stream, a);
 }
 
 bool requests_ok(int64_t num_slots, int32_t page_size, int64_t ld_table, int64_t max_pages, int64_t num_seqs)
 {
     return page_size >= 1 && num_slots >= 0 && num_slots % page_size == 0 && max_pages >= 0 && ld_table >= max_pages &&
            num_seqs >= 0 && serving::extent_ok(num_seqs, ld_table, 4);
+}
+
+bool select_sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t num_seqs, int64_t max_pages)
+{
+    return tokens >= 0 && heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && num_seqs >= 0 && max_pages >= 0;
+}
+
+bool select_sizes_supported(int64_t tokens, int32_t heads, int64_t num_seqs, int64_t max_pages)
+{
+    return heads <= 1024 && num_seqs <= 65535 && tokens <= (1 << 23) / heads && max_pages <= kMostPages;
 }
 
 }  // namespace
@@ -527,22 +777,30 @@ extern "C" nvfp4_status_t nvfp4_page_keys(const uint8_t* k_packed, const uint8_t
     return launched();
 }
 
+extern "C" int64_t nvfp4_select_pages_workspace(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t num_seqs,
+                                                int64_t max_pages)
+{
+    if (!select_sizes_ok(tokens, heads, kv_heads, num_seqs, max_pages) ||
+        !select_sizes_supported(tokens, heads, num_seqs, max_pages))
+        return -1;
+    return select_plan(tokens, heads, kv_heads, num_seqs, max_pages).workspace;
+}
+
 extern "C" nvfp4_status_t nvfp4_select_pages(const uint16_t* q, int64_t tokens, int64_t ld_q, int32_t heads,
                                              int32_t kv_heads, int32_t head_dim, const int8_t* keys,
                                              const int8_t* exponents, int64_t num_slots, int32_t page_size,
                                              const int32_t* block_table, int64_t ld_table, int64_t max_pages,
                                              const int32_t* seq_lens, const int32_t* query_offsets, int64_t num_seqs,
-                                             int32_t top_k, int32_t first, int32_t local, int32_t* pages,
-                                             hipStream_t stream)
+                                             int32_t top_k, int32_t first, int32_t local, int32_t* pages, void* workspace,
+                                             int64_t workspace_bytes, hipStream_t stream)
 {
     using namespace serving;
-    if (tokens < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || top_k < 0 || first < 0 || local < 1 ||
-        ld_q < 0 || !requests_ok(num_slots, page_size, ld_table, max_pages, num_seqs))
+    if (!select_sizes_ok(tokens, heads, kv_heads, num_seqs, max_pages) || top_k < 0 || first < 0 || local < 1 || ld_q < 0 ||
+        workspace_bytes < 0 || !requests_ok(num_slots, page_size, ld_table, max_pages, num_seqs))
         return NVFP4_ERROR_INVALID_VALUE;
-    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || heads > 1024 || num_seqs > 65535 ||
-        num_slots > INT32_MAX || tokens > (1 << 23) / heads || max_pages > kMostPages ||
-        max_pages > (1 << 30) / page_size || top_k > kMostListed || first > kMostListed || local > kMostListed ||
-        first + top_k + local > kMostListed)
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || !select_sizes_supported(tokens, heads, num_seqs, max_pages) ||
+        num_slots > INT32_MAX || max_pages > (1 << 30) / page_size || top_k > kMostListed || first > kMostListed ||
+        local > kMostListed || first + top_k + local > kMostListed)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     if (ld_q < (int64_t)heads * head_dim || !extent_ok(tokens, ld_q, 2))
         return NVFP4_ERROR_INVALID_VALUE;
@@ -554,24 +812,20 @@ extern "C" nvfp4_status_t nvfp4_select_pages(const uint16_t* q, int64_t tokens, 
     if (!aligned(q, 16) || !aligned(keys, 16) || ld_q % 8 != 0 || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
         !aligned(query_offsets, 4) || !aligned(pages, 4))
         return NVFP4_ERROR_MISALIGNED;
-    Select a = {q, keys, exponents, pages,
-                {block_table, seq_lens, query_offsets, ld_table, (int)(num_slots / page_size), (int)max_pages,
-                 page_size, (int)num_seqs},
-                ld_q, (int)tokens, heads, kv_heads, top_k, first, local, 1, ((int)max_pages + 3) & ~3};
-    // Tokens of long chunks go to a workgroup together, as many as 64 query rows and
-    // 64 KB of scores hold, at most 16.
-    const int group = heads / kv_heads;
-    while (a.together < 16 && a.together < tokens / num_seqs && (a.together + 1) * group <= kMostRows &&
-           (a.together + 1) * a.pitch * 4 <= 65536)
-        ++a.together;
-    const int64_t items = ceil_div(tokens, (int64_t)a.together) * kv_heads;
-    const dim3 grid((unsigned)items);
-    const unsigned lds = (unsigned)(a.together * a.pitch * 4);
+    const SelectPlan p = select_plan(tokens, heads, kv_heads, num_seqs, max_pages);
+    if (!aligned(workspace, 16))
+        return NVFP4_ERROR_MISALIGNED;
+    if (workspace_bytes < p.workspace || (p.workspace > 0 && !workspace))
+        return NVFP4_ERROR_INVALID_VALUE;
+    const Select a = {q, keys, exponents, pages, (float*)workspace,
+                      {block_table, seq_lens, query_offsets, ld_table, (int)(num_slots / page_size), (int)max_pages,
+                       page_size, (int)num_seqs},
+                      ld_q, (int)tokens, heads, kv_heads, top_k, first, local, p.together, p.pitch, p.chunks};
     if (head_dim == 64)
-        launch_select<64>(a, grid, lds, stream);
+        launch_select<64>(a, stream);
     else if (head_dim == 128)
-        launch_select<128>(a, grid, lds, stream);
+        launch_select<128>(a, stream);
     else
-        launch_select<256>(a, grid, lds, stream);
+        launch_select<256>(a, stream);
     return launched();
 }

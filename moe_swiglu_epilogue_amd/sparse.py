@@ -17,8 +17,8 @@ from . import binding as _b
 from .serving import (_BF16, _F32, _I32, _I32_MAX, _I64, _U8, _all, _at_most, _check, _cuda, _current, _elsewhere, _empty,
                       _fits, _heads, _new, _scalar, _table, _vector, _workspace)
 
-EXPORTS = ("nvfp4_rope_append", "nvfp4_page_keys", "nvfp4_select_pages", "nvfp4_sparse_attention",
-           "nvfp4_sparse_attention_workspace")
+EXPORTS = ("nvfp4_rope_append", "nvfp4_page_keys", "nvfp4_select_pages", "nvfp4_select_pages_workspace",
+           "nvfp4_sparse_attention", "nvfp4_sparse_attention_workspace")
 
 _LIB = None
 _I8 = torch.int8
@@ -33,12 +33,14 @@ def _lib():
                                         _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]
         L.nvfp4_page_keys.argtypes = [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp]
         L.nvfp4_select_pages.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp, _i64, _i64, _vp, _vp,
-                                         _i64, _i32, _i32, _i32, _vp, _vp]
+                                         _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp]
+        L.nvfp4_select_pages_workspace.argtypes = [_i64, _i32, _i32, _i64, _i64]
         L.nvfp4_sparse_attention.argtypes = [_vp, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _i64, _i64,
                                              _vp, _vp, _i64, _vp, _i64, _f32, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
         L.nvfp4_sparse_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64, _i64]
         for fn in (L.nvfp4_rope_append, L.nvfp4_page_keys, L.nvfp4_select_pages, L.nvfp4_sparse_attention):
             fn.restype = C.c_int
+        L.nvfp4_select_pages_workspace.restype = _i64
         L.nvfp4_sparse_attention_workspace.restype = _i64
         _LIB = L
     return _LIB
@@ -62,6 +64,16 @@ def _pages(page_size, rows):
         raise ValueError("page_size must be at least 1 and fit 32 bits")
     if rows % page_size:
         raise ValueError("the cache must hold whole pages")
+
+
+@functools.lru_cache(maxsize=256)
+def _select_workspace(*sizes):
+    return _lib().nvfp4_select_pages_workspace(*sizes)
+
+
+@functools.lru_cache(maxsize=256)
+def _sparse_workspace(*sizes):
+    return _lib().nvfp4_sparse_attention_workspace(*sizes)
 
 
 # ---- entry points --------------------------------------------------------------
@@ -191,7 +203,8 @@ def nvfp4_page_keys(k_packed: torch.Tensor, k_scales: torch.Tensor, block_table:
 
 def nvfp4_select_pages(q: torch.Tensor, keys: torch.Tensor, exponents: torch.Tensor, block_table: torch.Tensor,
                        seq_lens: torch.Tensor, query_offsets: torch.Tensor, *, page_size: int, top_k: int, first: int = 1,
-                       local: int = 2, pages: torch.Tensor | None = None, stream=None):
+                       local: int = 2, pages: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
     """The pages that each token of q BF16 [tokens, heads, head_dim] attends to, for
     each key/value head: the first `first` pages of its request, the last `local`
     up to its own, and the top_k others with the largest score by the page keys
@@ -211,6 +224,7 @@ def nvfp4_select_pages(q: torch.Tensor, keys: torch.Tensor, exponents: torch.Ten
         _fits(v, name, 32)
     n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device)
     shape = (tokens, kv, max(first, 0) + max(top_k, 0) + max(local, 0))
+    need = _select_workspace(tokens, heads, kv, n, width)
 
     def launch(st):
         out = pages
@@ -219,17 +233,13 @@ def nvfp4_select_pages(q: torch.Tensor, keys: torch.Tensor, exponents: torch.Ten
             out = _empty(shape if shape[2] <= 2048 else (0,), dtype=_I32, device=device)
         else:
             _b._out(out, shape, _I32, device, "pages")
+        work, wp, size = _workspace(workspace, need, device)
         _check(_lib().nvfp4_select_pages(q.data_ptr(), tokens, ld_q, heads, kv, dim, keys.data_ptr(), exponents.data_ptr(),
                                          count * page_size, page_size, table, ld, width, lens, offsets, n, top_k, first,
-                                         local, out.data_ptr(), st), "nvfp4_select_pages")
+                                         local, out.data_ptr(), wp, size, st), "nvfp4_select_pages")
         return out
 
     return _run(launch, device, stream)
-
-
-@functools.lru_cache(maxsize=256)
-def _sparse_workspace(*sizes):
-    return _lib().nvfp4_sparse_attention_workspace(*sizes)
 
 
 def nvfp4_sparse_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, v_packed: torch.Tensor,

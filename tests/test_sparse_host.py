@@ -98,25 +98,37 @@ def test_page_keys_validation(lib):
 
 
 def select(lib, q=A, tokens=4, ld_q=1024, heads=8, kv=2, dim=128, keys=A, e=A, ns=160, page=16, table=A, ld=8, mp=8, lens=A, off=A,
-           n=2, top=4, first=1, local=2, pages=A):
+           n=2, top=4, first=1, local=2, pages=A, ws=A, wb=2 ** 40):
     return lib.nvfp4_select_pages(q, tokens, ld_q, heads, kv, dim, keys, e, ns, page, table, ld, mp, lens, off, n, top, first, local,
-                                  pages, None)
+                                  pages, ws, wb, None)
 
 
 def test_select_validation(lib):
     for bad in (dict(tokens=-1), dict(heads=0), dict(heads=7), dict(kv=0), dict(top=-1), dict(first=-1), dict(local=0), dict(ld_q=1016),
                 dict(ld_q=2 ** 62), dict(ns=-16), dict(ns=161), dict(page=0), dict(mp=-1), dict(ld=7), dict(n=-1), dict(q=None),
-                dict(keys=None), dict(e=None), dict(table=None), dict(lens=None), dict(off=None), dict(pages=None)):
+                dict(keys=None), dict(e=None), dict(table=None), dict(lens=None), dict(off=None), dict(pages=None), dict(wb=-1),
+                dict(wb=0), dict(ws=None)):
         assert select(lib, **bad) == INVALID, bad
     for bad in (dict(dim=96, ld_q=2048), dict(heads=2048, ld_q=2 ** 19), dict(n=65536), dict(tokens=2 ** 28), dict(ns=2 ** 31),
                 dict(mp=32769, ld=2 ** 16), dict(mp=2 ** 14, ld=2 ** 16, page=2 ** 17, ns=2 ** 18), dict(top=2046),
                 dict(first=2043), dict(local=2044), dict(top=2 ** 31 - 1), dict(top=2 ** 31 - 1, first=2 ** 31 - 1, local=2 ** 31 - 1)):
         assert select(lib, **bad) == SHAPE, bad
     for bad in (dict(q=A + 8), dict(keys=A + 8), dict(ld_q=1028), dict(table=A + 2), dict(lens=A + 2), dict(off=A + 2),
-                dict(pages=A + 2)):
+                dict(pages=A + 2), dict(ws=A + 8)):
         assert select(lib, **bad) == MISALIGNED, bad
     for empty in (dict(tokens=0), dict(n=0)):
         assert select(lib, **empty) == OK
+
+
+def test_select_workspace(lib):
+    """Scores of all pages for few tokens; none for many, and where they would be large."""
+    size = lib.nvfp4_select_pages_workspace
+    assert size(1, 32, 8, 1, 2049) == 8 * 2052 * 4 and size(64, 64, 8, 64, 1024) == 64 * 8 * 1024 * 4
+    assert size(4096, 32, 8, 1, 500) == 0 and size(4096, 32, 8, 4096, 500) == 0 and size(0, 8, 8, 0, 9) == 0
+    assert size(5, 8, 2, 2, 30) == 5 * 2 * 32 * 4 and size(600, 4, 4, 1, 32768) == 0
+    for bad in ((-1, 8, 8, 1, 4), (1, 8, 3, 1, 4), (1, 8, 8, -1, 4), (1, 8, 8, 1, -4), (1, 8, 8, 1, 32769), (1, 2048, 8, 1, 4),
+                (1, 8, 8, 65536, 4), (2 ** 21, 8, 8, 1, 4)):
+        assert size(*bad) == -1, bad
 
 
 def sparse(lib, q=A, tokens=4, ld_q=1024, heads=8, kv=2, dim=128, kp=A, ks=A, vp=A, vs=A, ns=160, page=16, table=A, ld=8, mp=8, lens=A,
