@@ -2,6 +2,7 @@
 #include "fp4_operand.hpp"
 #include "nvfp4_device.hpp"
 #include "serving_common.hpp"
+#include "sparse_common.hpp"
 #include "nvfp4_sparse.h"
 
 namespace {
@@ -140,18 +141,6 @@ struct Select {
 constexpr int kMostRows = 64;      // query rows that are compared at once
 
 typedef int int4v __attribute__((ext_vector_type(4)));
-
-// The request of token t, -1 if it is none's: the last b with offsets[b] <= t.
-__device__ __forceinline__ int request_of(const Requests& r, int t)
-{
-    const int lane = threadIdx.x & 63;
-    int b = -1;
-    for (int base = 0; base <= r.num_seqs; base += 64) {
-        const int i = base + lane;
-        b += __popcll(__ballot(i <= r.num_seqs && r.offsets[min(i, r.num_seqs)] <= t));
-    }
-    return b >= r.num_seqs ? -1 : b;
-}
 
 // FP32 as whole numbers in the same order.
 __device__ __forceinline__ uint32_t ordered(float v)
@@ -394,22 +383,24 @@ __device__ __forceinline__ void quantize_queries(Queries<D>& q8, const uint16_t*
 template <int D>
 struct PageTile {
     int4v key[D / 64];
-    int exponent;        // -1: not a page to be chosen
+    int exponent;
+    bool in;             // a page to be chosen
 };
 
-// entry: this lane's page in the cache, any other number for none.
-template <int D>
-__device__ __forceinline__ void load_pages(PageTile<D>& t, const Select& a, int entry, int h)
+// Loads the tiles of the pages entry[u] (this lane's of each; any number that is none
+// reads the cache's first, which must exist). Nothing waits for a load here.
+template <int D, int N>
+__device__ __forceinline__ void load_pages(PageTile<D> (&t)[N], const Select& a, const int (&entry)[N], int h)
 {
     const int g = (threadIdx.x & 63) >> 4;
-    const bool in = entry >= 0 && entry < a.r.num_pages;
-    const int64_t at = (int64_t)(in ? entry : 0) * a.kv_heads + h;
-    t.exponent = -1;
-    if (in) {
-        t.exponent = min(max((int)a.exponents[at], 0), 64);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        t[u].in = entry[u] >= 0 && entry[u] < a.r.num_pages;
+        const int64_t at = (int64_t)(t[u].in ? entry[u] : 0) * a.kv_heads + h;
+        t[u].exponent = a.exponents[at];
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
-            t.key[k] = *(const int4v*)(a.keys + at * D + 64 * k + 16 * g);
+            t[u].key[k] = *(const int4v*)(a.keys + at * D + 64 * k + 16 * g);
     }
 }
 
@@ -422,7 +413,7 @@ __device__ __forceinline__ void compare(const PageTile<D>& t, const Queries<D>& 
     const int parts = (heads + 15) / 16;
     auto score = [&](int of, int v) {
         if (of < run)
-            put(of, t.exponent < 0 ? -INFINITY : ldexpf((float)v, t.exponent));
+            put(of, t.in ? ldexpf((float)v, min(max(t.exponent, 0), 64)) : -INFINITY);
     };
     // row tiles: several tokens each, or several for a token
 #pragma unroll 1
@@ -537,7 +528,7 @@ __device__ __forceinline__ void clear(SelectShared<W>& lds)
 }
 
 template <int D>
-__global__ __launch_bounds__(256) void select_chunk_kernel(Select a)
+__global__ __launch_bounds__(256, 4) void select_chunk_kernel(Select a)
 {
     constexpr int W = 4, kAhead = D > 128 ? 2 : 4;
     extern __shared__ __align__(16) float score[];        // [tokens][pitch]; -inf: not to be chosen
@@ -553,7 +544,7 @@ __global__ __launch_bounds__(256) void select_chunk_kernel(Select a)
     // the tokens of one request at a time
     for (int run = 1; token < token_end; token += run) {
         run = 1;
-        const int b = request_of(a.r, token);
+        const int b = sparse::request_of(a.r.offsets, a.r.num_seqs, token);
         if (b < 0)
             continue;
         const Place r = place_of(a.r, b);
@@ -581,11 +572,13 @@ __global__ __launch_bounds__(256) void select_chunk_kernel(Select a)
 #pragma unroll 1
             for (int j0 = a.first + 16 * wave; j0 < before; j0 += 16 * W * kAhead) {
                 PageTile<D> tile[kAhead];
+                int entry[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    const int j = j0 + 16 * W * u + n;
-                    load_pages(tile[u], a, j >= before ? -1 : h0 ? r.table[j] : __float_as_int(score[j]), h);
+                    const int j = min(j0 + 16 * W * u + n, before - 1);
+                    entry[u] = h0 ? r.table[j] : __float_as_int(score[j]);
                 }
+                load_pages(tile, a, entry, h);
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int j = j0 + 16 * W * u + n;
@@ -609,34 +602,39 @@ __global__ __launch_bounds__(256) void select_chunk_kernel(Select a)
     }
 }
 
-constexpr int kPagesOfScores = 256;      // of a workgroup of score_pages_kernel
+constexpr int kPagesOfScores = 256;      // that a workgroup of score_pages_kernel takes at a time
 
 template <int D>
-__global__ __launch_bounds__(256) void score_pages_kernel(Select a)
+__global__ __launch_bounds__(256, 4) void score_pages_kernel(Select a)
 {
     constexpr int W = 4, kTiles = kPagesOfScores / 16 / W;
     __shared__ __align__(16) Queries<D> q8;
     const int n = threadIdx.x & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = a.heads / a.kv_heads, bits = bits_of(group);
     const int h = blockIdx.x % a.kv_heads, chunk = blockIdx.x / a.kv_heads % a.chunks;
-    const int first = a.first + chunk * kPagesOfScores + 16 * wave;
     int token = blockIdx.x / a.kv_heads / a.chunks * a.together;
     const int token_end = min(token + a.together, a.tokens);
 #pragma unroll 1
     for (int run = 1; token < token_end; token += run) {
         run = 1;
-        const int b = request_of(a.r, token);
+        const int b = sparse::request_of(a.r.offsets, a.r.num_seqs, token);
         if (b < 0)
             continue;
         const Place r = place_of(a.r, b);
         run = min(token_end, r.behind) - token;
         const int before = scored_before(a, min(r.len - r.behind + token + run, r.len) - 1);
-        if (first - 16 * wave >= before)
+        const int begin = a.first + chunk * kPagesOfScores + 16 * wave;
+        if (begin - 16 * wave >= before)
             continue;
-        PageTile<D> tile[kTiles];
+        // table entries and queries are on their way together; a wait for the queries
+        // behind the keys would be one for the keys
+        auto entries = [&](int first, int (&entry)[kTiles]) {
 #pragma unroll
-        for (int u = 0; u < kTiles; ++u)
-            load_pages(tile[u], a, first + 16 * W * u + n < before ? r.table[first + 16 * W * u + n] : -1, h);
+            for (int u = 0; u < kTiles; ++u)
+                entry[u] = r.table[min(first + 16 * W * u + n, before - 1)];
+        };
+        int entry[kTiles];
+        entries(begin, entry);
         const uint16_t* q = a.q + token * a.ld_q + h * group * D;
         float* score = a.scores + ((int64_t)token * a.kv_heads + h) * a.pitch;
 #pragma unroll 1
@@ -644,16 +642,24 @@ __global__ __launch_bounds__(256) void score_pages_kernel(Select a)
             const int heads = min(group - h0, kMostRows);
             __syncthreads();                              // the queries of before are read
             quantize_queries<D, W>(q8, q, a.ld_q, group, h0, heads, run);
-            __syncthreads();
+#pragma unroll 1
+            for (int first = begin; first - 16 * wave < before; first += a.chunks * kPagesOfScores) {
+                if (first != begin || h0)
+                    entries(first, entry);
+                PageTile<D> tile[kTiles];
+                load_pages(tile, a, entry, h);
+                if (first == begin)
+                    __syncthreads();
 #pragma unroll
-            for (int u = 0; u < kTiles; ++u) {
-                const int j = first + 16 * W * u + n;
-                if (j - n < before)
-                    compare<D>(tile[u], q8, heads, bits, run, [&](int of, float v) {
-                        float* at = score + (int64_t)of * a.kv_heads * a.pitch + j;
-                        if (j < before)
-                            *at = h0 ? fmaxf(*at, v) : v;
-                    });
+                for (int u = 0; u < kTiles; ++u) {
+                    const int j = first + 16 * W * u + n;
+                    if (j - n < before)
+                        compare<D>(tile[u], q8, heads, bits, run, [&](int of, float v) {
+                            float* at = score + (int64_t)of * a.kv_heads * a.pitch + j;
+                            if (j < before)
+                                *at = h0 ? fmaxf(*at, v) : v;
+                        });
+                }
             }
         }
     }
@@ -665,7 +671,7 @@ __global__ __launch_bounds__(64 * W) void list_pages_kernel(Select a)
     extern __shared__ __align__(16) float score[];
     __shared__ __align__(16) SelectShared<W> lds;
     const int token = blockIdx.x / a.kv_heads;
-    const int b = request_of(a.r, token);
+    const int b = sparse::request_of(a.r.offsets, a.r.num_seqs, token);
     if (b < 0)
         return;
     const Place r = place_of(a.r, b);
@@ -690,14 +696,20 @@ SelectPlan select_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t 
 {
     SelectPlan p = {1, 0, ((int)max_pages + 3) & ~3, 0};
     // Tokens of long chunks go to a workgroup together, as many as 64 query rows and
-    // 64 KB of scores hold, at most 16.
+    // 16 KB of scores hold, at most 16: four workgroups a compute unit (2048 tokens of
+    // 500 pages: 54 us, with 64 KB 71).
     const int group = heads / kv_heads;
     while (p.together < 16 && p.together < tokens / (num_seqs < 1 ? 1 : num_seqs) &&
-           (p.together + 1) * group <= kMostRows && (int64_t)(p.together + 1) * p.pitch * 4 <= 65536)
+           (p.together + 1) * group <= kMostRows && (int64_t)(p.together + 1) * p.pitch * 4 <= 16384)
         ++p.together;
+    // Workgroups for 256 pages at a time, as many as the card holds at once (1024):
+    // those of short requests have nothing to do but start (64 requests of up to 1024
+    // pages: 2560 of them 16 us, 1024 TIME us).
     const int64_t bytes = tokens * kv_heads * p.pitch * 4;
-    if (serving::ceil_div(tokens, (int64_t)p.together) * kv_heads <= 768 && bytes <= 1 << 28) {
-        p.chunks = serving::ceil_div(p.pitch, kPagesOfScores);
+    const int64_t items = serving::ceil_div(tokens, (int64_t)p.together) * kv_heads;
+    if (items <= 768 && bytes <= 1 << 28) {
+        const int64_t most = serving::ceil_div(p.pitch, kPagesOfScores), fit = items < 1 ? 1 : 1024 / items;
+        p.chunks = (int)(fit < 1 ? 1 : fit < most ? fit : most);
         p.workspace = bytes;
     }
     return p;
@@ -714,7 +726,7 @@ void launch_select(const Select& a, hipStream_t stream)
     }
     const unsigned lists = (unsigned)(a.tokens * a.kv_heads);
     hipLaunchKernelGGL((score_pages_kernel<D>), dim3(items * a.chunks), dim3(256), 0, stream, a);
-    if (a.pitch <= 2048)
+    if (a.pitch <= 4096)
         hipLaunchKernelGGL((list_pages_kernel<4>), dim3(lists), dim3(256), a.pitch * 4, stream, a);
     else
         hipLaunchKernelGGL((list_pages_kernel<16>), dim3(lists), dim3(1024), a.pitch * 4, stream, a);
@@ -817,6 +829,10 @@ extern "C" nvfp4_status_t nvfp4_select_pages(const uint16_t* q, int64_t tokens, 
         return NVFP4_ERROR_MISALIGNED;
     if (workspace_bytes < p.workspace || (p.workspace > 0 && !workspace))
         return NVFP4_ERROR_INVALID_VALUE;
+    // A lane without a page reads the cache's first; without a cache it reads q, which is
+    // as long as a page's keys, and does not use it.
+    if (num_slots == 0)
+        keys = exponents = (const int8_t*)q;
     const Select a = {q, keys, exponents, pages, (float*)workspace,
                       {block_table, seq_lens, query_offsets, ld_table, (int)(num_slots / page_size), (int)max_pages,
                        page_size, (int)num_seqs},

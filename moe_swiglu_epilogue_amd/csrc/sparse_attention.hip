@@ -9,6 +9,7 @@
 // row sees of a tile is a word of bits made from the page's bits and the row's
 // position. A page that several tokens list is loaded and converted once.
 #include "attention_rows.hpp"
+#include "sparse_common.hpp"
 #include "nvfp4_sparse.h"
 
 namespace {
@@ -21,17 +22,6 @@ struct Sparse {
     int list_len;
     int together;      // tokens that a workgroup takes
 };
-
-// The request of token t, -1 if it is none's: the last b with offsets[b] <= t.
-__device__ __forceinline__ int request_of(const Attn& a, int t, int lane)
-{
-    int b = -1;
-    for (int base = 0; base <= a.num_seqs; base += 64) {
-        const int i = base + lane;
-        b += __popcll(__ballot(i <= a.num_seqs && a.offsets[min(i, a.num_seqs)] <= t));
-    }
-    return b >= a.num_seqs ? -1 : b;
-}
 
 // The listed pages that some token sees: the page in the cache, the position of its
 // first token in the request, and a bit for each token that listed it. While the
@@ -177,7 +167,7 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
     // the tokens of one request at a time
     for (int run = 1; token < token_end; token += run) {
         run = 1;
-        const int b = request_of(a, token, lane);
+        const int b = sparse::request_of(a.offsets, a.num_seqs, token);
         if (b < 0)
             continue;
         const int behind = a.offsets[b + 1];
