@@ -1,15 +1,18 @@
 // Rotation of q and k, and the write of k and v into the paged NVFP4 cache
 // (include/nvfp4_sparse.h).
 //
-// A workgroup takes a token. Its first threads look up the token's angles, a
-// cosine and sine for each pair, and put them into LDS; then every thread owns
-// 8 dimensions, the same for every head that it takes, keeps their cosines and
-// signed sines in registers and walks over the heads of q, k and v:
-//   out[d] = x[d] c[d] + x[partner of d] s[d],
+// A workgroup takes some tokens. Its threads look up their angles, a cosine and sine
+// for each pair, and put them into LDS; then every thread owns 8 or 16 dimensions
+// and walks over the tokens and their heads of q, k and v:
+//   out[d] = x[d] c[d] + x[partner of d] s[d]     (s: the sine with its sign),
 // a product, a product and a sum in binary32, each rounded, as the definition
-// has them. A block of 16 values of k or v is two
-// neighbouring lanes', which exchange their largest magnitudes and quantize
-// eight values each.
+// has them. A block of 16 values of k or v is two neighbouring lanes', which
+// exchange their largest magnitudes and quantize eight values each.
+//
+// Bound by memory traffic for long prompts, which needs many loads on their way: the
+// rows of several heads are requested at once, the first of them in front of the
+// angles. Every value is read once and q is written once, so both pass the caches
+// by (non-temporal).
 #include "nvfp4_device.hpp"
 #include "serving_common.hpp"
 #include "nvfp4_sparse.h"
@@ -17,7 +20,7 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostPairs = 256;
+constexpr int kMostPairs = 256, kMostTokens = 4;
 
 typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
@@ -30,13 +33,15 @@ struct Append {
     const int64_t* slots;
     uint8_t *kp, *ks, *vp, *vs;
     int64_t ld_q, ld_k, ld_v, ld_out, ld_positions, num_slots;
-    int tokens, heads, kv_heads, dim, rot, axes, max_position, parts;
+    int tokens, heads, kv_heads, dim, rot, axes, max_position;
+    int together, parts;       // tokens of a workgroup, or workgroups of a token
 };
 
-// How pairs lie: (j, j + rot / 2) with rot / 2 a multiple of 8, so that the
-// partners of a thread's 8 dimensions are 8 in a row too; the same with any
-// rot; (2 j, 2 j + 1).
-enum Pairs { kHalves8, kHalves, kNeighbours };
+// How pairs lie: (j, j + rot / 2), with rot = dim a multiple of 32, so that a thread
+// takes 8 dimensions and their 8 partners; with rot / 2 a multiple of 8, so that the
+// partners of a thread's 8 dimensions are 8 in a row too, which it reads as well; with
+// any rot; (2 j, 2 j + 1).
+enum Pairs { kWhole, kHalves8, kHalves, kNeighbours };
 
 __device__ __forceinline__ void widen(uint4v w, float (&x)[8])
 {
@@ -86,92 +91,197 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// What a thread loads of a head: its 8 dimensions, and for pairs in halves their
+// partners.
+template <Pairs kPairs>
+struct Row {
+    static constexpr int kWords = kPairs == kNeighbours || kPairs == kHalves ? 1 : 2;
+    uint4v w[kWords];
+};
+
+// The heads of a token, q's, k's and v's one after the other; -1 behind them and
+// where k and v are not to be written.
+__device__ __forceinline__ const uint16_t* head_of(const Append& a, int64_t t, int unit)
+{
+    return unit < a.heads ? a.q + t * a.ld_q + unit * a.dim
+           : unit < a.heads + a.kv_heads ? a.k + t * a.ld_k + (unit - a.heads) * a.dim
+                                         : a.v + t * a.ld_v + (unit - a.heads - a.kv_heads) * a.dim;
+}
+
+// partner: where the 8 partners begin, less than 0 where there are none.
+template <Pairs kPairs>
+__device__ __forceinline__ void load_row(Row<kPairs>& r, const uint16_t* head, int d0, int partner)
+{
+    r.w[0] = __builtin_nontemporal_load((const uint4v*)(head + d0));
+    if (kPairs == kWhole)
+        r.w[Row<kPairs>::kWords - 1] = __builtin_nontemporal_load((const uint4v*)(head + partner));
+    if (kPairs == kHalves8 && partner >= 0)
+        r.w[Row<kPairs>::kWords - 1] = *(const uint4v*)(head + partner);
+}
+
+// The angles of a thread's 8 dimensions, a bit for each that turns.
+struct Angles {
+    float c[8], s[8];
+    uint32_t turn;
+};
+
+struct Turns {
+    __align__(16) float c[kMostTokens * kMostPairs], s[kMostTokens * kMostPairs];
+    __align__(16) uint8_t in[kMostTokens * kMostPairs];
+    int64_t slot[kMostTokens];
+};
+
+// From the pairs' angles of a token, which begin at `at`.
+template <Pairs kPairs>
+__device__ __forceinline__ Angles angles_of(const Turns& lds, int at, int d0, int half, int rot)
+{
+    Angles g;
+    g.turn = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int d = d0 + i;
+        const bool second = kPairs == kNeighbours ? i & 1 : kPairs != kWhole && d >= half;
+        const int j = at + (kPairs == kNeighbours ? d >> 1 : second ? d - half : d);
+        const bool inside = kPairs == kWhole || d < rot;
+        const float s = inside ? lds.s[j] : 0.0f;
+        g.c[i] = inside ? lds.c[j] : 1.0f;
+        g.s[i] = second ? s : -s;
+        g.turn |= inside && lds.in[j] ? 1u << i : 0;
+    }
+    return g;
+}
+
+struct Scales {
+    nvfp4::RowScale k, v;
+};
+
+__device__ __forceinline__ void write_row(const Append& a, const Scales& scales, int64_t t, int64_t slot, int unit, int d,
+                                          const float (&z)[8])
+{
+    if (unit < a.heads) {
+        __builtin_nontemporal_store(
+            uint4v{bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])},
+            (uint4v*)(a.q_out + t * a.ld_out + unit * a.dim + d));
+        return;
+    }
+    const bool is_v = unit >= a.heads + a.kv_heads;
+    const int h = unit - a.heads - (is_v ? a.kv_heads : 0);
+    uint32_t sf;
+    const nvfp4::RowScale rs = {is_v ? scales.v.gs : scales.k.gs, is_v ? scales.v.k : scales.k.k,
+                                is_v ? scales.v.rk : scales.k.rk, is_v ? scales.v.pow2 : scales.k.pow2};
+    const uint32_t codes = quantize8(z, rs, sf);
+    const int64_t at = (slot * a.kv_heads + h) * (a.dim / 16);
+    *(uint32_t*)((is_v ? a.vp : a.kp) + at * 8 + d / 2) = codes;
+    if ((d & 8) == 0)
+        (is_v ? a.vs : a.ks)[at + d / 16] = (uint8_t)sf;
+}
+
+template <Pairs kPairs>
+__device__ __forceinline__ void turn_row(const Append& a, const Scales& scales, const Angles& g, const Row<kPairs>& r,
+                                         int64_t t, int64_t slot, int unit, int d0, int half)
+{
+    float y[8], x[8];                                     // its dimensions and their partners
+    widen(r.w[0], y);
+    if (unit < a.heads + a.kv_heads && g.turn != 0) {
+        if (kPairs == kWhole || kPairs == kHalves8) {
+            widen(r.w[Row<kPairs>::kWords - 1], x);
+        } else if (kPairs == kNeighbours) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = y[i ^ 1];
+        } else {
+            const uint16_t* head = head_of(a, t, unit);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int d = d0 + i, at = d < half ? d + half : d < a.rot ? d - half : d;
+                x[i] = __uint_as_float((uint32_t)head[at] << 16);
+            }
+        }
+        const bool all = g.turn == 255;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float z = y[i] * g.c[i] + x[i] * g.s[i], o = x[i] * g.c[i] + y[i] * -g.s[i];
+            x[i] = all || g.turn >> i & 1 ? o : x[i];
+            y[i] = all || g.turn >> i & 1 ? z : y[i];
+        }
+    } else if (kPairs == kWhole) {
+        widen(r.w[Row<kPairs>::kWords - 1], x);
+    }
+    write_row(a, scales, t, slot, unit, d0, y);
+    if (kPairs == kWhole)
+        write_row(a, scales, t, slot, unit, d0 + half, x);
+}
+
 template <Pairs kPairs>
 __global__ __launch_bounds__(kThreads) void rope_append_kernel(Append a)
 {
-    __shared__ float cosines[kMostPairs], sines[kMostPairs];
-    __shared__ bool turns[kMostPairs];
+    constexpr int kAhead = 2;                             // heads that a thread has in flight
+    __shared__ Turns lds;
     const int half = a.rot / 2;
-    const int per_head = a.dim / 8;                 // threads of a head, at most 64
-    const int at_once = kThreads / per_head;        // heads that the workgroup takes at once
+    const int per_head = a.dim / (kPairs == kWhole ? 16 : 8);     // threads of a head, at most 64
+    const int at_once = kThreads / per_head;              // heads that the workgroup takes at once
     const int d0 = threadIdx.x % per_head * 8;
     const int mine = threadIdx.x / per_head;
-    const int part = blockIdx.x % a.parts;
-    const int units = a.heads + 2 * a.kv_heads;
-    const nvfp4::RowScale k_scale = nvfp4::row_scale(a.k_gs ? a.k_gs[0] : 1.0f);
-    const nvfp4::RowScale v_scale = nvfp4::row_scale(a.v_gs ? a.v_gs[0] : 1.0f);
+    const int units = a.heads + 2 * a.kv_heads, step = a.parts * at_once;
+    const int partner = kPairs == kWhole || d0 < half ? d0 + half : d0 < a.rot ? d0 - half : -1;
+    const Scales scales = {nvfp4::row_scale(a.k_gs ? a.k_gs[0] : 1.0f), nvfp4::row_scale(a.v_gs ? a.v_gs[0] : 1.0f)};
 
-    for (int64_t t = blockIdx.x / a.parts; t < a.tokens; t += gridDim.x / a.parts) {
-        __syncthreads();
-        if ((int)threadIdx.x < half) {
-            const int j = threadIdx.x;
+    const int64_t groups = ((int64_t)a.tokens + a.together - 1) / a.together;
+    for (int64_t group = blockIdx.x / a.parts; group < groups; group += gridDim.x / a.parts) {
+        const int t0 = (int)group * a.together, n = min(a.together, a.tokens - t0);
+        // the heads of the n tokens one after the other, `step` at a time
+        struct At {
+            int token, unit;
+        };
+        auto next = [&](At x) {
+            x.unit += step;
+            while (x.unit >= units && x.token < n) {
+                x.unit -= units;
+                ++x.token;
+            }
+            return x;
+        };
+        At at[kAhead];
+        at[0] = next({0, (int)(blockIdx.x % a.parts) * at_once + mine - step});
+        if (mine >= at_once)
+            at[0].token = n;
+        Row<kPairs> row[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (u)
+                at[u] = next(at[u - 1]);
+            if (at[u].token < n)
+                load_row(row[u], head_of(a, t0 + at[u].token, at[u].unit), d0, partner);
+        }
+
+        __syncthreads();                                  // the angles of the tokens before are read
+        for (int i = threadIdx.x; i < n * half; i += kThreads) {
+            const int token = n == 1 ? 0 : i / half, j = i - token * half;
             const int axis = a.pair_axis ? a.pair_axis[j] : 0;
             const bool known = axis >= 0 && axis < a.axes;
-            const int p = known ? a.positions[axis * a.ld_positions + t] : -1;
+            const int p = known ? a.positions[axis * a.ld_positions + t0 + token] : -1;
             const bool in = p >= 0 && p < a.max_position;
-            turns[j] = in;
-            if (in) {
-                cosines[j] = a.cos_sin[(int64_t)p * a.rot + j];
-                sines[j] = a.cos_sin[(int64_t)p * a.rot + half + j];
-            }
+            lds.in[token * kMostPairs + j] = in;
+            lds.c[token * kMostPairs + j] = in ? a.cos_sin[(int64_t)p * a.rot + j] : 1.0f;
+            lds.s[token * kMostPairs + j] = in ? a.cos_sin[(int64_t)p * a.rot + half + j] : 0.0f;
         }
+        if ((int)threadIdx.x < n)
+            lds.slot[threadIdx.x] = a.slots[t0 + threadIdx.x];
         __syncthreads();
-        if (mine >= at_once)
-            continue;
-        float c[8], s[8];
-        bool turn[8];
+        while (at[0].token < n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = d0 + i;
-            const bool second = kPairs == kNeighbours ? i & 1 : d >= half;
-            const int j = kPairs == kNeighbours ? d >> 1 : second ? d - half : d;
-            turn[i] = d < a.rot && turns[j];
-            c[i] = turn[i] ? cosines[j] : 1.0f;
-            s[i] = turn[i] ? second ? sines[j] : -sines[j] : 0.0f;
-        }
-        const int64_t slot = a.slots[t];
-        const bool stored = slot >= 0 && slot < a.num_slots;
-        for (int unit = part * at_once + mine; unit < units; unit += a.parts * at_once) {
-            const bool is_q = unit < a.heads, is_v = unit >= a.heads + a.kv_heads;
-            const int h = is_q ? unit : is_v ? unit - a.heads - a.kv_heads : unit - a.heads;
-            if (!is_q && !stored)
-                continue;
-            const uint16_t* head = is_q ? a.q + t * a.ld_q : is_v ? a.v + t * a.ld_v : a.k + t * a.ld_k;
-            head += h * a.dim;
-            float y[8];
-            const uint4v w = *(const uint4v*)(head + d0);
-            widen(w, y);
-            if (!is_v) {
-                float x[8];
-                if (kPairs == kNeighbours) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = y[i ^ 1];
-                } else if (kPairs == kHalves8) {
-                    const int at = d0 < half ? d0 + half : d0 < a.rot ? d0 - half : d0;
-                    widen(*(const uint4v*)(head + at), x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int d = d0 + i;
-                        const int at = d < half ? d + half : d < a.rot ? d - half : d;
-                        x[i] = __uint_as_float((uint32_t)head[at] << 16);
-                    }
+            for (int u = 0; u < kAhead; ++u)
+                if (at[u].token < n) {
+                    const int64_t slot = lds.slot[at[u].token];
+                    if (at[u].unit < a.heads || (slot >= 0 && slot < a.num_slots))
+                        turn_row<kPairs>(a, scales, angles_of<kPairs>(lds, at[u].token * kMostPairs, d0, half, a.rot), row[u],
+                                         t0 + at[u].token, slot, at[u].unit, d0, half);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = turn[i] ? y[i] * c[i] + x[i] * s[i] : y[i];
-            }
-            if (is_q) {
-                *(uint4v*)(a.q_out + t * a.ld_out + h * a.dim + d0) =
-                    uint4v{bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7])};
-            } else {
-                uint32_t sf;
-                const uint32_t codes = quantize8(y, is_v ? v_scale : k_scale, sf);
-                const int64_t at = slot * a.kv_heads * (a.dim / 16) + h * (a.dim / 16);
-                *(uint32_t*)((is_v ? a.vp : a.kp) + at * 8 + d0 / 2) = codes;
-                if ((d0 & 8) == 0)
-                    (is_v ? a.vs : a.ks)[at + d0 / 16] = (uint8_t)sf;
+            for (int u = 0; u < kAhead; ++u) {
+                at[u] = next(u ? at[u - 1] : at[kAhead - 1]);
+                if (at[u].token < n)
+                    load_row(row[u], head_of(a, t0 + at[u].token, at[u].unit), d0, partner);
             }
         }
     }
@@ -222,20 +332,30 @@ extern "C" nvfp4_status_t nvfp4_rope_append(
         return NVFP4_ERROR_INVALID_VALUE;
     Append a = {q, k, v, q_out, positions, pair_axis, cos_sin, k_gs, v_gs, slots, k_packed, k_scales,
                 v_packed, v_scales, q ? ld_q : 0, ld_k, ld_v, q ? ld_out : 0, num_axes > 1 ? ld_positions : 0,
-                num_slots, (int)tokens, heads, kv_heads, head_dim, rot_dim, num_axes, (int)max_position, 1};
-    // Few tokens: the heads of one are split over workgroups, each of which takes
-    // its share at once.
-    const int at_once = kThreads / (head_dim / 8), all = ceil_div(heads + 2 * kv_heads, at_once);
+                num_slots, (int)tokens, heads, kv_heads, head_dim, rot_dim, num_axes, (int)max_position, 1, 1};
+    const Pairs pairs = interleaved ? kNeighbours : rot_dim == head_dim && rot_dim % 32 == 0 ? kWhole
+                        : rot_dim % 16 == 0 ? kHalves8 : kHalves;
+    // Few tokens: the heads of one are split over workgroups, each of which takes its
+    // share at once. Many: a workgroup takes several tokens, until at most a tenth of its
+    // threads idle in the last round (5003 tokens of 36 heads, three axes: 25 us with
+    // one, 19 with four; 16384 of 80: 116 with one, 105 with two, 111 with four).
+    const int at_once = kThreads / (head_dim / (pairs == kWhole ? 16 : 8)), all = ceil_div(heads + 2 * kv_heads, at_once);
     if (tokens * all <= 4096)
         a.parts = all;
-    // workgroups beyond 2^22 loop over the tokens (a grid holds less than 2^32 threads)
-    const int64_t most = (1 << 22) / a.parts;
-    const dim3 grid((unsigned)((tokens < most ? tokens : most) * a.parts));
-    if (interleaved)
-        hipLaunchKernelGGL((rope_append_kernel<kNeighbours>), grid, dim3(kThreads), 0, stream, a);
-    else if (rot_dim % 16 == 0)
-        hipLaunchKernelGGL((rope_append_kernel<kHalves8>), grid, dim3(kThreads), 0, stream, a);
     else
+        while (a.together < kMostTokens && tokens / a.together >= 2048 &&
+               10 * a.together * (heads + 2 * kv_heads) < 9 * ceil_div(a.together * (heads + 2 * kv_heads), at_once) * at_once)
+            a.together *= 2;
+    // workgroups beyond 2^22 loop over the tokens (a grid holds less than 2^32 threads)
+    const int64_t groups = ceil_div(tokens, (int64_t)a.together), most = (1 << 22) / a.parts;
+    const dim3 grid((unsigned)((groups < most ? groups : most) * a.parts));
+    if (pairs == kWhole)
+        hipLaunchKernelGGL((rope_append_kernel<kWhole>), grid, dim3(kThreads), 0, stream, a);
+    else if (pairs == kHalves8)
+        hipLaunchKernelGGL((rope_append_kernel<kHalves8>), grid, dim3(kThreads), 0, stream, a);
+    else if (pairs == kHalves)
         hipLaunchKernelGGL((rope_append_kernel<kHalves>), grid, dim3(kThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL((rope_append_kernel<kNeighbours>), grid, dim3(kThreads), 0, stream, a);
     return launched();
 }

@@ -15,7 +15,7 @@ import torch
 
 from . import binding as _b
 from .serving import (_BF16, _F32, _I32, _I32_MAX, _I64, _U8, _all, _at_most, _check, _cuda, _current, _elsewhere, _empty,
-                      _fits, _heads, _new, _scalar, _table, _vector, _workspace)
+                      _heads, _scalar, _table, _vector, _workspace)
 
 EXPORTS = ("nvfp4_rope_append", "nvfp4_page_keys", "nvfp4_select_pages", "nvfp4_select_pages_workspace",
            "nvfp4_sparse_attention", "nvfp4_sparse_attention_workspace")
@@ -59,11 +59,52 @@ def _run(launch, device, stream):
         return launch(st)
 
 
-def _pages(page_size, rows):
-    if not 1 <= page_size <= _I32_MAX:
+# The checks of a call that passes, in as few steps as they take (a call of a few
+# microseconds looks at a dozen tensors); what does not pass goes to serving's checks,
+# which say what is wrong.
+def _rows(t, name, device, index):
+    """Pitch of the rows of [tokens, heads, head_dim]."""
+    if t.dtype is _BF16 and t.get_device() == index and t.dim() == 3:
+        n, h, d = t.shape
+        row, head, one = t.stride()
+        if head == d and one == 1:
+            if n <= 1:
+                return h * d
+            if row >= h * d:
+                return row
+    return _heads(t, name, device)
+
+
+def _line(t, name, dtype, device, index, n):
+    """Pointer of a contiguous vector of n values."""
+    if t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    return _vector(t, name, dtype, device, n)
+
+
+def _caches(tensors, names, device, index, codes, scales):
+    """Pointers of packed and scale caches in turn."""
+    for t, shape in zip(tensors, (codes, scales, codes, scales)):
+        if t.dtype is not _U8 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+            return _all(tensors, names, _U8, device, (codes, scales, codes, scales)[:len(tensors)])
+    return [t.data_ptr() for t in tensors]
+
+
+def _one(t, name, device, index):
+    """Pointer of a global scale, or None."""
+    if t is None:
+        return None
+    if t.dtype is _F32 and t.get_device() == index and t.numel() == 1:
+        return t.data_ptr()
+    return _scalar(t, name, _F32, device)
+
+
+def _page_size(v):
+    if not 1 <= v <= _I32_MAX:
         raise ValueError("page_size must be at least 1 and fit 32 bits")
-    if rows % page_size:
-        raise ValueError("the cache must hold whole pages")
+
+
+_CACHES = ("k_packed", "k_scales", "v_packed", "v_scales")
 
 
 @functools.lru_cache(maxsize=256)
@@ -95,54 +136,60 @@ def nvfp4_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     Returns the rotated q (BF16, like q; a new tensor, or q_out), or None without
     q."""
     device = _cuda(k, "k")
-    ld_k, ld_v = _heads(k, "k", device), _heads(v, "v", device)
-    tokens, kv, dim = k.shape
-    if v.shape != k.shape:
+    index = device.index
+    ld_k, ld_v = _rows(k, "k", device, index), _rows(v, "v", device, index)
+    shape = k.shape
+    tokens, kv, dim = shape
+    if v.shape != shape:
         raise ValueError("v must have k's shape")
     ld_q = heads = 0
     if q is not None:
-        ld_q = _heads(q, "q", device)
-        if q.shape[0] != tokens or q.shape[2] != dim:
+        ld_q = _rows(q, "q", device, index)
+        n, heads, d = q.shape
+        if n != tokens or d != dim:
             raise ValueError("q must be [tokens, heads, head_dim] with k's tokens and head_dim")
-        heads = q.shape[1]
         if heads < 1:
             raise ValueError("q must have at least one head")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if positions.dtype is not _I32 or positions.device != device or positions.dim() not in (1, 2):
+    axes = positions.dim()
+    if positions.dtype is not _I32 or positions.get_device() != index or not 1 <= axes <= 2:
         raise TypeError("positions must be an int32 tensor [tokens] or [axes, tokens] on the input's device")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.shape[-1] != tokens or axes < 1:
+    if axes == 2:
+        axes, n = positions.shape
+        ld_pos, step = positions.stride()
+    else:
+        n, ld_pos, step = positions.numel(), tokens, positions.stride(0)
+    if n != tokens or axes < 1:
         raise ValueError("positions must hold one value per token and axis")
-    if tokens > 1 and positions.stride(-1) != 1:
+    if tokens > 1 and step != 1:
         raise TypeError("positions must have unit token stride")
-    ld_pos = positions.stride(0) if axes > 1 else tokens
-    if ld_pos < tokens:
+    if axes == 1:
+        ld_pos = tokens
+    elif ld_pos < tokens:
         raise ValueError("positions' axes must not overlap")
-    if cos_sin.dtype is not _F32 or cos_sin.device != device or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+    if cos_sin.dtype is not _F32 or cos_sin.get_device() != index or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise TypeError("cos_sin must be a contiguous 2-D float32 tensor on the input's device")
     most, rot = cos_sin.shape
     if rot % 2 or rot > dim:
         raise ValueError("cos_sin must be [max_position, rot_dim] with rot_dim even, at most head_dim")
-    axis = None if pair_axis is None else _vector(pair_axis, "pair_axis", _I32, device, rot // 2)
-    slots = _vector(slot_mapping, "slot_mapping", _I64, device, tokens)
+    axis = None if pair_axis is None else _line(pair_axis, "pair_axis", _I32, device, index, rot // 2)
+    slots = _line(slot_mapping, "slot_mapping", _I64, device, index, tokens)
     if k_packed.dim() != 2:
         raise ValueError("k_packed must be [num_slots, kv_heads * head_dim / 2]")
     rows, cols = k_packed.shape[0], kv * dim
-    codes, scales = (rows, cols // 2), (rows, cols // 16)
-    kp, ks, vp, vs = _all((k_packed, k_scales, v_packed, v_scales), ("k_packed", "k_scales", "v_packed", "v_scales"), _U8,
-                          device, (codes, scales, codes, scales))
-    kg = _scalar(k_gs, "k_gs", _F32, device)
-    vg = _scalar(v_gs, "v_gs", _F32, device)
+    kp, ks, vp, vs = _caches((k_packed, k_scales, v_packed, v_scales), _CACHES, device, index, (rows, cols // 2),
+                             (rows, cols // 16))
+    kg, vg = _one(k_gs, "k_gs", device, index), _one(v_gs, "v_gs", device, index)
 
     def launch(st):
         out, op, ld_out = q_out, None, 0
         if q is not None:
             if out is None:
-                out = _empty((tokens, heads, dim), dtype=_BF16, device=device)
+                out = _empty(tokens, heads, dim, dtype=_BF16, device=device)
                 ld_out = heads * dim
             else:
-                ld_out = _heads(out, "q_out", device)
+                ld_out = _rows(out, "q_out", device, index)
                 if out.shape != q.shape:
                     raise ValueError("q_out must have q's shape")
             op = out.data_ptr()
@@ -156,19 +203,23 @@ def nvfp4_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     return _run(launch, device, stream)
 
 
-def _requests(block_table, seq_lens, query_offsets, device):
-    lens = _vector(seq_lens, "seq_lens", _I32, device)
+def _requests(block_table, seq_lens, query_offsets, device, index):
     n = seq_lens.numel()
-    offsets = _vector(query_offsets, "query_offsets", _I32, device, n + 1)
+    lens = _line(seq_lens, "seq_lens", _I32, device, index, n)
+    offsets = _line(query_offsets, "query_offsets", _I32, device, index, n + 1)
+    if block_table.dtype is _I32 and block_table.get_device() == index and block_table.dim() == 2 and block_table.is_contiguous():
+        rows, width = block_table.shape
+        if rows == n:
+            return n, block_table.data_ptr(), width, width, lens, offsets
     ld, width = _table(block_table, n, device)
     return n, block_table.data_ptr(), ld, width, lens, offsets
 
 
-def _page_keys(keys, exponents, device):
-    if keys.dtype is not _I8 or keys.device != device or keys.dim() != 3 or not keys.is_contiguous():
+def _page_keys(keys, exponents, index):
+    if keys.dtype is not _I8 or keys.get_device() != index or keys.dim() != 3 or not keys.is_contiguous():
         raise TypeError("keys must be a contiguous int8 tensor [pages, kv_heads, head_dim] on the input's device")
     pages, kv, dim = keys.shape
-    if exponents.dtype is not _I8 or exponents.device != device or not exponents.is_contiguous():
+    if exponents.dtype is not _I8 or exponents.get_device() != index or not exponents.is_contiguous():
         raise TypeError("exponents must be a contiguous int8 tensor on the input's device")
     if exponents.shape != (pages, kv):
         raise ValueError("exponents must be [pages, kv_heads]")
@@ -184,13 +235,12 @@ def nvfp4_page_keys(k_packed: torch.Tensor, k_scales: torch.Tensor, block_table:
     kv_heads], in place; other pages' keys keep their values. max_query_len, the
     most new tokens of a request, steers the speed only. Returns (keys, exponents)."""
     device = _cuda(k_packed, "k_packed")
-    pages, kv, dim = _page_keys(keys, exponents, device)
-    if not 1 <= page_size <= _I32_MAX:
-        raise ValueError("page_size must be at least 1 and fit 32 bits")
+    index = device.index
+    pages, kv, dim = _page_keys(keys, exponents, index)
+    _page_size(page_size)
     rows = pages * page_size
-    kp, ks = _all((k_packed, k_scales), ("k_packed", "k_scales"), _U8, device,
-                  ((rows, kv * dim // 2), (rows, kv * dim // 16)))
-    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device)
+    kp, ks = _caches((k_packed, k_scales), _CACHES, device, index, (rows, kv * dim // 2), (rows, kv * dim // 16))
+    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device, index)
     max_query_len = _at_most(max_query_len, "max_query_len")
 
     def launch(st):
@@ -213,26 +263,25 @@ def nvfp4_select_pages(q: torch.Tensor, keys: torch.Tensor, exponents: torch.Ten
     Rows of no request are left as they were (``pages`` allocated here holds
     nothing there)."""
     device = _cuda(q, "q")
-    ld_q = _heads(q, "q", device)
+    index = device.index
+    ld_q = _rows(q, "q", device, index)
     tokens, heads, dim = q.shape
-    count, kv, key_dim = _page_keys(keys, exponents, device)
+    count, kv, key_dim = _page_keys(keys, exponents, index)
     if key_dim != dim:
         raise ValueError("keys must have q's head_dim")
-    if not 1 <= page_size <= _I32_MAX:
-        raise ValueError("page_size must be at least 1 and fit 32 bits")
-    for v, name in ((top_k, "top_k"), (first, "first"), (local, "local")):
-        _fits(v, name, 32)
-    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device)
-    shape = (tokens, kv, max(first, 0) + max(top_k, 0) + max(local, 0))
+    _page_size(page_size)
+    listed = first + top_k + local
+    if first < 0 or top_k < 0 or local < 1 or listed > 2048:
+        raise ValueError("first and top_k must be at least 0, local at least 1, and their sum at most 2048")
+    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device, index)
     need = _select_workspace(tokens, heads, kv, n, width)
 
     def launch(st):
         out = pages
         if out is None:
-            # too long a list is refused below, before it is written
-            out = _empty(shape if shape[2] <= 2048 else (0,), dtype=_I32, device=device)
+            out = _empty(tokens, kv, listed, dtype=_I32, device=device)
         else:
-            _b._out(out, shape, _I32, device, "pages")
+            _b._out(out, (tokens, kv, listed), _I32, device, "pages")
         work, wp, size = _workspace(workspace, need, device)
         _check(_lib().nvfp4_select_pages(q.data_ptr(), tokens, ld_q, heads, kv, dim, keys.data_ptr(), exponents.data_ptr(),
                                          count * page_size, page_size, table, ld, width, lens, offsets, n, top_k, first,
@@ -256,23 +305,24 @@ def nvfp4_sparse_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: to
     q) and, with ``lse`` True or a tensor, also lse FP32 [tokens, heads]. Rows of
     no request are left as they were."""
     device = _cuda(q, "q")
-    ld_q = _heads(q, "q", device)
+    index = device.index
+    ld_q = _rows(q, "q", device, index)
     tokens, heads, dim = q.shape
-    if pages.dtype is not _I32 or pages.device != device or pages.dim() != 3 or not pages.is_contiguous():
+    if pages.dtype is not _I32 or pages.get_device() != index or pages.dim() != 3 or not pages.is_contiguous():
         raise TypeError("pages must be a contiguous int32 tensor [tokens, kv_heads, list_len] on the input's device")
-    if pages.shape[0] != tokens:
+    lists, kv, listed = pages.shape
+    if lists != tokens:
         raise ValueError("pages must have one list per token")
-    kv, listed = pages.shape[1], pages.shape[2]
     if k_packed.dim() != 2:
         raise ValueError("k_packed must be [num_slots, kv_heads * head_dim / 2]")
     rows, cols = k_packed.shape[0], kv * dim
-    codes, scales = (rows, cols // 2), (rows, cols // 16)
-    kp, ks, vp, vs = _all((k_packed, k_scales, v_packed, v_scales), ("k_packed", "k_scales", "v_packed", "v_scales"), _U8,
-                          device, (codes, scales, codes, scales))
-    _pages(page_size, rows)
-    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device)
-    kg = _scalar(k_gs, "k_gs", _F32, device)
-    vg = _scalar(v_gs, "v_gs", _F32, device)
+    kp, ks, vp, vs = _caches((k_packed, k_scales, v_packed, v_scales), _CACHES, device, index, (rows, cols // 2),
+                             (rows, cols // 16))
+    _page_size(page_size)
+    if rows % page_size:
+        raise ValueError("the cache must hold whole pages")
+    n, table, ld, width, lens, offsets = _requests(block_table, seq_lens, query_offsets, device, index)
+    kg, vg = _one(k_gs, "k_gs", device, index), _one(v_gs, "v_gs", device, index)
     if scale is None:
         scale = 1.0 / math.sqrt(dim) if dim else 1.0
     need = _sparse_workspace(tokens, heads, kv, dim, page_size, n, listed)
@@ -280,14 +330,15 @@ def nvfp4_sparse_attention(q: torch.Tensor, k_packed: torch.Tensor, k_scales: to
     def launch(st):
         o, z, zp = out, None, None
         if o is None:
-            o = _empty((tokens, heads, dim), dtype=_BF16, device=device)
+            o = _empty(tokens, heads, dim, dtype=_BF16, device=device)
             ld_out = heads * dim
         else:
-            ld_out = _heads(o, "out", device)
+            ld_out = _rows(o, "out", device, index)
             if o.shape != q.shape:
                 raise ValueError("out must have q's shape")
         if lse is not None and lse is not False:
-            z = _new(None if lse is True else lse, (tokens, heads), _F32, device, "lse")
+            z = (_empty(tokens, heads, dtype=_F32, device=device) if lse is True
+                 else _b._out(lse, (tokens, heads), _F32, device, "lse"))
             zp = z.data_ptr()
         work, wp, size = _workspace(workspace, need, device)
         _check(_lib().nvfp4_sparse_attention(q.data_ptr(), tokens, ld_q, heads, kv, dim, kp, ks, vp, vs, rows, page_size, table,
