@@ -25,9 +25,12 @@ __device__ __forceinline__ int length_of(const Requests& r, int b)
 
 // ---- page keys -----------------------------------------------------------------
 // A workgroup takes a page and up to 64 blocks of 16 dimensions (whole heads): a
-// thread owns a block and every so many of the page's tokens. A cache value
-// times 2^10 is a whole number below 2^21.4, so a sum of four of them is exact in
-// FP32; these go to binary64 sums, which are exact for pages up to 2^31 tokens.
+// thread owns a block and every so many of the page's tokens, 8 of which are on their
+// way at a time. A cache value times 2^10 is a whole number below 2^21.4, so a sum
+// of four of them is exact in FP32; these go to binary64 sums, which are exact for
+// pages up to 2^31 tokens. The threads' sums meet in LDS, where every thread adds
+// some up. Bound by memory latency: a workgroup's chain of loads (lengths, table,
+// tokens) and its start.
 struct PageKeys {
     const uint8_t *kp, *ks;
     int8_t *keys, *exponents;
@@ -35,13 +38,30 @@ struct PageKeys {
     int kv_heads, dim, per_request;
 };
 
+// sum[i] += scale * the i-th of 16 codes, exact where the sum is.
+__device__ __forceinline__ void add16(float (&sum)[16], uint2 w, float scale)
+{
+    auto pair = [&](int i, auto v) {
+        sum[i] = __builtin_fmaf(v[0], scale, sum[i]);
+        sum[i + 1] = __builtin_fmaf(v[1], scale, sum[i + 1]);
+    };
+    pair(0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 0));
+    pair(2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 1));
+    pair(4, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 2));
+    pair(6, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.x, 1.0f, 3));
+    pair(8, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.y, 1.0f, 0));
+    pair(10, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.y, 1.0f, 1));
+    pair(12, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.y, 1.0f, 2));
+    pair(14, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w.y, 1.0f, 3));
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 {
-    constexpr int kHeadBlocks = D / 16;
+    constexpr int kHeadBlocks = D / 16, kAhead = 8;
     __shared__ double sums[kThreads][17];
-    __shared__ double largest[64];
-    const int b = blockIdx.x / a.per_request;
+    // the requests' first pages first: workgroups that find none come last
+    const int b = blockIdx.x % a.r.num_seqs;
     const int blocks = a.kv_heads * kHeadBlocks;          // of 16 dimensions, of a token
     const int first_block = blockIdx.y * 64, here = min(blocks - first_block, 64);
     int width = kHeadBlocks;                              // threads over blocks: a power of two
@@ -52,63 +72,85 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
     const int n = max(a.r.offsets[b + 1] - a.r.offsets[b], 0);
     const int begin = max(len - n, 0) / a.r.page, end = len / a.r.page;
 
-    for (int j = begin + blockIdx.x % a.per_request; j < end; j += a.per_request) {
+    for (int j = begin + blockIdx.x / a.r.num_seqs; j < end; j += a.per_request) {
         const int entry = a.r.table[b * a.r.ld_table + j];
         if (entry < 0 || entry >= a.r.num_pages)
             continue;
         double total[16];
+#pragma unroll
         for (int i = 0; i < 16; ++i)
             total[i] = 0;
         if (block < here) {
             const int64_t at = (int64_t)entry * a.r.page * blocks + first_block + block;
-            for (int t0 = lane; t0 < a.r.page; t0 += 4 * lanes) {
-                float part[16];
-                for (int i = 0; i < 16; ++i)
-                    part[i] = 0;
+#pragma unroll 1
+            for (int t0 = lane; t0 < a.r.page; t0 += kAhead * lanes) {
+                // tokens behind the page: its last one, with a scale of 0
+                uint2 w[kAhead];
+                uint32_t sf[kAhead];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int t = t0 + u * lanes;
-                    if (t >= a.r.page)
-                        break;
-                    const uint2 w = *(const uint2*)(a.kp + (at + (int64_t)t * blocks) * 8);
-                    float x[16];
-                    nvfp4::dequantize16(w, a.ks[at + (int64_t)t * blocks], 1024.0f, x);
-                    for (int i = 0; i < 16; ++i)
-                        part[i] += x[i];
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t x = at + (int64_t)min(t0 + u * lanes, a.r.page - 1) * blocks;
+                    w[u] = *(const uint2*)(a.kp + x * 8);
+                    sf[u] = a.ks[x];
                 }
-                for (int i = 0; i < 16; ++i)
-                    total[i] += (double)part[i];
+#pragma unroll
+                for (int half = 0; half < kAhead; half += 4) {
+                    float part[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        part[i] = 0;
+#pragma unroll
+                    for (int u = half; u < half + 4; ++u)
+                        add16(part, w[u], t0 + u * lanes < a.r.page ? 1024.0f * nvfp4::fp8_e4m3_decode(sf[u]) : 0.0f);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        total[i] += (double)part[i];
+                }
             }
         }
         __syncthreads();                                  // the sums of the page before are read
+#pragma unroll
         for (int i = 0; i < 16; ++i)
             sums[threadIdx.x][i] = total[i];
         __syncthreads();
-        if (lane == 0 && block < here) {
-            for (int k = 1; k < lanes; ++k)
-                for (int i = 0; i < 16; ++i)
-                    total[i] += sums[k * width + block][i];
-            double top = 0;
-            for (int i = 0; i < 16; ++i)
-                top = fmax(top, fabs(total[i]));
-            largest[block] = top;
-        }
-        __syncthreads();
-        if (lane == 0 && block < here) {
-            double top = 0;
-            for (int i = 0; i < kHeadBlocks; ++i)
-                top = fmax(top, largest[block / kHeadBlocks * kHeadBlocks + i]);
-            // bits - 7; 2^bits > top >= 2^(bits - 1)
-            const int e = top < 128.0 ? 0 : ilogb(top) - 6;
-            uint4v w = {0, 0, 0, 0};
-            for (int i = 0; i < 16; ++i) {
-                const int key = min(max((int)rint(ldexp(total[i], -e)), -127), 127);
-                w[i >> 2] |= (uint32_t)(key & 255) << (8 * (i & 3));
+        // A thread adds up some dimensions of a block; those of a head are in a row of at
+        // most 64 threads and find their largest sum by exchanges.
+        const int parts = min(lanes, min(16, 64 / kHeadBlocks)), share = 16 / parts;     // threads of a block, dimensions
+        if ((int)threadIdx.x < width * parts) {
+            const int of = threadIdx.x / parts, d0 = threadIdx.x % parts * share;
+            double sum[4], top = 0;                       // share: 1, 2 or 4, as parts is 4, 8 or 16
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum[i] = 0;
+                if (i < share) {
+                    for (int k = 0; k < lanes; ++k)
+                        sum[i] += sums[k * width + of][d0 + i];
+                    top = fmax(top, fabs(sum[i]));
+                }
             }
-            const int64_t at = (int64_t)entry * blocks + first_block + block;
-            *(uint4v*)(a.keys + at * 16) = w;
-            if (block % kHeadBlocks == 0)
-                a.exponents[at / kHeadBlocks] = (int8_t)e;
+            for (int d = 1; d < kHeadBlocks * parts; d *= 2)
+                top = fmax(top, __shfl_xor(top, d));
+            // the length of a whole number in binary is its exponent and 1
+            const int bits = top < 1.0 ? 0 : (int)(__double_as_longlong(top) >> 52) - 1022;
+            const int e = max(bits - 7, 0);
+            const double scale = __longlong_as_double((int64_t)(1023 - e) << 52);       // 2^-e
+            if (of < here) {
+                const int64_t at = (int64_t)entry * blocks + first_block + of;
+                uint32_t w = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w |= (uint32_t)(min(max((int)rint(sum[i] * scale), -127), 127) & 255) << (8 * i);
+                int8_t* out = a.keys + at * 16 + d0;
+                if (share == 4) {
+                    *(uint32_t*)out = w;
+                } else {
+                    out[0] = (int8_t)w;
+                    if (share == 2)
+                        out[1] = (int8_t)(w >> 8);
+                }
+                if (of % kHeadBlocks == 0 && d0 == 0)
+                    a.exponents[at / kHeadBlocks] = (int8_t)e;
+            }
         }
     }
 }
