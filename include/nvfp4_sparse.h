@@ -80,7 +80,9 @@ nvfp4_status_t nvfp4_rope_append(const uint16_t *q, int64_t tokens, int64_t ld_q
  * (E2M1 code times E4M3 scale, without the global scale),
  *   S_d = sum over the page's tokens of 2^10 k_t[d]        (a whole number),
  *   e   = max(0, bits - 7), bits the length of max_d |S_d| in binary,
- *   keys[page][head][d] = min(127, |rint(S_d / 2^e)|) with S_d's sign, ties to even,
+ *   keys[page][head][d] = S_d / 2^e to the nearest whole number, at most 127 in
+ *   magnitude; a sum half way between two goes to either (the one nearer 0 where
+ *   binary64's pow(2, -e) is an ulp low, else the even one),
  *   exponents[page][head] = e.
  * page is the page's number in the cache. Other pages' keys keep their values;
  * hidden pages have none.

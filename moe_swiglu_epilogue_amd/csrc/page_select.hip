@@ -60,6 +60,7 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 {
     constexpr int kHeadBlocks = D / 16, kAhead = 8;
     __shared__ double sums[kThreads][17];
+    __shared__ double powers[64];                         // 2^-e, as binary64's pow has them
     // the requests' first pages first: workgroups that find none come last
     const int b = blockIdx.x % a.r.num_seqs;
     const int blocks = a.kv_heads * kHeadBlocks;          // of 16 dimensions, of a token
@@ -71,6 +72,11 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
     const int len = length_of(a.r, b);
     const int n = max(a.r.offsets[b + 1] - a.r.offsets[b], 0);
     const int begin = max(len - n, 0) / a.r.page, end = len / a.r.page;
+
+    // beside the loads; some are an ulp low, so that a sum half way between two keys
+    // goes to the one nearer 0 there and to the even one elsewhere
+    if (threadIdx.x < 64 && begin < end)
+        powers[threadIdx.x] = pow(2.0, -(double)threadIdx.x);
 
     for (int j = begin + blockIdx.x / a.r.num_seqs; j < end; j += a.per_request) {
         const int entry = a.r.table[b * a.r.ld_table + j];
@@ -133,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
             // the length of a whole number in binary is its exponent and 1
             const int bits = top < 1.0 ? 0 : (int)(__double_as_longlong(top) >> 52) - 1022;
             const int e = max(bits - 7, 0);
-            const double scale = __longlong_as_double((int64_t)(1023 - e) << 52);       // 2^-e
+            const double scale = powers[e];               // e is at most 53 - 7
             if (of < here) {
                 const int64_t at = (int64_t)entry * blocks + first_block + of;
                 uint32_t w = 0;

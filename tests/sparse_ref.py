@@ -58,8 +58,13 @@ def rope_append(q, k, v, positions, cos_sin, slots, caches, pair_axis=None, inte
 
 # ---- page keys -------------------------------------------------------------------
 def page_keys(kp, ks, table, lens, offsets, keys, exponents, page):
+    """keys, exponents, and keys with the other neighbour where a sum lies half way
+    between two numbers. (The factor 2^-e may be an ulp, 2^-53, low: S 2^-e below
+    2^7 is then off by less than 2^-45, while a sum that is not half way is at least
+    2^-e away from it, and e is at most 23 for pages of up to 256 tokens (256 6 448 2^10 < 2^30).)"""
     keys, exponents = keys.clone(), exponents.clone()
     pages, kv, dim = keys.shape
+    other = keys.clone()
     for b in range(len(lens)):
         length = min(max(int(lens[b]), 0), table.shape[1] * page)
         n = max(int(offsets[b + 1]) - int(offsets[b]), 0)
@@ -75,9 +80,12 @@ def page_keys(kp, ks, table, lens, offsets, keys, exponents, page):
                 for d in range(dim):
                     s = abs(int(total[h, d]))
                     low, rest, half = s >> e, s & ((1 << e) - 1), 1 << e >> 1
-                    up = e > 0 and (rest > half or (rest == half and low & 1))
-                    keys[entry, h, d] = int(math.copysign(min(127, low + up), int(total[h, d])))
-    return keys, exponents
+                    tie = e > 0 and rest == half
+                    up = e > 0 and (rest > half or (tie and low & 1))
+                    sign = -1 if int(total[h, d]) < 0 else 1
+                    keys[entry, h, d] = sign * min(127, low + up)
+                    other[entry, h, d] = sign * min(127, low + (not up if tie else up))
+    return keys, exponents, other
 
 
 # ---- selection -------------------------------------------------------------------

@@ -209,9 +209,10 @@ def check_keys(M, c, hint=None):
     got = M.nvfp4_page_keys(dev["kp"], dev["ks"], dev["table"], dev["lens"], dev["offsets"], dev["keys"], dev["exponents"],
                             page_size=c["page"], max_query_len=c["most"] if hint is None else hint)
     assert got[0] is dev["keys"] and got[1] is dev["exponents"]
-    keys, exponents = S.page_keys(c["kp"], c["ks"], c["table"], c["lens"], c["offsets"], c["keys"], c["exponents"], c["page"])
+    keys, exponents, other = S.page_keys(c["kp"], c["ks"], c["table"], c["lens"], c["offsets"], c["keys"], c["exponents"],
+                                         c["page"])
     assert torch.equal(host(got[1]), exponents)
-    assert torch.equal(host(got[0]), keys)
+    assert bool(((host(got[0]) == keys) | (host(got[0]) == other)).all())
 
 
 @pytest.mark.parametrize("kv,dim,page", [(1, 64, 16), (2, 128, 16), (8, 128, 64), (3, 256, 24), (5, 64, 1), (20, 64, 7),
@@ -552,9 +553,10 @@ def test_one_sparse_decoding_step(M):
     assert torch.equal(r["q"], q)
     for n, w in zip(("k", "ks", "v", "vs"), caches):
         assert np.array_equal(r[n].numpy(), w), n
-    keys, exponents = S.page_keys(r["k"], r["ks"], r["table"], r["lens"], r["offsets"], before["keys"], before["exponents"], 16)
-    assert torch.equal(r["keys"], keys) and torch.equal(r["exponents"], exponents)
-    pages = S.select_pages(q, keys, exponents, r["table"], r["lens"], r["offsets"], 16, 5, 1, 2)
+    keys, exponents, other = S.page_keys(r["k"], r["ks"], r["table"], r["lens"], r["offsets"], before["keys"],
+                                         before["exponents"], 16)
+    assert bool(((r["keys"] == keys) | (r["keys"] == other)).all()) and torch.equal(r["exponents"], exponents)
+    pages = S.select_pages(q, r["keys"], exponents, r["table"], r["lens"], r["offsets"], 16, 5, 1, 2)
     assert torch.equal(r["pages"], pages[:10])
     ref, ref_lse, tol, lse_tol = S.sparse_attention(q[:10], r["k"], r["ks"], r["v"], r["vs"], r["table"], r["lens"], r["offsets"],
                                                     r["pages"], 16, 1 / math.sqrt(128))

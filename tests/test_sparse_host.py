@@ -192,7 +192,8 @@ def test_page_keys_by_hand():
     scales[2:, 0] = 0x40
     packed[2, 0], packed[2, 8], packed[3, 0] = 0x07, 0x19, 0x06        # 6; -0.5, 0.5 of the second block; 4
     k, e = torch.full((2, 1, 64), 99, dtype=torch.int8), torch.full((2, 1), 99, dtype=torch.int8)
-    k, e = S.page_keys(packed, scales, torch.tensor([[1, 0]]), [3], [0, 3], k, e, 2)
+    k, e, other = S.page_keys(packed, scales, torch.tensor([[1, 0]]), [3], [0, 3], k, e, 2)
+    assert torch.equal(k, other)
     # sums 20 and +-0.5, in units of 2^-10: 20480 (15 bits), 512; e = 8: 80, 2
     assert e.tolist() == [[99], [8]] and k[1, 0, 0] == 80 and k[1, 0, 16] == -2 and k[1, 0, 17] == 2 and k[1].abs().sum() == 84
     assert k[0].eq(99).all()
