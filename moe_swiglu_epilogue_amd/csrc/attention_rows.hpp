@@ -1,8 +1,9 @@
 // Attention over pages of the NVFP4 cache for few query rows: what the kernels of
-// paged_attention.hip and sparse_attention.hip share. A tile of 32 tokens is
-// loaded and converted by a wave (load_tile), its scores, exponentials and
-// products are added up in registers (attend), and the parts of a range that was
-// split over workgroups are joined by a kernel of its own (attn_join_kernel).
+// paged_attention.hip and sparse_attention.hip share. A tile of 32 tokens is loaded
+// by a wave (load_tile), its scores, exponentials and products are added up in
+// registers (attend_tile.inc), a workgroup's waves are joined (join_waves.inc), and
+// the parts of a range that was split over workgroups are joined by a kernel of its
+// own (attn_join_kernel).
 #pragma once
 
 #include "attention_plan.hpp"
@@ -82,18 +83,11 @@ __device__ __forceinline__ int* used_splits(const Attn& a, int D)
     return (int*)(a.part + (int64_t)a.splits * a.tokens * a.heads * (D + 2));
 }
 
-// The splits that hold some of a span's tokens.
-__device__ __forceinline__ int splits_of(const Span& s)
-{
-    return max(1, (s.end - s.begin + s.chunk - 1) / s.chunk);
-}
-
-__device__ __forceinline__ void write_split(const Attn& a, int D, int split, int used, int64_t row, float m, float l)
+// Writes a row's reference and sum of one split.
+__device__ __forceinline__ void write_part(const Attn& a, int D, int split, int64_t row, float m, float l)
 {
     const int64_t rows = (int64_t)a.tokens * a.heads;
     *(float2*)(a.part + a.splits * rows * D + 2 * (split * rows + row)) = make_float2(m, l);
-    if (split == 0)
-        used_splits(a, D)[row] = used;
 }
 
 __device__ __forceinline__ uint32_t page_of(const Attn& a, uint32_t t)
@@ -330,163 +324,6 @@ __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, Table table
         const uint64_t at = mine * srow + (D > 64 ? 8 * c + 4 * (lane >> 5) : 0);
         t.ks[c] = *(const uint32_t*)(ks + at);
         t.vs[c] = *(const uint32_t*)(vs + at);
-    }
-}
-
-// One tile for a wave's query rows: scores, their exponentials and the sums. Row
-// rt sees those of its 32 tokens whose bit is set in seen(rt), as far as the tile
-// shows them; `whole`: every row sees all.
-template <int D, int RT, class Seen>
-__device__ __forceinline__ void attend(const Tile<D>& t, int lane, const half8v (&q)[RT][D / 32], const float (&factor)[RT],
-                                       bool whole, Seen seen_by, float (&m)[RT], float (&l)[RT],
-                                       float4v (&o)[RT][Tile<D>::C][Tile<D>::VM])
-{
-    using T = Tile<D>;
-    constexpr int C = T::C, VM = T::VM;
-    const int g = lane >> 4, n = lane & 15;
-    // S^T = K Q^T
-    float4v sc[RT][2];
-    for (int hh = 0; hh < 2; ++hh)
-        for (int rt = 0; rt < RT; ++rt)
-            sc[rt][hh] = float4v{0, 0, 0, 0};
-    for (int c = 0; c < C; ++c) {
-        const uint32_t mine = t.shown ? t.ks[c] : 0;
-        for (int hh = 0; hh < 2; ++hh) {
-            uint32_t w = from_lane(mine, n + 16 * hh + (D > 64 ? 32 * (g >> 1) : 0));
-            w >>= D > 64 ? 16 * (g & 1) : 8 * g;
-            const half2v sk = e4m3x2(w);
-            for (int i = 0; i < T::KW; ++i) {
-                const half8v kf = fp4x8(t.k[hh][c][i], D > 64 ? sk[i >> 1] : sk[0]);
-                for (int rt = 0; rt < RT; ++rt)
-                    sc[rt][hh] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        kf, q[rt][T::KW * c + i], sc[rt][hh], 0, 0, 0);
-            }
-        }
-    }
-
-    // exponentials: base 2, against the row's reference
-    const uint32_t hid = ~(uint32_t)__ballot(t.shown);     // bit j: token j does not count
-    whole = whole && hid == 0;
-    half8v p[RT];
-    for (int rt = 0; rt < RT; ++rt) {
-        float x[8];
-        for (int i = 0; i < 8; ++i)
-            x[i] = sc[rt][i >> 2][i & 3];
-        float top = largest(x);
-        if (!whole) {
-            const uint32_t seen = ~hid & seen_by(rt);
-            for (int i = 0; i < 8; ++i) {
-                const int in = 16 * (i >> 2) + 4 * g + (i & 3);
-                x[i] = seen >> in & 1 ? x[i] : -INFINITY;
-            }
-            top = largest(x);
-        }
-        top *= factor[rt];
-        if (__any(top > m[rt] + (kHeadroom + kSlack))) {
-            const float up = fmaxf(m[rt], row_max(top) - kHeadroom);
-            const float f = m[rt] == up ? 1.0f : __builtin_amdgcn_exp2f(m[rt] - up);
-            m[rt] = up;
-            l[rt] *= f;
-            for (int c = 0; c < C; ++c)
-                for (int i = 0; i < VM; ++i)
-                    o[rt][c][i] *= f;
-        }
-        // a row that has seen nothing keeps m = -inf: its terms are 0
-        const float base = m[rt] == -INFINITY ? 0.0f : m[rt];
-        for (int i = 0; i < 8; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], factor[rt], -base));
-            l[rt] += x[i];
-            p[rt][i] = (_Float16)x[i];
-        }
-    }
-
-    // O^T += V^T P^T
-    for (int c = 0; c < C; ++c) {
-        const uint32_t mine = t.shown ? t.vs[c] : 0;
-        const uint32_t byte = D > 64 ? (n >> 1) & 3 : n >> 2;
-        const uint32_t sel = byte | (4 + byte) << 8 | 0x0c0c0000u;
-        half2v sv[4];
-        uint32_t even[4], odd[4];       // dimensions 2x, 2x + 1 of token pairs, a byte each
-        for (int u = 0; u < 4; ++u) {
-            const int tok = 16 * (u >> 1) + 4 * g + 2 * (u & 1) + (D > 64 ? 32 * (n >> 3) : 0);
-            sv[u] = e4m3x2(__builtin_amdgcn_perm(from_lane(mine, tok + 1), from_lane(mine, tok), sel));
-            const uint32_t x = t.v[2 * u][c], y = t.v[2 * u + 1][c];
-            even[u] = (x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u);
-            odd[u] = (x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u);
-        }
-        for (int i = 0; i < VM; ++i) {
-            const uint32_t* w = i & 1 ? odd : even;
-            const half8v vf = join(fp4x2(w[0], i >> 1) * sv[0], fp4x2(w[1], i >> 1) * sv[1],
-                                   fp4x2(w[2], i >> 1) * sv[2], fp4x2(w[3], i >> 1) * sv[3]);
-            for (int rt = 0; rt < RT; ++rt)
-                o[rt][c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[rt][c][i], 0, 0, 0);
-        }
-    }
-}
-
-// LDS of a workgroup's W waves for joining their rows.
-template <int D, int W = 4>
-struct Joined {
-    float o[W][16][D + 4];
-    float m[W][16], l[W][16];
-};
-
-// Joins the W waves, a row tile at a time, and writes the rows row0 ... of the
-// `rows` that begin at token `first`, or their part of the workspace where the
-// tokens are split; `used`: how many splits have work.
-template <int D, int RT, int W = 4>
-__device__ __forceinline__ void join_waves(const Attn& a, Joined<D, W>& lds, int split, int used, int first, int rows,
-                                           int row0, int h, const float (&m)[RT], const float (&l)[RT],
-                                           const float4v (&o)[RT][Tile<D>::C][Tile<D>::VM])
-{
-    constexpr int C = Tile<D>::C, VM = Tile<D>::VM;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int group = a.heads / a.kv_heads;
-    for (int rt = 0; rt < RT; ++rt) {
-        const float sum = row_sum(l[rt]);
-        __syncthreads();
-        for (int c = 0; c < C; ++c)
-            for (int r = 0; r < 4; ++r)
-                for (int i = 0; i < VM; i += 4)
-                    *(float4v*)&lds.o[wave][n][128 * c + VM * (4 * g + r) + i] =
-                        float4v{o[rt][c][i][r], o[rt][c][i + 1][r], o[rt][c][i + 2][r], o[rt][c][i + 3][r]};
-        if (g == 0) {
-            lds.m[wave][n] = m[rt];
-            lds.l[wave][n] = sum;
-        }
-        __syncthreads();
-        const int row = tid >> 4, r = row0 + 16 * rt + row;
-        if (r >= rows || (W > 4 && row >= 16))
-            continue;
-        float top = -INFINITY, total = 0, f[W];
-        for (int w = 0; w < W; ++w)
-            top = fmaxf(top, lds.m[w][row]);
-        for (int w = 0; w < W; ++w) {
-            f[w] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(lds.m[w][row] - top);
-            total += f[w] * lds.l[w][row];
-        }
-        const int64_t token = first + r / group;
-        const int head = h * group + r % group;
-        const bool whole_row = a.splits == 1;
-        const float norm = whole_row ? (total != 0 ? (a.v_gs ? a.v_gs[0] : 1.0f) / total : 0.0f) : 1.0f;
-        for (int d = (tid & 15) * 4; d < D; d += 64) {
-            float4v v = {0, 0, 0, 0};
-            for (int w = 0; w < W; ++w)
-                v += f[w] * *(float4v*)&lds.o[w][row][d];
-            v *= norm;
-            if (whole_row)
-                *(uint2v*)(a.out + token * a.ld_out + head * D + d) = uint2v{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
-            else
-                *(float4v*)(a.part + (((int64_t)split * a.tokens + token) * a.heads + head) * D + d) = v;
-        }
-        if ((tid & 15) == 0) {
-            if (!whole_row) {
-                write_split(a, D, split, used, token * a.heads + head, top, total);
-            } else if (a.lse) {
-                a.lse[token * a.heads + head] = total != 0 ? (top + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
-            }
-        }
     }
 }
 

@@ -7,6 +7,14 @@
 
 namespace {
 
+__device__ __forceinline__ void write_split(const Attn& a, const Span& s, int D, int split, int64_t row,
+                                            float m, float l)
+{
+    write_part(a, D, split, row, m, l);
+    if (split == 0)
+        used_splits(a, D)[row] = max(1, (s.end - s.begin + s.chunk - 1) / s.chunk);
+}
+
 // ---- few query rows (tiles: attention_rows.hpp) -------------------------------
 // Waves a SIMD (workgroups a compute unit) that the registers allow without
 // spilling (one row tile of head_dim 128: 62 us for 64 requests with three, 72 with
@@ -19,7 +27,9 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
 {
     using T = Tile<D>;
     constexpr int C = T::C, KF = D / 32, VM = T::VM;
-    __shared__ Joined<D> lds;
+    constexpr int kPad = D + 4;
+    __shared__ float o_lds[4][16][kPad];
+    __shared__ float m_lds[4][16], l_lds[4][16];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -113,8 +123,9 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
         }
 
         auto compute = [&](const Tile<D>& t, int t0) {
-            attend<D, RT>(t, lane, q, factor, t0 >= s.all_begin && t0 + 32 <= s.all_end,
-                          [&](int rt) { return bits_between(lo[rt] - t0, hi[rt] - t0); }, m, l, o);
+#define WHOLE t0 >= s.all_begin && t0 + 32 <= s.all_end
+#define SEEN(rt) bits_between(lo[rt] - t0, hi[rt] - t0)
+#include "attend_tile.inc"
         };
         for (; t0 < last; t0 += 256) {
             compute(even, t0);
@@ -126,7 +137,10 @@ __global__ __launch_bounds__(256, (kRowsWaves<D, RT, kPaged16>)) void attn_rows_
             e1 = entries(t0 + 640);
         }
 
-        join_waves<D, RT>(a, lds, split, splits_of(s), s.first, s.rows, row0, h, m, l, o);
+#define ROWS s.rows
+#define FIRST s.first
+#define WRITE_SPLIT(row, m, l) write_split(a, s, D, split, row, m, l)
+#include "join_waves.inc"
     }
 }
 
@@ -497,7 +511,7 @@ __global__ __launch_bounds__(512) void attn_prompt_kernel(Attn a)
                 }
             if (half == 0) {
                 if (!whole_row) {
-                    write_split(a, D, split, splits_of(s), token * a.heads + head, m, total);
+                    write_split(a, s, D, split, token * a.heads + head, m, total);
                 } else if (a.lse) {
                     a.lse[token * a.heads + head] = total != 0 ? (m + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
                 }

@@ -14,7 +14,7 @@
 
 namespace {
 
-constexpr int kMostListed = 2048;
+constexpr int kMostListed = 2048, kWaves = 4, kThreads = 64 * kWaves;
 
 struct Sparse {
     Attn a;
@@ -32,23 +32,35 @@ struct Listed {
     uint16_t by[kMostListed];
 };
 
-template <int D, int W>
+template <int D>
+struct Joined {
+    float o[kWaves][16][D + 4];
+    float m[kWaves][16], l[kWaves][16];
+};
+
+template <int D>
 union Shared {
-    Joined<D, W> joined;
+    Joined<D> joined;
     Listed list;
 };
 
-template <int W>
+// A part of a row's listed tokens: all parts hold some.
+__device__ __forceinline__ void write_split(const Attn& a, int D, int split, int64_t row, float m, float l)
+{
+    write_part(a, D, split, row, m, l);
+    if (split == 0)
+        used_splits(a, D)[row] = a.splits;
+}
+
 struct Counts {
-    int n[W];
+    int n[kWaves];
     int repeated;
 };
 
 // Looks up the lists of the tokens t, ..., t + run - 1 of request b, the first of them
 // at position pos0, and joins them. Returns the number of pages; `run` becomes 1
 // where a token has listed a page twice, which then counts twice.
-template <int W>
-__device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W>& counts, int b, int t, int h, int pos0,
+__device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts& counts, int b, int t, int h, int pos0,
                                          int& run)
 {
     const Attn& a = s.a;
@@ -57,7 +69,7 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W
     int entries = run * pitch;
     if (tid == 0)
         counts.repeated = 0;
-    for (int e = tid; e < entries; e += 64 * W) {
+    for (int e = tid; e < entries; e += kThreads) {
         const int token = run == 1 ? 0 : e / pitch, i = e - token * pitch;
         const int p = i < s.list_len ? s.pages[((int64_t)(t + token) * a.kv_heads + h) * s.list_len + i] : -1;
         int page = -1;
@@ -71,7 +83,7 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W
     __syncthreads();
     if (run > 1) {
         // an entry stands for its page if no token before has listed it
-        for (int e = tid; e < entries; e += 64 * W) {
+        for (int e = tid; e < entries; e += kThreads) {
             const int p = list.first[e], token = e / pitch;
             if (p < 0)
                 continue;
@@ -93,14 +105,14 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W
         if (counts.repeated) {
             run = 1;
             entries = pitch;
-            for (int e = tid; e < entries; e += 64 * W)
+            for (int e = tid; e < entries; e += kThreads)
                 list.by[e] = list.first[e] >= 0 ? 1 : 0;
             __syncthreads();
         }
     }
     // the entries that stand for a page, moved to the front
     int total = 0;
-    for (int base = 0; base < entries; base += 64 * W) {
+    for (int base = 0; base < entries; base += kThreads) {
         const int e = base + tid;
         const int by = e < entries ? list.by[e] : 0;
         const int page = by ? list.page[e] : 0, p = by ? list.first[e] : 0;
@@ -109,7 +121,7 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W
             counts.n[wave] = __popcll(in);
         __syncthreads();
         int at = total + __popcll(in & ((1ull << lane) - 1));
-        for (int w = 0; w < W; ++w) {
+        for (int w = 0; w < kWaves; ++w) {
             at += w < wave ? counts.n[w] : 0;
             total += counts.n[w];
         }
@@ -123,16 +135,17 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts<W
     return total;
 }
 
-template <int D, int RT, bool kPaged16, int W>
-constexpr int kSparseWaves = W == 8 ? 1 : RT == 1 && D <= 128 && kPaged16 ? 3 : D * RT <= 256 ? 2 : 1;
+// Workgroups a compute unit, as many as the registers of the rows hold.
+template <int D, int RT, bool kPaged16>
+constexpr int kResident = RT == 1 && D <= 128 && kPaged16 ? 3 : D * RT <= 256 ? 2 : 1;
 
-template <int D, int RT, bool kPaged16, int W>
-__global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sparse_rows_kernel(Sparse s)
+template <int D, int RT, bool kPaged16>
+__global__ __launch_bounds__(kThreads, (kResident<D, RT, kPaged16>)) void sparse_rows_kernel(Sparse s)
 {
     using T = Tile<D>;
-    constexpr int C = T::C, KF = D / 32, VM = T::VM, kStep = 32 * W;
-    __shared__ Shared<D, W> lds;
-    __shared__ Counts<W> counts;
+    constexpr int C = T::C, KF = D / 32, VM = T::VM, kStep = 32 * kWaves;
+    __shared__ Shared<D> lds;
+    __shared__ Counts counts;
     const Attn& a = s.a;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, n = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -175,7 +188,7 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
         const int len = a.num_pages > 0 ? min(max(a.lens[b], 0), a.max_pages * a.page) : 0;
         const int pos0 = min(len - behind + token, len - 1);
         __syncthreads();                        // the LDS of what came before is read
-        const int range = make_list<W>(s, lds.list, counts, b, token, h, pos0, run) * a.page;
+        const int range = make_list(s, lds.list, counts, b, token, h, pos0, run) * a.page;
         // the splits take equal parts of what there is
         const int chunk = a.splits == 1 ? range : ((range + a.splits - 1) / a.splits + 127) & ~127;
         const int first = split * chunk, last = __builtin_amdgcn_readfirstlane(min(first + chunk, range));
@@ -241,25 +254,25 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
         }
         const int everyone = (1 << run) - 1;
         auto compute = [&](Tile<D>& t, int t0) {
-            bool whole = true;
-            uint32_t seen[RT];
+            bool all = true;
+            uint32_t sees_of[RT];
             if (kPaged16) {
                 int place[2], by[2];
                 for (int hh = 0; hh < 2; ++hh) {
                     const int at = min(t0 + 16 * hh, last - 16), i = (int)page_of(a, at);
                     place[hh] = __builtin_amdgcn_readfirstlane(lds.list.first[i]) + (at - i * a.page);
                     by[hh] = __builtin_amdgcn_readfirstlane(lds.list.by[i]);
-                    whole = whole && by[hh] == everyone && place[hh] + 15 <= pos0;
+                    all = all && by[hh] == everyone && place[hh] + 15 <= pos0;
                 }
                 // what lies behind the request's tokens may be anything
                 t.shown = t.shown && ((lane & 16) ? place[1] : place[0]) + n < len;
                 for (int rt = 0; rt < RT; ++rt)
-                    seen[rt] = ~0u;
-                if (!whole)
+                    sees_of[rt] = ~0u;
+                if (!all)
                     for (int rt = 0; rt < RT; ++rt) {
-                        seen[rt] = 0;
+                        sees_of[rt] = 0;
                         for (int hh = 0; hh < 2; ++hh)
-                            seen[rt] |= by[hh] >> bit[rt] & 1 ? bits_between(0, min(pos[rt] - place[hh] + 1, 16)) << 16 * hh : 0;
+                            sees_of[rt] |= by[hh] >> bit[rt] & 1 ? bits_between(0, min(pos[rt] - place[hh] + 1, 16)) << 16 * hh : 0;
                     }
             } else {
                 const int at = t0 + (lane & 31), i = (int)page_of(a, min(at, last - 1));
@@ -267,15 +280,17 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
                 const int by = at < last ? lds.list.by[i] : 0;
                 t.shown = t.shown && place < len;
                 for (int rt = 0; rt < RT; ++rt)
-                    seen[rt] = 0;
+                    sees_of[rt] = 0;
                 for (int k = 0; k < run; ++k) {
-                    const uint32_t all = (uint32_t)__ballot((by >> k & 1) && place <= pos0 + k);
-                    whole = whole && all == ~0u;
+                    const uint32_t shows = (uint32_t)__ballot((by >> k & 1) && place <= pos0 + k);
+                    all = all && shows == ~0u;
                     for (int rt = 0; rt < RT; ++rt)
-                        seen[rt] = bit[rt] == k ? all : seen[rt];
+                        sees_of[rt] = bit[rt] == k ? shows : sees_of[rt];
                 }
             }
-            attend<D, RT>(t, lane, q, factor, whole, [&](int rt) { return seen[rt]; }, m, l, o);
+#define WHOLE all
+#define SEEN(rt) sees_of[rt]
+#include "attend_tile.inc"
         };
         for (; t0 < last; t0 += 2 * kStep) {
             compute(even, t0);
@@ -287,14 +302,21 @@ __global__ __launch_bounds__(64 * W, (kSparseWaves<D, RT, kPaged16, W>)) void sp
             e1 = entries(t0 + 5 * kStep);
         }
         __syncthreads();                        // the list is read, its LDS goes to the join
-        join_waves<D, RT, W>(a, lds.joined, split, a.splits, token, run * group, row0, h, m, l, o);
+        const int first_row = token;
+        auto& o_lds = lds.joined.o;
+        auto& m_lds = lds.joined.m;
+        auto& l_lds = lds.joined.l;
+#define ROWS run * group
+#define FIRST first_row
+#define WRITE_SPLIT(row, m, l) write_split(a, D, split, row, m, l)
+#include "join_waves.inc"
     }
 }
 
 // How the work is cut: tokens that a workgroup takes together, its query rows, and
 // splits of the listed tokens where there are too few workgroups for the card.
 struct SparsePlan {
-    int together, block, row_blocks, splits, waves;
+    int together, block, row_blocks, splits;
 };
 
 SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t page_size,
@@ -314,8 +336,7 @@ SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t 
     p.row_blocks = ceil_div(rows, p.block);
     const int64_t range = list_len * page_size;
     const int64_t items = ceil_div(tokens, (int64_t)p.together) * kv_heads * p.row_blocks;
-    const int64_t slots = 512;
-    int64_t splits = items < 1 ? 1 : slots / items;
+    int64_t splits = items < 1 ? 1 : 512 / items;
     if (splits > ceil_div(range, (int64_t)128))
         splits = ceil_div(range, (int64_t)128);
     if (splits > 256)
@@ -323,7 +344,6 @@ SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t 
     if (splits < 1 || tokens * heads > (1 << 22))
         splits = 1;
     p.splits = (int)splits;
-    p.waves = 4;
     return p;
 }
 
@@ -333,9 +353,9 @@ template <int D, int RT>
 void launch_rows(const Sparse& s, dim3 grid, hipStream_t stream)
 {
     if (s.a.page % 16 == 0 && s.a.num_pages > 0)
-        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, true, 4>), grid, dim3(256), 0, stream, s);
+        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, true>), grid, dim3(kThreads), 0, stream, s);
     else
-        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, false, 4>), grid, dim3(256), 0, stream, s);
+        hipLaunchKernelGGL((sparse_rows_kernel<D, RT, false>), grid, dim3(kThreads), 0, stream, s);
 }
 
 template <int D>
