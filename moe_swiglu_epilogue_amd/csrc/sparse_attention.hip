@@ -135,6 +135,38 @@ __device__ __forceinline__ int make_list(const Sparse& s, Listed& list, Counts& 
     return total;
 }
 
+// A value's scale that is NaN would reach the rows that do not see its token, as 0
+// times NaN is NaN: it is taken out of the tile, and the rows that see the token get it.
+template <int D, int RT>
+__device__ __forceinline__ void part_nans(Tile<D>& t, const uint32_t (&sees)[RT], int lane,
+                                          float4v (&o)[RT][Tile<D>::C][Tile<D>::VM])
+{
+    const int g = lane >> 4;
+#pragma unroll
+    for (int c = 0; c < Tile<D>::C; ++c) {
+        const uint32_t nan = t.shown ? ((t.vs[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : 0;
+        if (__any(nan != 0)) {
+            // byte b of a lane: 16 dimensions, those of the lanes g = b, or for 128 dimensions
+            // those 2 (b % 2) + (0, 1) of g = b / 2 and, of the second half wave, g = 2 + b / 2
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint64_t tokens = __ballot(nan >> (8 * b + 7) & 1);
+                const uint32_t mine = D > 64 && g >= 2 ? (uint32_t)(tokens >> 32) : (uint32_t)tokens;
+                const bool own = D > 64 ? (g & 1) == b >> 1 : g == b;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int i = 0; i < Tile<D>::VM; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (D == 64 || r >> 1 == (b & 1))
+                                o[rt][c][i][r] = own && (mine & sees[rt]) ? NAN : o[rt][c][i][r];
+            }
+            t.vs[c] &= ~((nan >> 7) * 255u);
+        }
+    }
+}
+
 // Workgroups a compute unit, as many as the registers of the rows hold.
 template <int D, int RT, bool kPaged16>
 constexpr int kResident = RT == 1 && D <= 128 && kPaged16 ? 3 : D * RT <= 256 ? 2 : 1;
@@ -288,6 +320,8 @@ __global__ __launch_bounds__(kThreads, (kResident<D, RT, kPaged16>)) void sparse
                         sees_of[rt] = bit[rt] == k ? shows : sees_of[rt];
                 }
             }
+            if (!all)
+                part_nans<D, RT>(t, sees_of, lane, o);
 #define WHOLE all
 #define SEEN(rt) sees_of[rt]
 #include "attend_tile.inc"

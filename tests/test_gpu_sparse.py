@@ -3,6 +3,7 @@ their plain definitions (tests/sparse_ref.py): rotated queries, cache bytes, pag
 keys and page lists bit for bit, attention within bounds that count its roundings;
 empty rows and requests, hidden pages, odd sizes, pitches, other streams, captured
 graphs, and the operators run one after the other."""
+import ctypes as C
 import math
 
 import numpy as np
@@ -353,6 +354,41 @@ def test_select_the_longest_table(M):
     check_select(M, c, 2045, 1, 2)
 
 
+def test_select_the_longest_table_for_many_tokens(M):
+    """As many tokens as go to workgroups that keep all scores in LDS, with tables of
+    the most pages and queries of the largest head."""
+    n = 32768
+    c = request_case(10, 8, 256, 1, [n, 60], [2, 98], heads=8, width=n)
+    say("select longest table, many tokens")
+    assert M.sparse.raw().nvfp4_select_pages_workspace(100, 8, 8, 2, n) == 0
+    check_select(M, c, 50, 1, 2)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [40, 30, 2]])
+def test_select_queries_that_are_not_finite(M, news):
+    """A token with such a query gets a valid list; the others' are what they were."""
+    c = request_case(17, 2, 128, 4, [600, 333, 90], news, heads=8)
+    top, first, local = 20, 1, 2
+    bad = c["offsets"][1].item()
+    q = c["q"].clone()
+    q[bad, 1, 3], q[bad, 6, 100] = math.nan, -math.inf
+    say("select not finite", news)
+
+    def run(q):
+        dev = device(dict(c, q=q))
+        return host(M.nvfp4_select_pages(dev["q"], dev["keys"], dev["exponents"], dev["table"], dev["lens"], dev["offsets"],
+                                         page_size=4, top_k=top, first=first, local=local))
+    want, got = run(c["q"]), run(q)
+    others = torch.arange(len(q)) != bad
+    assert torch.equal(got[others], want[others])
+    own = (333 - news[1]) // 4
+    for h in range(2):
+        p = got[bad, h]
+        n = int((p >= 0).sum())
+        assert bool((p[n:] == -1).all()) and bool((p[1:n] > p[:n - 1]).all()) and p[n - 1] == own
+        assert p[0] == 0 and p[n - 2] == own - 1 and n <= top + first + local
+
+
 # ---- attention -------------------------------------------------------------------
 def lists(c, kv, n, seed, wild=False):
     """Random pages for each token and head, some repeated, some that show nothing."""
@@ -493,7 +529,180 @@ def test_sparse_attention_unseen_slots_may_hold_anything(M, page):
     assert torch.equal(host(got[0]), want[0]) and torch.equal(host(got[1]), want[1])
 
 
+@pytest.mark.parametrize("news", [[1, 1], [6, 5]])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 16), (256, 32), (64, 3), (128, 10), (256, 9)])
+def test_sparse_attention_nan_is_not_hidden(M, dim, page, news):
+    """A NaN in a query, or in a key or value that a row sees, reaches that row's
+    output; rows that do not see it keep their bytes."""
+    c = request_case(16, 2, dim, page, [20 * page, 7 * page + 3], news, heads=4)
+    tokens = sum(news)
+    p = torch.arange(5, dtype=torch.int32).expand(tokens, 2, 5).contiguous()
+    p[0, :, 2] = 9                                    # the only one that lists page 9 of request 0, and not 2
+    dev = device(c)
+    say("sparse NaN", dim, page, news)
+    want, want_lse = [host(x).clone() for x in call_sparse(M, c, dev, p.cuda())]
+    assert not bool(torch.isnan(want.float()).any())
+    q = c["q"].clone()
+    q[1, 3, 47] = math.nan
+    out, lse = [host(x) for x in call_sparse(M, c, device(dict(c, q=q)), p.cuda())]
+    hit = torch.zeros(tokens, 4, dtype=torch.bool)
+    hit[1, 3] = True
+    assert bool(torch.isnan(out[hit].float()).all()) and bool(torch.isnan(lse[hit]).all())
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    slot = int(c["table"][0, 9]) * page + page - 1
+    hit = torch.zeros(tokens, 4, dtype=torch.bool)
+    hit[0, :2] = True                                 # key/value head 0's
+    d = device(c)
+    d["ks"][slot, 2] = 0xff
+    out, lse = [host(x) for x in call_sparse(M, c, d, p.cuda())]
+    assert bool(torch.isnan(out[hit].float()).all()) and bool(torch.isnan(lse[hit]).all())
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    for block in range(dim // 16):                    # 16 dimensions of the value: those alone
+        d = device(c)
+        d["vs"][slot, block] = 0x7f if block % 2 else 0xff
+        out, lse = [host(x) for x in call_sparse(M, c, d, p.cuda())]
+        nan = torch.zeros(out.shape, dtype=torch.bool)
+        nan[0, :2, 16 * block:16 * block + 16] = True
+        assert torch.equal(torch.isnan(out.float()), nan), block
+        assert torch.equal(out[~nan], want[~nan]) and torch.equal(lse, want_lse), block
+
+
 # ---- together --------------------------------------------------------------------
+@pytest.mark.parametrize("page", [2, 16])
+def test_pages_far_into_a_large_cache(M, page):
+    """The last pages of caches of 5 GB (offsets beyond 32 bits) give what the same
+    pages give in a small cache."""
+    kv, dim, heads, slots = 32, 256, 32, 1200 * 1024
+    c = request_case(18, kv, dim, page, [40 * page + 1, 9 * page], [1, 3], heads=heads)
+    small = c["kp"].shape[0] // page
+    shift = slots // page - small
+    far = dict(c, table=torch.where(c["table"] >= 0, c["table"] + shift, c["table"]))
+    a, b = device(c), device(far)
+    say("far pages", page)
+    for n in ("kp", "ks", "vp", "vs", "keys", "exponents"):
+        rows = slots if n in ("kp", "ks", "vp", "vs") else slots // page
+        big = torch.zeros((rows, *c[n].shape[1:]), dtype=c[n].dtype, device="cuda")
+        big[rows - c[n].shape[0]:] = a[n]
+        b[n] = big
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(4, kv, dim, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    positions = torch.tensor([5, 1, 2, 3], dtype=torch.int32).cuda()
+    cos_sin = torch.randn(8, dim, generator=g).cuda()
+    got = []
+    for d, base in ((a, 0), (b, shift * page)):
+        own = torch.tensor([int(c["table"][0, 40]) * page] + [int(c["table"][1, i // page]) * page + i % page
+                                                              for i in range(9 * page - 3, 9 * page)]) + base
+        q = M.nvfp4_rope_append(d["q"], k, v, positions, cos_sin, own.cuda(), d["kp"], d["ks"], d["vp"], d["vs"])
+        M.nvfp4_page_keys(d["kp"], d["ks"], d["table"], d["lens"], torch.tensor([0, 40 * page, 49 * page], dtype=torch.int32).cuda(),
+                          d["keys"], d["exponents"], page_size=page, max_query_len=40 * page)
+        pages = M.nvfp4_select_pages(q, d["keys"], d["exponents"], d["table"], d["lens"], d["offsets"], page_size=page, top_k=6)
+        out, lse = M.nvfp4_sparse_attention(q, d["kp"], d["ks"], d["vp"], d["vs"], d["table"], d["lens"], d["offsets"], pages,
+                                            page_size=page, scale=c["scale"], lse=True)
+        tail = [d[n][len(d[n]) - len(c[n]):] for n in ("kp", "ks", "vp", "vs", "keys", "exponents")]
+        got.append([host(x).clone() for x in (q, pages, out, lse, *tail)])
+        if base:
+            assert not bool(d["kp"][:base].any()) and not bool(d["keys"][:shift].any())
+    for i, (x, y) in enumerate(zip(*got)):
+        assert torch.equal(x, y), i
+
+
+def test_steps_on_two_streams(M):
+    """Two steps that may run at the same time, with caches and workspaces of their own."""
+    want = []
+    for seed in (3, 4):
+        s = step_state(seed)
+        first_keys(M, s)
+        want.append({k: host(v).clone() for k, v in one_step(M, s).items()})
+    states = [step_state(seed) for seed in (3, 4)]
+    for s in states:
+        first_keys(M, s)
+    torch.cuda.synchronize()
+    say("two streams")
+    streams, got = [torch.cuda.Stream() for _ in states], [None, None]
+    for _ in range(3):
+        for i, s in enumerate(states):
+            with torch.cuda.stream(streams[i]):
+                s["table"].copy_(step_state(3 + i)["table"])
+                got[i] = one_step(M, s)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for k, v in got[i].items():
+            assert torch.equal(host(v), want[i][k]), (i, k)
+
+
+def test_sparse_refusals(M):
+    """What the binding and the library refuse, with tensors of every operator; nothing
+    is launched, nothing written."""
+    c = request_case(19, 2, 128, 16, [70, 33], [1, 2], heads=8)
+    d = device(c)
+    pages = torch.zeros(3, 2, 4, dtype=torch.int32).cuda()
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16).cuda()
+    positions, slots = torch.zeros(3, dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int64).cuda()
+    cos_sin = torch.zeros(9, 128).cuda()
+    before = {n: host(v).clone() for n, v in d.items() if isinstance(v, torch.Tensor)}
+    refused = (TypeError, ValueError, M.Nvfp4Error)
+
+    def append(q=d["q"], k=k, v=k, p=positions, t=cos_sin, s=slots, kp=d["kp"], ks=d["ks"], vp=d["vp"], vs=d["vs"], **more):
+        M.nvfp4_rope_append(q, k, v, p, t, s, kp, ks, vp, vs, **more)
+
+    def keys(kp=d["kp"], ks=d["ks"], t=d["table"], n=d["lens"], o=d["offsets"], keys=d["keys"], e=d["exponents"], page=16, most=2):
+        M.nvfp4_page_keys(kp, ks, t, n, o, keys, e, page_size=page, max_query_len=most)
+
+    def select(q=d["q"], keys=d["keys"], e=d["exponents"], t=d["table"], n=d["lens"], o=d["offsets"], page=16, top=4, **more):
+        M.nvfp4_select_pages(q, keys, e, t, n, o, page_size=page, top_k=top, **more)
+
+    def sparse(q=d["q"], kp=d["kp"], ks=d["ks"], vp=d["vp"], vs=d["vs"], t=d["table"], n=d["lens"], o=d["offsets"], p=pages,
+               page=16, **more):
+        M.nvfp4_sparse_attention(q, kp, ks, vp, vs, t, n, o, p, page_size=page, **more)
+
+    wide = torch.zeros(3, 8, 256, dtype=torch.bfloat16).cuda()
+    bad = [(append, x) for x in (
+        dict(q=d["q"].float()), dict(q=d["q"].cpu()), dict(q=d["q"][:2]), dict(q=d["q"][:, :0]), dict(q=wide[:, :, ::2]), dict(k=k.cpu()),
+        dict(k=k[0]), dict(v=k[:, :1]), dict(p=positions.long()), dict(p=positions[:2]), dict(p=positions.cpu()),
+        dict(p=torch.zeros(3, 2, dtype=torch.int32).cuda().t()), dict(p=torch.zeros(3, dtype=torch.int32).cuda().expand(2, 3)),
+        dict(t=cos_sin.double()), dict(t=cos_sin[:, :127]), dict(t=cos_sin[:, :64]), dict(t=torch.zeros(9, 256).cuda()),
+        dict(t=cos_sin[0]), dict(s=slots.int()), dict(s=slots[:2]), dict(kp=d["kp"][:, :64]), dict(ks=d["ks"][:9]),
+        dict(vp=d["vp"].view(torch.int8)), dict(vs=d["ks"].cpu()), dict(vp=d["kp"]), dict(vs=d["ks"]),
+        dict(pair_axis=torch.zeros(63, dtype=torch.int32).cuda()), dict(pair_axis=torch.zeros(64).cuda()),
+        dict(k_gs=torch.zeros(2).cuda()), dict(v_gs=torch.ones(1)), dict(q_out=d["q"]), dict(q_out=d["q"][:2]),
+        dict(q=None, q_out=d["q"]), dict(q=wide[:, :, :128]), dict(p=torch.zeros(17, 3, dtype=torch.int32).cuda()),
+        dict(kp=d["kp"][0], ks=d["ks"][0]))]
+    bad += [(keys, x) for x in (
+        dict(kp=d["kp"].cpu()), dict(kp=d["kp"][:32]), dict(ks=d["ks"].float()), dict(t=d["table"].long()), dict(t=d["table"][:1]),
+        dict(t=d["table"].t()), dict(n=d["lens"].long()), dict(o=d["offsets"][:2]), dict(keys=d["keys"].float()),
+        dict(keys=d["keys"][:, :, :64]), dict(keys=d["keys"][:1]), dict(e=d["exponents"][:, :1]), dict(e=d["exponents"].int()),
+        dict(page=0), dict(page=8), dict(page=-16), dict(page=2 ** 31), dict(page=2 ** 63), dict(most=-1), dict(page=16.0),
+        dict(n=d["lens"].cpu()), dict(o=d["offsets"].cpu()))]
+    bad += [(select, x) for x in (
+        dict(q=d["q"].half()), dict(q=d["q"][0]), dict(q=d["q"][:, :7]), dict(q=d["q"][:, :, :64]), dict(keys=d["keys"].cpu()),
+        dict(e=d["exponents"].float()), dict(t=d["table"].float()), dict(n=d["lens"][:1]), dict(o=d["offsets"].long()), dict(page=0),
+        dict(top=-1), dict(top=2046), dict(top=2 ** 40), dict(first=-1), dict(first=2 ** 64), dict(local=0), dict(local=2047),
+        dict(pages=pages), dict(pages=torch.zeros(3, 2, 7).cuda()), dict(top=4.0), dict(q=wide[:, :, ::2]),
+        dict(workspace=torch.empty(8, dtype=torch.uint8).cuda()), dict(t=torch.zeros(2, 32769, dtype=torch.int32).cuda()),
+        dict(page=2 ** 29))]
+    bad += [(sparse, x) for x in (
+        dict(q=d["q"].float()), dict(q=d["q"][:2]), dict(q=d["q"][:, :7]), dict(q=wide[:, :, ::2]), dict(p=pages.long()), dict(p=pages[:2]),
+        dict(p=pages[0]), dict(p=pages[:, :1]), dict(p=pages.cpu()), dict(p=pages[:, :, ::2]),
+        dict(p=torch.zeros(3, 2, 2049, dtype=torch.int32).cuda()), dict(page=0), dict(page=7), dict(page=2 ** 31), dict(page=2 ** 40),
+        dict(t=d["table"].cpu()), dict(n=d["lens"].float()), dict(o=d["offsets"][1:]), dict(kp=d["kp"][:, :8]), dict(vs=d["vs"][1:]),
+        dict(ks=d["ks"].int()), dict(scale=math.nan), dict(scale=math.inf), dict(k_gs=torch.zeros(3).cuda()), dict(out=d["q"][:2]),
+        dict(out=d["q"].float()), dict(lse=torch.zeros(3, 7).cuda()), dict(lse=torch.zeros(3, 8).half().cuda()),
+        dict(p=pages[:, :0]),
+        dict(p=torch.zeros(3, 2, 400, dtype=torch.int32).cuda(), workspace=torch.empty(64, dtype=torch.uint8).cuda()))]
+    for call in (append, keys, select, sparse):           # what the others change is all that is wrong
+        say("taken", call.__name__)
+        if call is not append:
+            call()
+    for name in before:
+        d[name].copy_(before[name])
+    for call, change in bad:
+        say("refused", call.__name__, {n: tuple(v.shape) if isinstance(v, torch.Tensor) else v for n, v in change.items()})
+        with pytest.raises((*refused, C.ArgumentError)):
+            call(**change)
+    for n, v in before.items():
+        assert torch.equal(host(d[n]), v), n
+
+
 def step_state(seed=3):
     """Six requests over pages of 16, 8/2 heads of 128: caches with pages' keys."""
     g = torch.Generator().manual_seed(seed)
