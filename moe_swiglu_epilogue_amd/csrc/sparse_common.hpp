@@ -6,9 +6,11 @@
 
 namespace sparse {
 
-// The request of token t by the requests' offsets, -1 if it is none's: the last b
-// with offsets[b] <= t. The t-th request (single tokens) or the last one (a chunk)
-// is tried first, which takes one round of loads; a wave then looks at 64 at a time.
+// The request b of token t, offsets[b] <= t < offsets[b + 1], -1 if it is none's. The
+// t-th request (single tokens) or the last one (a chunk) is tried first, which takes
+// one round of loads; a wave then counts 64 offsets at a time. Offsets that fall
+// may give -1, but never a request that ends in front of the token, which a loop over
+// tokens could not leave.
 __device__ __forceinline__ int request_of(const int32_t* offsets, int num_seqs, int t)
 {
     const int guess = min(t, num_seqs - 1);
@@ -21,7 +23,7 @@ __device__ __forceinline__ int request_of(const int32_t* offsets, int num_seqs, 
         const int i = base + lane;
         b += __popcll(__ballot(i <= num_seqs && offsets[min(i, num_seqs)] <= t));
     }
-    return b >= num_seqs ? -1 : b;
+    return b < 0 || b >= num_seqs || offsets[b] > t || offsets[b + 1] <= t ? -1 : b;
 }
 
 }  // namespace sparse

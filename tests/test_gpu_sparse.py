@@ -703,6 +703,26 @@ def test_sparse_refusals(M):
         assert torch.equal(host(d[n]), v), n
 
 
+@pytest.mark.parametrize("offsets", [[0, 30, 12, 40], [5, 5, 5, 5], [40, 30, 20, 10], [-7, 10 ** 9, 20, 2 ** 31 - 1], [0, -2 ** 31, 40, 3]])
+def test_offsets_that_fall(M, offsets):
+    """Such offsets are no requests; what they give is not specified, but every call
+    ends and writes lists of valid pages."""
+    c = request_case(20, 2, 64, 16, [100, 300, 555], [10, 20, 10], heads=8)
+    dev = device(dict(c, offsets=torch.tensor(offsets, dtype=torch.int32)))
+    say("falling offsets", offsets)
+    M.nvfp4_page_keys(dev["kp"], dev["ks"], dev["table"], dev["lens"], dev["offsets"], dev["keys"], dev["exponents"], page_size=16,
+                      max_query_len=20)
+    for n in (40, 3):
+        q = dev["q"][:n]
+        pages = torch.full((n, 2, 12), -1, dtype=torch.int32).cuda()
+        M.nvfp4_select_pages(q, dev["keys"], dev["exponents"], dev["table"], dev["lens"], dev["offsets"], page_size=16, top_k=9,
+                             pages=pages)
+        got = host(pages)
+        assert bool(((got >= -1) & (got < c["table"].shape[1])).all())
+        call_sparse(M, c, dict(dev, q=q), pages)
+        torch.cuda.synchronize()
+
+
 def step_state(seed=3):
     """Six requests over pages of 16, 8/2 heads of 128: caches with pages' keys."""
     g = torch.Generator().manual_seed(seed)
