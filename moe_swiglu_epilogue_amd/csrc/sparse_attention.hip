@@ -388,10 +388,15 @@ SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t 
            (p.together + 1) * list_len * page_size <= (1 << 30))
         ++p.together;
     const int rows = p.together * group;
-    p.block = head_dim > 128 ? 16 : rows <= 64 ? ceil_div(rows, 16) * 16 : 64;
+    const int64_t range = list_len * page_size, units = ceil_div(tokens, (int64_t)p.together) * kv_heads;
+    // More rows share a tile's conversion, but take the registers of other waves: 512
+    // tokens of 64 heads on one of 128, 64 pages of 32: 112 us in blocks of 16, 83 of 32,
+    // 144 of 64; 48 such tokens 28, 27 and 62 us. Of 64 dimensions 512 tokens take 87, 67 and
+    // 51 us, 48 of them 23, 21 and 27.
+    const int most = head_dim > 128 ? 16 : head_dim > 64 || units < 512 ? 32 : 64;
+    p.block = rows <= 16 || most == 16 ? 16 : rows <= 32 || most == 32 ? 32 : 64;
     p.row_blocks = ceil_div(rows, p.block);
-    const int64_t range = list_len * page_size;
-    const int64_t items = ceil_div(tokens, (int64_t)p.together) * kv_heads * p.row_blocks;
+    const int64_t items = units * p.row_blocks;
     int64_t splits = items < 1 ? 1 : 512 / items;
     if (splits > ceil_div(range, (int64_t)128))
         splits = ceil_div(range, (int64_t)128);
@@ -424,12 +429,11 @@ void launch(const Sparse& s, int block, hipStream_t stream)
     if (block == 16) {
         launch_rows<D, 1>(s, grid, stream);
     } else if constexpr (D <= 128) {
-        if (block == 32)
+        if (block == 32) {
             launch_rows<D, 2>(s, grid, stream);
-        else if (block == 48)
-            launch_rows<D, 3>(s, grid, stream);
-        else
+        } else if constexpr (D == 64) {
             launch_rows<D, 4>(s, grid, stream);
+        }
     }
     if (a.splits > 16)
         hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);

@@ -473,6 +473,15 @@ def test_sparse_attention_tokens_that_share_pages(M, heads, kv, dim, page, n):
     check_sparse(M, c, p)
 
 
+@pytest.mark.parametrize("heads,dim,page", [(40, 64, 16), (64, 64, 5), (70, 64, 32), (40, 128, 16)])
+def test_sparse_attention_many_tokens_with_many_rows(M, heads, dim, page):
+    """Enough tokens of more than 32 heads on one that a workgroup takes all of them."""
+    c = request_case(heads + dim + page, 1, dim, page, [20 * page, 400, 140], [200, 300, 40], heads=heads, pad=1)
+    say("sparse many rows", heads, dim, page)
+    check_sparse(M, c, lists(c, 1, 5, 1), gs=(0.7, 1.9))
+    check_sparse(M, c, lists(c, 1, 9, 2, wild=True))
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_sparse_attention_rows_that_see_nothing(M, dim):
     """Empty contexts, queries before the context, hidden pages, empty lists, lists of
