@@ -30,7 +30,8 @@ __device__ __forceinline__ int length_of(const Requests& r, int b)
 // of four of them is exact in FP32; these go to binary64 sums, which are exact for
 // pages up to 2^31 tokens. The threads' sums meet in LDS, where every thread adds
 // some up. Bound by memory latency: a workgroup's chain of loads (lengths, table,
-// tokens) and its start.
+// tokens) and its start. A step of 256 requests 6.2 us, 6 prompts of up to 16384 tokens
+// (21 MB) 12.
 struct PageKeys {
     const uint8_t *kp, *ks;
     int8_t *keys, *exponents;
@@ -170,9 +171,12 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 //   Many tokens: a workgroup takes some that follow each other in one request and a
 // key/value head, keeps their scores in LDS, and a wave each selects; a single
 // token's is selected by all waves (select_chunk_kernel).
+// 2048 tokens of 32/8 heads of 128 behind 30000 (500 pages of 64): 56 us, 31 of them
+// vector arithmetic, most of it the search's.
 //   Few tokens: a compute unit alone reads keys at some 25 GB/s, so their pages go to a
 // workgroup for each 256 (score_pages_kernel), and by way of the workspace to a
-// workgroup for each list (list_pages_kernel).
+// workgroup for each list (list_pages_kernel). One request of 2048 pages 13 us, 64 of up
+// to 1024 20 us; latency, and for many requests keys of 128 bytes from all over the cache.
 struct Select {
     const uint16_t* q;
     const int8_t *keys, *exponents;
