@@ -171,11 +171,11 @@ __global__ __launch_bounds__(kThreads) void page_keys_kernel(PageKeys a)
 //   Many tokens: a workgroup takes some that follow each other in one request and a
 // key/value head, keeps their scores in LDS, and a wave each selects; a single
 // token's is selected by all waves (select_chunk_kernel).
-// 2048 tokens of 32/8 heads of 128 behind 30000 (500 pages of 64): 56 us, 31 of them
+// 2048 tokens of 32/8 heads of 128 behind 30000 (500 pages of 64): 54 us, some 30 of them
 // vector arithmetic, most of it the search's.
 //   Few tokens: a compute unit alone reads keys at some 25 GB/s, so their pages go to a
 // workgroup for each 256 (score_pages_kernel), and by way of the workspace to a
-// workgroup for each list (list_pages_kernel). One request of 2048 pages 13 us, 64 of up
+// workgroup for each list (list_pages_kernel). One request of 2048 pages 12 us, 64 of up
 // to 1024 20 us; latency, and for many requests keys of 128 bytes from all over the cache.
 struct Select {
     const uint16_t* q;
@@ -253,10 +253,10 @@ struct SelectShared {
 
 // The top-th largest of score[first .. before): the scores between the smallest and
 // the largest are counted in 256 equal parts, and the search goes on in the part that
-// holds the top-th, until all of it is wanted or it holds one value. By one wave
+// holds the top-th, until all of it is wanted, or one, or it holds one value. By one wave
 // (W = 1) in bins of its own, or by all of a workgroup's. The parts that hold the
-// smallest and the largest score differ, so every round leaves a score out; two
-// rounds are usual. (A wave alone takes 8 clocks an instruction: halving the range by
+// smallest and the largest score differ, so every round leaves a score out; one or
+// two rounds are usual. (A wave alone takes 8 clocks an instruction: halving the range by
 // counts took a dozen rounds of 0.6 us.) The first 8 scores of a lane stay in
 // registers, which is all up to 512 pages a wave.
 template <int W, class Shared>
@@ -373,6 +373,8 @@ __device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int
         hi = number(high);
         if (n == want)
             return {lo, ~0u};
+        if (want == 1)
+            return {hi, 1};
     }
     return {lo, want};
 }
