@@ -259,6 +259,10 @@ struct SelectShared {
 // two rounds are usual. (A wave alone takes 8 clocks an instruction: halving the range by
 // counts took a dozen rounds of 0.6 us.) The first 8 scores of a lane stay in
 // registers, which is all up to 512 pages a wave.
+//   Scores that the kernels write are -inf or finite and at most 2^86 in magnitude. Of
+// any others (a workspace that another call writes to) the search ends and at most top are
+// chosen all the same: NaN is never chosen, and where `scale` is 0, as hi - lo is +inf,
+// a round leaves nothing out and is the last.
 template <int W, class Shared>
 __device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int first, int before, int top)
 {
@@ -285,7 +289,7 @@ __device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int
     };
     uint32_t low = ~0u, high = 0, n = 0;
     each([&](float v) {
-        const bool in = v != -INFINITY;
+        const bool in = v > -INFINITY;
         low = min(low, in ? ordered(v) : ~0u);
         high = max(high, in ? ordered(v) : 0);
         n += in;
@@ -369,6 +373,8 @@ __device__ __forceinline__ Limit find_limit(Shared& lds, const float* score, int
             low = lds.lo[turn ^ 1];
             high = lds.hi[turn ^ 1];
         }
+        if (number(low) == lo && number(high) == hi)
+            return {hi, want};
         lo = number(low);
         hi = number(high);
         if (n == want)
