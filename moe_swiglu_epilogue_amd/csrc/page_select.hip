@@ -731,10 +731,22 @@ __global__ __launch_bounds__(64 * W) void list_pages_kernel(Select a)
     extern __shared__ __align__(16) float score[];
     __shared__ __align__(16) SelectShared<W> lds;
     const int token = blockIdx.x / a.kv_heads;
-    const int b = sparse::request_of(a.r.offsets, a.r.num_seqs, token);
-    if (b < 0)
-        return;
-    const Place r = place_of(a.r, b);
+    // The request that score_pages_kernel has scored the token for: that of the first
+    // token of its run. With offsets that fall the token's own may be another one, with
+    // pages that nobody has scored.
+    Place r;
+    for (int at = a.together > 1 ? token - token % a.together : token;;) {
+        const int b = sparse::request_of(a.r.offsets, a.r.num_seqs, at);
+        if (b < 0) {
+            if (at++ == token)
+                return;
+            continue;
+        }
+        r = place_of(a.r, b);
+        if (r.behind > token)
+            break;
+        at = r.behind;
+    }
     const int p = min(r.len - r.behind + token, r.len - 1), before = scored_before(a, p);
     const float* from = a.scores + (int64_t)blockIdx.x * a.pitch;
     for (int j = a.first + threadIdx.x; j < before; j += 64 * W)
