@@ -329,8 +329,9 @@ __device__ __forceinline__ void load_tile(Tile<D>& t, const Attn& a, Table table
 
 // Joins the splits of the query rows: kWaves waves a (token, head), which take a
 // share of the splits each. Bound by latency: everything it needs to know, which
-// rows count and how many splits they have, is loaded at once.
-template <int D, int kWaves>
+// rows count and how many splits they have, is loaded at once. A row counts where its
+// token is a request's, or (kMarked) where it has splits.
+template <int D, int kWaves, bool kMarked>
 __global__ __launch_bounds__(256) void attn_join_kernel(Attn a)
 {
     constexpr int kLanes = D / 4, kAtOnce = 64 / kLanes * kWaves;    // lanes a row of D; splits read at once
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Attn a)
         }
         top = fmaxf(top, m[i]);
     }
-    const bool shown = mine && token >= a.offsets[0] && token < a.offsets[a.num_seqs];
+    const bool shown = mine && (kMarked ? used > 0 : token >= a.offsets[0] && token < a.offsets[a.num_seqs]);
     for (int d = 32; d; d >>= 1)
         top = fmaxf(top, __shfl_xor(top, d));
     float total = 0;

@@ -556,9 +556,9 @@ void launch(const Attn& a, int block, hipStream_t stream)
             launch_rows<D, 4>(a, grid, stream);
     }
     if (a.splits > 16)
-        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_join_kernel<D, 4, false>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);
     else if (a.splits > 1)
-        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)(a.tokens * a.heads + 3) / 4), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_join_kernel<D, 1, false>), dim3((unsigned)(a.tokens * a.heads + 3) / 4), dim3(256), 0, stream, a);
 }
 
 bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int64_t num_seqs,

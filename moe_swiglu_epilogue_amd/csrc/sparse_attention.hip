@@ -236,8 +236,12 @@ __global__ __launch_bounds__(kThreads, (kResident<D, RT, kPaged16>)) void sparse
     for (int run = 1; token < token_end; token += run) {
         run = 1;
         const int b = sparse::request_of(a.offsets, a.num_seqs, token);
-        if (b < 0)
+        if (b < 0) {
+            // the join leaves a token of no request alone
+            if (a.splits > 1 && split == 0 && tid < 16 * RT && row0 + tid < group)
+                used_splits(a, D)[(int64_t)token * a.heads + h * group + row0 + tid] = 0;
             continue;
+        }
         const int behind = a.offsets[b + 1];
         run = min(token_end, behind) - token;
         const int len = a.num_pages > 0 ? min(max(a.lens[b], 0), a.max_pages * a.page) : 0;
@@ -446,9 +450,9 @@ void launch(const Sparse& s, int block, hipStream_t stream)
         }
     }
     if (a.splits > 16)
-        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_join_kernel<D, 4, true>), dim3((unsigned)(a.tokens * a.heads)), dim3(256), 0, stream, a);
     else if (a.splits > 1)
-        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)(a.tokens * a.heads + 3) / 4), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((attn_join_kernel<D, 1, true>), dim3((unsigned)(a.tokens * a.heads + 3) / 4), dim3(256), 0, stream, a);
 }
 
 bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t page_size, int64_t list_len)
