@@ -460,10 +460,12 @@ bool sizes_ok(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t page_size
     return tokens >= 0 && heads >= 1 && kv_heads >= 1 && heads % kv_heads == 0 && page_size >= 1 && list_len >= 0;
 }
 
-bool sizes_supported(int64_t tokens, int32_t heads, int32_t head_dim, int32_t page_size, int64_t list_len)
+bool sizes_supported(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t page_size, int64_t num_seqs,
+                     int64_t list_len)
 {
     return (head_dim == 64 || head_dim == 128 || head_dim == 256) && heads <= 1024 && tokens <= (1 << 23) / heads &&
-           list_len <= kMostListed && list_len <= (1 << 30) / page_size;
+           num_seqs <= 65535 && num_seqs * kv_heads <= (1 << 22) && list_len <= kMostListed &&
+           list_len <= (1 << 30) / page_size;
 }
 
 }  // namespace
@@ -473,7 +475,7 @@ extern "C" int64_t nvfp4_sparse_attention_workspace(int64_t tokens, int32_t head
                                                     int64_t list_len)
 {
     if (num_seqs < 0 || !sizes_ok(tokens, heads, kv_heads, page_size, list_len) ||
-        !sizes_supported(tokens, heads, head_dim, page_size, list_len))
+        !sizes_supported(tokens, heads, kv_heads, head_dim, page_size, num_seqs, list_len))
         return -1;
     const SparsePlan p = sparse_plan(tokens, heads, kv_heads, head_dim, page_size, num_seqs, list_len);
     return p.splits > 1 ? tokens * heads * 4 * ((head_dim + 2) * p.splits + 1) : 0;
@@ -492,8 +494,8 @@ extern "C" nvfp4_status_t nvfp4_sparse_attention(
         max_pages < 0 || ld_table < max_pages || num_seqs < 0 || !extent_ok(num_seqs, ld_table, 4) || ld_q < 0 ||
         ld_out < 0 || workspace_bytes < 0 || !(scale - scale == 0.0f))
         return NVFP4_ERROR_INVALID_VALUE;
-    if (!sizes_supported(tokens, heads, head_dim, page_size, list_len) || num_slots > INT32_MAX || num_seqs > 65535 ||
-        num_seqs * kv_heads > (1 << 22) || max_pages > (1 << 30) / page_size)
+    if (!sizes_supported(tokens, heads, kv_heads, head_dim, page_size, num_seqs, list_len) || num_slots > INT32_MAX ||
+        max_pages > (1 << 30) / page_size)
         return NVFP4_ERROR_UNSUPPORTED_SHAPE;
     const int64_t cols = (int64_t)heads * head_dim;
     if (ld_q < cols || ld_out < cols || !extent_ok(tokens, ld_q, 2) || !extent_ok(tokens, ld_out, 2))
