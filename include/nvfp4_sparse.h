@@ -23,7 +23,9 @@
  * its L = seq_lens[b] tokens (below 0: 0; past max_pages * page_size: that),
  * its i-th at position L - n + i; token t of the request stands in page
  * block_table[b][t / page_size] of the cache. A page is hidden where its table
- * entry is outside [0, num_slots / page_size).
+ * entry is outside [0, num_slots / page_size). query_offsets do not fall; with some
+ * that do, every call ends and keeps to its buffers, lists hold pages of the table,
+ * and nothing more is specified.
  */
 #ifndef NVFP4_SPARSE_H
 #define NVFP4_SPARSE_H
@@ -124,6 +126,10 @@ nvfp4_status_t nvfp4_page_keys(const uint8_t *k_packed, const uint8_t *k_scales,
  * multiple of 8; q and keys 16-byte aligned. workspace:
  * nvfp4_select_pages_workspace(...) bytes (may be 0, then workspace may be NULL),
  * 16-byte aligned. One kernel, or two for few tokens.
+ * max_pages is taken for the longest request's pages: it chooses the workspace and
+ * the cut of the work, not the result. Of a table with more columns only those that
+ * the longest request needs should be named (ld_table may be larger): 2048 tokens
+ * of up to 500 pages take four times as long with 2049 columns as with 501.
  */
 nvfp4_status_t nvfp4_select_pages(const uint16_t *q, int64_t tokens, int64_t ld_q, int32_t heads,
                                   int32_t kv_heads, int32_t head_dim, const int8_t *keys,

@@ -769,7 +769,9 @@ SelectPlan select_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int64_t 
     SelectPlan p = {1, 0, ((int)max_pages + 3) & ~3, 0};
     // Tokens of long chunks go to a workgroup together, as many as 64 query rows and
     // 16 KB of scores hold, at most 16: four workgroups a compute unit (2048 tokens of
-    // 500 pages: 54 us, with 64 KB 71).
+    // 500 pages: 54 us, with 64 KB 71). The table's width stands for the requests' lengths
+    // and the batch's average for theirs: a wider table (115 us with 2048 columns, 218 with
+    // 2049) and single tokens beside a chunk leave fewer together than would fit.
     const int group = heads / kv_heads;
     while (p.together < 16 && p.together < tokens / (num_seqs < 1 ? 1 : num_seqs) &&
            (p.together + 1) * group <= kMostRows && (int64_t)(p.together + 1) * p.pitch * 4 <= 16384)

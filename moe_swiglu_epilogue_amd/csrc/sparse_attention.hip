@@ -394,6 +394,8 @@ SparsePlan sparse_plan(int64_t tokens, int32_t heads, int32_t kv_heads, int32_t 
     SparsePlan p;
     const int group = heads / kv_heads;
     const int64_t pitch = ceil_div(list_len, (int64_t)4) * 4;
+    // by the batch's average: 512 tokens of one request beside 255 single ones take 370 us,
+    // the two apart 318
     const int64_t average = tokens / (num_seqs < 1 ? 1 : num_seqs);
     p.together = 1;
     while (p.together < average && (p.together + 1) * group <= 16 && (p.together + 1) * pitch <= 1024 &&

@@ -261,7 +261,8 @@ def nvfp4_select_pages(q: torch.Tensor, keys: torch.Tensor, exponents: torch.Ten
     (ties to the lower page). Returns int32 [tokens, kv_heads, first + top_k +
     local], page numbers within the request in ascending order, -1 behind them.
     Rows of no request are left as they were (``pages`` allocated here holds
-    nothing there)."""
+    nothing there). The work is cut by the table's width: of a table wider than the
+    longest request pass the columns that it needs, ``block_table[:, :n]``."""
     device = _cuda(q, "q")
     index = device.index
     ld_q = _rows(q, "q", device, index)

@@ -1,6 +1,8 @@
 """The sparse-attention operators on the GPU (include/nvfp4_sparse.h) against
 their plain definitions (tests/sparse_ref.py): rotated queries, cache bytes, page
 keys and page lists bit for bit, attention within bounds that count its roundings;
+(a page key half way between two numbers may be either here, and is held to one in
+test_gpu_sparse_routes.py)
 empty rows and requests, hidden pages, odd sizes, pitches, other streams, captured
 graphs, and the operators run one after the other."""
 import ctypes as C

@@ -213,3 +213,30 @@ def test_page_keys_half_way(M, page):
     ties = (e > 0)[..., None] & (sums.abs() % (2 ** e[..., None].long()) == 2 ** (e[..., None].long() - 1).clamp(min=0))
     say("sums half way", int(ties.sum()), "exponents", sorted(set(e[ties.any(-1)].flatten().tolist())))
     assert int(ties.sum()) > 100
+
+
+# ---- tables with columns that no request needs ---------------------------------------
+@pytest.mark.parametrize("news", [[1, 1, 2], [70, 30, 41], [1000, 500, 333]])
+def test_tables_wider_than_the_requests(M, news):
+    """A wide table, and the columns of it that the longest request needs (rows with a
+    pitch), give the same keys, lists and rows as a table without others."""
+    kv, dim, page = 2, 64, 4
+    c = request_case(31, kv, dim, page, [1203, 900, 350], news, heads=8)
+    dev, need = device(c), 301
+    assert c["table"].shape[1] == need + 1
+    wide = torch.full((3, 5000), -1, dtype=torch.int32).cuda()
+    wide[:, :need + 1] = dev["table"]
+    wide[:, need:] = 2 ** 31 - 1                 # nobody's
+    say("wide tables", news)
+    got = []
+    for table in (dev["table"][:, :need].contiguous(), wide[:, :need], wide):
+        keys, exponents = dev["keys"].clone(), dev["exponents"].clone()
+        M.nvfp4_page_keys(dev["kp"], dev["ks"], table, dev["lens"], dev["offsets"], keys, exponents, page_size=page,
+                          max_query_len=max(news))
+        pages = M.nvfp4_select_pages(dev["q"], keys, exponents, table, dev["lens"], dev["offsets"], page_size=page, top_k=20)
+        out, lse = call_sparse(M, c, dict(dev, table=table), pages)
+        got.append([host(x).clone() for x in (keys, exponents, pages, out, lse)])
+    for other in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(got[0], other))
+    c.update(keys=got[0][0], exponents=got[0][1])
+    assert torch.equal(got[0][2], P.select_pages(c["q"], c["keys"], c["exponents"], c["table"], c["lens"], c["offsets"], page, 20, 1, 2))
